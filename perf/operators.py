@@ -5,7 +5,7 @@ true, through the package's entry points:
 
   product          out[seg] = a[seg] @ b[g]^T per segment, both operands in 8 bits with a power-of-two
                    scale for each block of 128 (rows: 1 x 128, weights: 128 x 128), the contraction
-                   contiguous in both: moe_group_gemm_fp8
+                   contiguous in both: moe_group_gemm_scaled
   quantise_rows    token rows gathered, weighted and put into 8 bits: moe_quant_rows
   quantise_weights the experts' weights in 8 bits, in both layouts: moe_quant_weight
   router           top-K experts of each token and their weights: moe_router_topk
@@ -305,8 +305,8 @@ def _own(st):
         # the input gradient contracts the weights' columns: [Kd, N] rows of N, out Kd wide
         kind = m.GEMM_DGRAD if st["grad"] else m.GEMM_FWD
         kd, n = (st["columns"], st["contraction"]) if st["grad"] else (st["contraction"], st["columns"])
-        ws = empty(m.group_gemm_fp8_workspace_bytes(), dtype=torch.uint8)
-        m.moe_group_gemm_fp8(kind, st["a"], st["a_scale"], st["b"], st["b_scale"], st["cu"], out, kd, n, ws)
+        ws = empty(m.group_gemm_scaled_workspace_bytes(), dtype=torch.uint8)
+        m.moe_group_gemm_scaled(kind, st["a"], st["a_scale"], st["b"], st["b_scale"], st["cu"], out, kd, n, ws)
         return out
     if op == "quantise_rows":
         rows, width = st["rows"] if st["gather"] is not None else st["source"], st["width"]
