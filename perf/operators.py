@@ -33,19 +33,19 @@ def listed():
     return [
         # one token's copies on the experts it chose: latency, the weights of a few experts
         dict(name="product_one_token", op="product", rows=6, groups=68, contraction=2048, columns=1408,
-             skew=0.3, fmt="e4m3", out="bf16", grad=False),
+             skew=0.3, fmt="e4m3", grad=False),
         # a decode batch of 64 tokens with 8 experts each: every expert's weights are read for a few rows
         dict(name="product_decode_batch", op="product", rows=512, groups=264, contraction=7168, columns=2048,
-             skew=0.3, fmt="e4m3", out="bf16", grad=False),
-        # a small step with very uneven and empty segments, fp32 results
+             skew=0.3, fmt="e4m3", grad=False),
+        # a small step with very uneven and empty segments
         dict(name="product_ragged", op="product", rows=5003, groups=18, contraction=1408, columns=2064,
-             skew=1.5, fmt="e4m3", out="f32", grad=False),
+             skew=1.5, fmt="e4m3", grad=False),
         # the up projection of a training or prefill step at the largest layer
         dict(name="product_up_large", op="product", rows=32768, groups=264, contraction=7168, columns=2048,
-             skew=0.3, fmt="e4m3", out="bf16", grad=False),
+             skew=0.3, fmt="e4m3", grad=False),
         # the input gradient of the up projection at the middle layer, gradients in e5m2
         dict(name="product_grad", op="product", rows=24576, groups=68, contraction=1408, columns=2048,
-             skew=0.3, fmt="e5m2", out="bf16", grad=True),
+             skew=0.3, fmt="e5m2", grad=True),
         # one token's hidden rows between the projections
         dict(name="quantise_few_rows", op="quantise_rows", rows=6, source=6, width=1408, div=1, dtype="bf16",
              fmt="e4m3", weighted=False, copy=False),
@@ -77,8 +77,7 @@ def draw(rng):
         while True:
             c = dict(op=op, rows=_log(rng, 1, 32768), groups=_log(rng, 1, 264), contraction=_log(rng, 128, 7168, 16),
                      columns=_log(rng, 128, 7168, 16), skew=rng.choice([0.0, 0.3, 0.8, 1.5]),
-                     fmt=rng.choice(["e4m3", "e4m3", "e5m2"]), out=rng.choice(["bf16", "bf16", "f32"]),
-                     grad=rng.random() < 0.4)
+                     fmt=rng.choice(["e4m3", "e4m3", "e5m2"]), grad=rng.random() < 0.4)
             mat = c["contraction"] * c["columns"]
             if c["rows"] * mat <= 32768 * 7168 * 2048 and c["groups"] * mat <= 264 * 7168 * 2048:
                 return c
@@ -192,7 +191,7 @@ def _plain_product(st):
         s = _spread(_values(st["b_scale"][g]), k).repeat_interleave(128, dim=0)[:n]
         return st["b"][g].float() * s
 
-    return torch.cat([a[lo:hi] @ weight(g).t() for g, lo, hi in st["segments"]]).to(DTYPE[st["out"]])
+    return torch.cat([a[lo:hi] @ weight(g).t() for g, lo, hi in st["segments"]]).bfloat16()
 
 
 def _block_exponent(top, fmt):
@@ -301,7 +300,7 @@ def _own(st):
 
     op = st["op"]
     if op == "product":
-        out = empty(st["rows"], st["columns"], dtype=DTYPE[st["out"]])
+        out = empty(st["rows"], st["columns"], dtype=torch.bfloat16)
         # the input gradient contracts the weights' columns: [Kd, N] rows of N, out Kd wide
         kind = m.GEMM_DGRAD if st["grad"] else m.GEMM_FWD
         kd, n = (st["columns"], st["contraction"]) if st["grad"] else (st["contraction"], st["columns"])
@@ -357,7 +356,7 @@ def work(case):
         m, g, k, n = case["rows"], case["groups"], case["contraction"], case["columns"]
         p = (1.0 + np.arange(g)) ** -case["skew"]
         used = float((1.0 - (1.0 - p / p.sum()) ** m).sum())  # experts with a row
-        return {"bytes": m * (k + k / 128) + used * (n * k + n * k / 16384) + m * n * size[case["out"]],
+        return {"bytes": m * (k + k / 128) + used * (n * k + n * k / 16384) + m * n * 2,
                 "flops": 2.0 * m * k * n}
     if op == "quantise_rows":
         rows, width, s = case["rows"], case["width"], size[case["dtype"]]
