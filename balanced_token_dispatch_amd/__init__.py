@@ -21,13 +21,18 @@ MOE_OK, MOE_EINVAL, MOE_ENOSPACE, MOE_EHIP = 0, 1, 2, 3
 DEV_BAD_EXPERT_ID, DEV_SLOT_OVERFLOW = 1, 2
 F32, BF16 = 0, 1
 GEMM_FWD, GEMM_DGRAD, GEMM_WGRAD = 0, 1, 2
+E4M3, E5M2 = 0, 1
+SCORES = {"softmax_topk": 0, "softmax": 1, "sigmoid": 2}   # moe_score
 
 EXPORTS = ("moe_status_string", "moe_plan_words", "moe_plan_workspace_bytes", "moe_plan",
            "moe_dispatch_layout_workspace_bytes", "moe_dispatch_layout", "moe_prefetch",
            "moe_permute", "moe_group_gemm", "moe_combine", "moe_replica_grad_fold",
            "moe_unpermute_reduce", "moe_combine_weight_grad", "moe_group_gemm_swiglu",
            "moe_swiglu_backward", "moe_group_gemm_workspace_bytes", "moe_plan_noalloc",
-           "moe_group_gemm_gather")
+           "moe_group_gemm_gather", "moe_scale_row_bytes", "moe_quant_rows", "moe_quant_weight",
+           "moe_group_gemm_scaled_workspace_bytes", "moe_group_gemm_scaled", "moe_router_topk",
+           "moe_router_backward", "moe_grad_sumsq_workspace_bytes", "moe_grad_sumsq",
+           "moe_grad_clip")
 
 PLAN_NOALLOC_SCRATCH_BYTES = 4 << 20   # MOE_PLAN_NOALLOC_SCRATCH_BYTES in moe.h
 
@@ -64,6 +69,22 @@ _lib.moe_combine_weight_grad.argtypes = [_D, ctypes.c_int, _I64, _I32, _P, _P, _
 _lib.moe_group_gemm_swiglu.argtypes = [ctypes.c_int, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P,
                                        _P, _SZ, _P]
 _lib.moe_swiglu_backward.argtypes = [ctypes.c_int, _I64, _I64, _P, _P, _P, _P]
+_lib.moe_scale_row_bytes.restype = _SZ
+_lib.moe_scale_row_bytes.argtypes = [_I64]
+for _n in ("moe_group_gemm_scaled_workspace_bytes", "moe_grad_sumsq_workspace_bytes"):
+    getattr(_lib, _n).restype = _SZ
+    getattr(_lib, _n).argtypes = []
+_lib.moe_quant_rows.argtypes = [ctypes.c_int, ctypes.c_int, _I64, _I64, _P, _I64, _P, _I32, _P, _P,
+                                _P, _P, _P]
+_lib.moe_quant_weight.argtypes = [ctypes.c_int, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P]
+_lib.moe_group_gemm_scaled.argtypes = [ctypes.c_int, ctypes.c_int, _I32, _I32, _I32, _I32,
+                                       _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+_lib.moe_router_topk.argtypes = [ctypes.c_int, ctypes.c_int, _I64, _I32, _I32, _P, _P,
+                                 ctypes.c_float, _P, _P, _P]
+_lib.moe_router_backward.argtypes = [ctypes.c_int, ctypes.c_int, _I64, _I32, _I32, _P, _P, _P,
+                                     ctypes.c_float, _P, _P]
+_lib.moe_grad_sumsq.argtypes = [_I32, _P, _P, _P, _P, _P, _SZ, _P]
+_lib.moe_grad_clip.argtypes = [_I32, _P, _P, _P, _P, ctypes.c_double, _P, _P, _P]
 for _n in EXPORTS[3:]:
     if _n.endswith("_bytes"):
         continue
@@ -174,7 +195,10 @@ def moe_group_gemm_gather(op, x_src, gather, gather_div, b, cu_seqlens, out, Kd,
     _check(_lib.moe_group_gemm_gather(op, _dtype(x_src), G, gather.numel(), Kd, N, _ptr(x_src),
                                       x_src.shape[0], _ptr(gather), gather_div, _ptr(b),
                                       _ptr(cu_seqlens), _ptr(out), wp, wn, _stream(stream)),
-           "moe_group_gemm_gather")
+           "moe_group_gemm_gather", "moe_scale_row_bytes", "moe_quant_rows", "moe_quant_weight",
+           "moe_group_gemm_scaled_workspace_bytes", "moe_group_gemm_scaled", "moe_router_topk",
+           "moe_router_backward", "moe_grad_sumsq_workspace_bytes", "moe_grad_sumsq",
+           "moe_grad_clip")
 
 
 def moe_group_gemm_swiglu(a, b, cu_seqlens, z, h, Kd, N, ws=None, stream=None):
@@ -213,3 +237,157 @@ def moe_combine_weight_grad(d, rank, y_all, dest_pos, dout, dw, stream=None):
 def moe_replica_grad_fold(d, rank, plan, dw, stream=None):
     _check(_lib.moe_replica_grad_fold(ctypes.byref(d), rank, _ptr(plan), _ptr(dw),
                                       dw[0].numel(), _stream(stream)), "moe_replica_grad_fold")
+
+
+# ---- 8-bit operands, router, gradient clipping ------------------------------------------------
+# These calls check their tensors: on the current device, contiguous, of the right type and size.
+
+_FP8 = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
+_SCALE = (torch.uint8, torch.float8_e8m0fnu)
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _take(name, t, dtypes, numel):
+    """The address of tensor t, refused unless it is on the current device, contiguous, of one of
+    the dtypes and (numel not None) of that many elements."""
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise MoeError(f"{name}: tensor on {t.device}, not on the current GPU")
+    if t.dtype not in dtypes:
+        raise MoeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if not t.is_contiguous():
+        raise MoeError(f"{name}: not contiguous")
+    if numel is not None and t.numel() != numel:
+        raise MoeError(f"{name}: shape {tuple(t.shape)}, expected {numel} elements")
+    return t.data_ptr()
+
+
+def scale_row_bytes(columns):
+    """Bytes of one row of scales over `columns` columns."""
+    return (columns + 2047) // 2048 * 16
+
+
+def moe_quant_rows(x, q, scale, gather=None, gather_div=1, row_scale=None, copy=None, stream=None):
+    """Rows of x (bf16 or fp32) into q (float8_e4m3fn or float8_e5m2) with a scale for each block of
+    128 columns; optionally gathered (x[gather[i] // gather_div]), weighted, and kept in `copy`."""
+    if x.dim() != 2:
+        raise MoeError(f"moe_quant_rows: x has {x.dim()} dimensions, expected 2")
+    src_rows, width = x.shape
+    rows = src_rows if gather is None else gather.numel()
+    xp = _take("x", x, _FLOATS, None)
+    qp = _take("q", q, _FP8, rows * width)
+    sp = _take("scale", scale, _SCALE, rows * scale_row_bytes(width))
+    gp = None if gather is None else _take("gather", gather, (torch.int32,), None)
+    wp = None
+    if row_scale is not None:
+        wp = _take("row_scale", row_scale, (torch.float32,), None)
+        if row_scale.numel() < (rows if gather is None else src_rows * gather_div):
+            raise MoeError("row_scale: fewer entries than rows (or gather entries) to weight")
+    cp = None if copy is None else _take("copy", copy, (x.dtype,), rows * width)
+    _check(_lib.moe_quant_rows(_FLOATS[x.dtype], _FP8[q.dtype], rows, width, xp, src_rows, gp,
+                               gather_div, wp, qp, sp, cp, _stream(stream)), "moe_quant_rows")
+
+
+def moe_quant_weight(w, q=None, q_scale=None, qt=None, qt_scale=None, stream=None):
+    """Expert weights w [G, Kd, N] into e4m3 with 128 x 128 block scales: q in w's order (DGRAD's
+    operand) and qt [G, N, Kd] (FWD's); either pair may be left out."""
+    if w.dim() != 3:
+        raise MoeError(f"moe_quant_weight: w has {w.dim()} dimensions, expected 3")
+    G, Kd, N = w.shape
+    e4 = (torch.float8_e4m3fn,)
+    p = [None if t is None else _take(n, t, d, c) for n, t, d, c in (
+        ("q", q, e4, G * Kd * N), ("q_scale", q_scale, _SCALE, G * -(-Kd // 128) * scale_row_bytes(N)),
+        ("qt", qt, e4, G * Kd * N), ("qt_scale", qt_scale, _SCALE, G * -(-N // 128) * scale_row_bytes(Kd)))]
+    _check(_lib.moe_quant_weight(_dtype(w), G, Kd, N, _take("w", w, _FLOATS, None), *p,
+                                 _stream(stream)), "moe_quant_weight")
+
+
+def group_gemm_scaled_workspace_bytes():
+    return _lib.moe_group_gemm_scaled_workspace_bytes()
+
+
+def moe_group_gemm_scaled(op, a, a_scale, b, b_scale, cu_seqlens, out, Kd, N, ws=None, stream=None):
+    """moe_group_gemm (FWD or DGRAD) on 8-bit operands: a from moe_quant_rows, b = qt (FWD) or q
+    (DGRAD) of moe_quant_weight; out bf16."""
+    G, M = cu_seqlens.numel() - 1, a.shape[0]
+    K, C = (Kd, N) if op == GEMM_FWD else (N, Kd)
+    ap = _take("a", a, _FP8, M * K)
+    asp = _take("a_scale", a_scale, _SCALE, M * scale_row_bytes(K))
+    bp = _take("b", b, (torch.float8_e4m3fn,), G * K * C)
+    bsp = _take("b_scale", b_scale, _SCALE, G * -(-C // 128) * scale_row_bytes(K))
+    cp = _take("cu_seqlens", cu_seqlens, (torch.int32,), None)
+    op_ = _take("out", out, (torch.bfloat16,), M * C)
+    wp, wn = (None, 0) if ws is None or ws.numel() == 0 else (_take("ws", ws, (ws.dtype,), None),
+                                                              ws.numel() * ws.element_size())
+    _check(_lib.moe_group_gemm_scaled(op, _FP8[a.dtype], G, M, Kd, N, ap, asp, bp, bsp, cp,
+                                      op_, wp, wn, _stream(stream)),
+           "moe_group_gemm_scaled")
+
+
+def _score(score):
+    if score not in SCORES:
+        raise MoeError(f"score {score!r}, expected one of {', '.join(SCORES)}")
+    return SCORES[score]
+
+
+def moe_router_topk(logits, topk_idx, topk_w, score="softmax_topk", bias=None, factor=1.0,
+                    stream=None):
+    """The K = topk_idx.shape[-1] experts of each token and their weights, from logits [T, E]."""
+    if logits.dim() != 2:
+        raise MoeError(f"moe_router_topk: logits has {logits.dim()} dimensions, expected 2")
+    T, E = logits.shape
+    K = topk_idx.shape[-1]
+    bp = None if bias is None else _take("bias", bias, (torch.float32,), E)
+    _check(_lib.moe_router_topk(_dtype(logits), _score(score), T, E, K,
+                                _take("logits", logits, _FLOATS, None), bp, factor,
+                                _take("topk_idx", topk_idx, (torch.int32,), T * K),
+                                _take("topk_w", topk_w, (torch.float32,), T * K),
+                                _stream(stream)), "moe_router_topk")
+
+
+def moe_router_backward(logits, topk_idx, dtopk_w, dlogits, score="softmax_topk", factor=1.0,
+                        stream=None):
+    """dlogits [T, E] from the gradient of the router weights, the choice held fixed."""
+    if logits.dim() != 2:
+        raise MoeError(f"moe_router_backward: logits has {logits.dim()} dimensions, expected 2")
+    T, E = logits.shape
+    K = topk_idx.shape[-1]
+    _check(_lib.moe_router_backward(_dtype(logits), _score(score), T, E, K,
+                                    _take("logits", logits, _FLOATS, None),
+                                    _take("topk_idx", topk_idx, (torch.int32,), T * K),
+                                    _take("dtopk_w", dtopk_w, (torch.float32,), T * K), factor,
+                                    _take("dlogits", dlogits, (logits.dtype,), T * E),
+                                    _stream(stream)), "moe_router_backward")
+
+
+def grad_sumsq_workspace_bytes():
+    return _lib.moe_grad_sumsq_workspace_bytes()
+
+
+def _table(grads):
+    """Host tables of a list of gradients: count, addresses, element counts, types."""
+    n = len(grads)
+    return (n, (ctypes.c_void_p * n)(*[_take("gradient", g, _FLOATS, None) for g in grads]),
+            (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
+            (ctypes.c_int * n)(*[_FLOATS[g.dtype] for g in grads]))
+
+
+def moe_grad_sumsq(grads, sumsq, ws, stream=None):
+    """sumsq (one float64) = the sum of squares over a list of gradients (fp32 or bf16)."""
+    n, ptr, numel, dt = _table(grads)
+    _check(_lib.moe_grad_sumsq(n, ptr, numel, dt, _take("sumsq", sumsq, (torch.float64,), 1),
+                               _take("ws", ws, (ws.dtype,), None), ws.numel() * ws.element_size(),
+                               _stream(stream)), "moe_grad_sumsq")
+
+
+def moe_grad_clip(grads, sumsq, max_norm, norm=None, out=None, stream=None):
+    """Scales a list of gradients by min(1, max_norm / (sqrt(sumsq) + 1e-6)), in place or into the
+    tensors of `out`; norm (one float32, optional) receives sqrt(sumsq)."""
+    n, ptr, numel, dt = _table(grads)
+    optr = ptr
+    if out is not None:
+        if len(out) != n:
+            raise MoeError(f"out: {len(out)} tensors for {n} gradients")
+        optr = (ctypes.c_void_p * n)(*[_take("out", o, (g.dtype,), g.numel()) for o, g in zip(out, grads)])
+    np_ = None if norm is None else _take("norm", norm, (torch.float32,), 1)
+    _check(_lib.moe_grad_clip(n, ptr, numel, dt, _take("sumsq", sumsq, (torch.float64,), 1),
+                              max_norm, np_, optr, _stream(stream)), "moe_grad_clip")

@@ -19,10 +19,15 @@
  *   moe_combine           router-weighted sum of each token's K expert rows
  *   backward: moe_permute (weighted), moe_group_gemm DGRAD/WGRAD,
  *             moe_replica_grad_fold
+ *   in 8 bits: moe_quant_weight once per weight update, moe_quant_rows in the
+ *             permutes' place, moe_group_gemm_scaled for FWD and DGRAD
+ *   around it: moe_router_topk (the ids and weights above, from the gate's
+ *             logits) and moe_router_backward; moe_grad_sumsq and
+ *             moe_grad_clip before the optimizer
  *
  * Conventions shared by every entry point
  *   - Every pointer argument is DEVICE memory owned by the caller, except
- *     `dims` (host).  The library allocates nothing; its only state is a
+ *     `dims` and the tables of moe_grad_sumsq / moe_grad_clip (host).  The library allocates nothing; its only state is a
  *     per-device cache of device properties and the static per-GPU scratch of
  *     moe_plan_noalloc.  Calls only enqueue work on `stream` (0 = the null
  *     stream) and never synchronise with the host.
@@ -75,6 +80,16 @@ enum {
 };
 
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+
+/* 8-bit formats (OCP): e4m3 has largest value 448 and no infinities, e5m2
+   largest value 57344 and infinities. */
+typedef enum { MOE_E4M3 = 0, MOE_E5M2 = 1 } moe_fp8;
+
+typedef enum {
+  MOE_SCORE_SOFTMAX_TOPK = 0, /* softmax over the K chosen logits             */
+  MOE_SCORE_SOFTMAX = 1,      /* softmax over all E logits, not renormalised  */
+  MOE_SCORE_SIGMOID = 2       /* logistic of each logit, over the chosen sum  */
+} moe_score;
 
 typedef enum {
   MOE_GEMM_FWD = 0,   /* out[seg] = a[seg] @ W[rho]                          */
@@ -357,6 +372,132 @@ moe_status_t moe_combine_weight_grad(const moe_dims *dims, moe_dtype dtype, int6
  * ------------------------------------------------------------------------- */
 moe_status_t moe_replica_grad_fold(const moe_dims *dims, int32_t rank, const int32_t *plan,
                                    float *dw, int64_t row_elems, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit operands.  A block of 128 values is stored as v * 2^-e, rounded to
+ * nearest even in an 8-bit format, with the byte e + 127 beside it; e is the
+ * least exponent >= -127 that brings the block's largest finite magnitude
+ * within the format's largest value, 0 for a block of zeros.  Scales are
+ * powers of two: scaling by them rounds nothing, and the matrix instructions
+ * take them as they are.  A non-finite value does not count for its block's
+ * scale; a NaN stays NaN, an infinity becomes NaN in e4m3.
+ *   Rows of scales hold one byte for each 128 columns, and are
+ * moe_scale_row_bytes(columns) = 16 ceil(columns / 2048) bytes long; bytes
+ * past the last block are written 127.  A last block of fewer than 128 columns
+ * has a scale of its own.  The pages name no 8-bit path; block scales are the
+ * usual framework variant of the expert GEMMs.
+ * ------------------------------------------------------------------------- */
+size_t moe_scale_row_bytes(int64_t columns);
+
+/* ---------------------------------------------------------------------------
+ * moe_quant_rows -- rows into 8 bits, optionally gathered and weighted on the
+ * way: moe_permute that writes what moe_group_gemm_scaled reads.
+ * Row i is x[i], or with `gather` x[gather[i] / gather_div] (zeros where
+ * gather[i] < 0 or that row is not in x); with row_scale (indexed by the
+ * gather entry, or by the row where there is no gather) each value is first
+ * multiplied by it in fp32.
+ *   x     [src_rows, width] of dtype (bf16 or fp32); without gather
+ *         src_rows >= rows.
+ *   q     [rows, width] bytes, scale [rows, moe_scale_row_bytes(width)].
+ *   copy  nullable, [rows, width] of dtype: the same rows unquantised (rounded
+ *         once where weighted), as moe_permute writes them, for the weight
+ *         gradient.
+ *   width % 16 == 0, 16 <= width <= 2^22; x, q, scale, copy 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+moe_status_t moe_quant_rows(moe_dtype dtype, moe_fp8 fmt, int64_t rows, int64_t width,
+                            const void *x, int64_t src_rows, const int32_t *gather,
+                            int32_t gather_div, const float *row_scale, void *q, void *scale,
+                            void *copy, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_quant_weight -- expert weights into e4m3 with a scale for each 128 x 128
+ * block, in the order DGRAD contracts (q) and the order FWD contracts (qt);
+ * either pair may be NULL.  Done once per weight update; moe_prefetch moves
+ * rows of all four tensors (their row_bytes are multiples of 16).
+ *   w        [G, Kd, N] of dtype (bf16 or fp32).
+ *   q        [G, Kd, N],  q_scale  [G, ceil(Kd/128), moe_scale_row_bytes(N)].
+ *   qt       [G, N, Kd],  qt_scale [G, ceil(N/128), moe_scale_row_bytes(Kd)].
+ *   Kd % 16 == 0, N % 16 == 0, both <= 2^22; all 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+moe_status_t moe_quant_weight(moe_dtype dtype, int32_t G, int32_t Kd, int32_t N, const void *w,
+                              void *q, void *q_scale, void *qt, void *qt_scale,
+                              hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_group_gemm_scaled -- moe_group_gemm with both operands in 8 bits, on
+ * MFMA with the scales applied inside the contraction and fp32 accumulation;
+ * one rounding to bf16.  Segments as in moe_group_gemm.  The matrix unit cuts
+ * each product off at 2^-13 of the largest of its 8 neighbours along the
+ * contraction (4e-5 of the result's norm on random operands).
+ *   FWD:   a [M_total, Kd], b = qt [G, N, Kd]  -> out [M_total, N]
+ *   DGRAD: a [M_total, N],  b = q  [G, Kd, N]  -> out [M_total, Kd]
+ *   a in a_fmt with a_scale [M_total, moe_scale_row_bytes(contraction)], b in
+ *   e4m3 with the scales moe_quant_weight wrote beside it; out bf16.
+ *   Kd % 16 == 0, N % 16 == 0, both <= 2^22; all 16-byte aligned.  WGRAD is
+ *   MOE_EINVAL (its contraction runs over the rows; it takes the 16-bit rows
+ *   through moe_group_gemm).
+ *   ws: optional device scratch (NULL: none) of at least
+ *   moe_group_gemm_scaled_workspace_bytes() bytes, else MOE_ENOSPACE, used as
+ *   moe_group_gemm's.
+ * ------------------------------------------------------------------------- */
+size_t moe_group_gemm_scaled_workspace_bytes(void);
+moe_status_t moe_group_gemm_scaled(moe_gemm_op op, moe_fp8 a_fmt, int32_t G, int32_t M_total,
+                                   int32_t Kd, int32_t N, const void *a, const void *a_scale,
+                                   const void *b, const void *b_scale, const int32_t *cu_seqlens,
+                                   void *out, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_router_topk -- the K experts of each token, and their weights, from the
+ * gate's logits: what moe_plan and moe_combine take.
+ * Chosen are the K largest logits, or with `bias` ([E] fp32, nullable) the K
+ * largest of score + bias, worked out in 64 bits, where the score is the logit
+ * (SOFTMAX_TOPK), its softmax over all experts (SOFTMAX) or its logistic
+ * (SIGMOID); listed by that value descending, ties to the lower id; a NaN
+ * counts as larger than any number.  The bias moves the choice only.  Weights
+ * (fp32) are factor times the score of the chosen logits: see moe_score.  An
+ * expert whose logit is -inf weighs 0, also where every chosen one is -inf.
+ *   logits [T, E] of dtype (bf16 or fp32), 1 <= E <= 1024, 1 <= K <= E,
+ *   topk_idx [T, K] int32, topk_w [T, K] fp32; factor finite.
+ * ------------------------------------------------------------------------- */
+moe_status_t moe_router_topk(moe_dtype dtype, moe_score score, int64_t T, int32_t E, int32_t K,
+                             const void *logits, const float *bias, float factor,
+                             int32_t *topk_idx, float *topk_w, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_router_backward -- dlogits from the gradient of the router weights
+ * (moe_combine_weight_grad), the choice held fixed.  Every entry of dlogits is
+ * written (0 for experts that the weights do not depend on).  An id outside
+ * [0, E) takes no part; an id listed twice counts twice.
+ *   topk_idx [T, K], dtopk_w [T, K] fp32, logits and dlogits [T, E] of dtype
+ *   (not the same buffer); score and factor as given to moe_router_topk.
+ * ------------------------------------------------------------------------- */
+moe_status_t moe_router_backward(moe_dtype dtype, moe_score score, int64_t T, int32_t E,
+                                 int32_t K, const void *logits, const int32_t *topk_idx,
+                                 const float *dtopk_w, float factor, void *dlogits,
+                                 hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_grad_sumsq -- *sumsq = the sum of the squares of all values of n tensors,
+ * in 64 bits and a fixed order.  Ranks that hold different gradients add their
+ * sums (an all-reduce of one double) before moe_grad_clip.
+ *   grads, numel, dtype: HOST arrays of n entries: device address (aligned to
+ *   the element), number of elements (0 allowed) and type (bf16 or fp32); read
+ *   before the call returns.
+ *   ws     >= moe_grad_sumsq_workspace_bytes() bytes, 8-byte aligned.  Calls
+ *          that share one workspace must not overlap.
+ * moe_grad_clip -- outs[i] = grads[i] * min(1, max_norm / (sqrt(*sumsq) + 1e-6))
+ * (fp32 product, one rounding), and *norm = sqrt(*sumsq) (norm may be NULL).
+ * outs[i] has the type and size of grads[i] and is grads[i] itself or does not
+ * overlap any tensor; a tensor clipped in place is left alone where the factor
+ * is 1.  A NaN sum gives NaN gradients.  max_norm >= 0.
+ * ------------------------------------------------------------------------- */
+size_t moe_grad_sumsq_workspace_bytes(void);
+moe_status_t moe_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,
+                            const moe_dtype *dtype, double *sumsq, void *ws, size_t ws_bytes,
+                            hipStream_t stream);
+moe_status_t moe_grad_clip(int32_t n, const void *const *grads, const int64_t *numel,
+                           const moe_dtype *dtype, const double *sumsq, double max_norm,
+                           float *norm, void *const *outs, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,226 @@
+"""The 8-bit path on the GPU: quantisers and the scaled grouped GEMM against float64."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import scaled_ref as ref
+from scaled_common import FP8, TORCH, Operands, bf16, bound
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import balanced_token_dispatch_amd as m
+    return m
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+# ---- rows ------------------------------------------------------------------------------------
+
+def run_rows(m, x, fmt, dtype, gather=None, div=1, row_scale=None, copy=False):
+    rows = len(x) if gather is None else len(gather)
+    xt = torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(TORCH[dtype]).cuda()
+    q = torch.full((rows, x.shape[1]), 3.0, device="cuda").to(FP8[fmt])
+    s = torch.full((rows, m.scale_row_bytes(x.shape[1])), 9, dtype=torch.uint8, device="cuda")
+    c = torch.full((rows, x.shape[1]), 7.0, dtype=TORCH[dtype], device="cuda") if copy else None
+    dev = lambda a, t: None if a is None else torch.from_numpy(np.asarray(a, t)).cuda()  # noqa: E731
+    m.moe_quant_rows(xt, q, s, gather=dev(gather, np.int32), gather_div=div,
+                     row_scale=dev(row_scale, np.float32), copy=c)
+    torch.cuda.synchronize()
+    return q, s, c
+
+
+def same(q, want):
+    assert np.array_equal(np.isnan(q), np.isnan(want))
+    assert np.array_equal(np.nan_to_num(q, nan=0.0, posinf=1e30, neginf=-1e30),
+                          np.nan_to_num(want, nan=0.0, posinf=1e30, neginf=-1e30))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,width", [(1, 16), (3, 128), (5, 144), (2, 1408), (7, 2048), (2, 2064), (1, 20496)])
+def test_quant_rows(m, fmt, dtype, rows, width):
+    rng = np.random.default_rng(rows * 7 + width)
+    x = rng.standard_normal((rows, width)) * 2.0 ** rng.integers(-40, 40, (rows, width))
+    x = bf16(x) if dtype == "bf16" else x.astype(np.float32)
+    q, s, _ = run_rows(m, x, fmt, dtype)
+    wq, ws, _ = ref.quant_rows(x, fmt)
+    assert np.array_equal(s.cpu().numpy(), ws)
+    same(host(q), wq)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_quant_rows_every_bf16_value(m, fmt):
+    """Each bf16 bit pattern beside a few others: zeros, subnormals, infinities and NaN."""
+    bits = np.arange(65536, dtype=np.uint32) << 16
+    x = bits.view(np.float32).reshape(512, 128)
+    q, s, _ = run_rows(m, x, fmt, "f32")
+    wq, ws, _ = ref.quant_rows(x, fmt)
+    assert np.array_equal(s.cpu().numpy(), ws)
+    same(host(q), wq)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_quant_rows_borders(m, fmt):
+    """Block maxima at and next to the format's largest value times a power of two, ties of every
+    kind, signed zeros, blocks of zeros, subnormal blocks, fp32's largest value."""
+    top = np.float32(ref.FORMATS[fmt][2])
+    rows = []
+    for e in (-126, -60, 0, 60, 100):
+        for v in (np.nextafter(top, np.float32(0)), top, np.nextafter(top, np.float32(np.inf))):
+            r = np.linspace(-1, 1, 128, dtype=np.float32) * top * np.float32(0.99)
+            r[17] = -v
+            rows.append(np.ldexp(r, e - 20 if e == 100 else e))
+    step = np.arange(128, dtype=np.float32) / 16 * (top / 8)
+    rows += [step, np.zeros(128), -np.zeros(128), np.full(128, 1e-45), np.full(128, 3e-39),
+             np.full(128, np.finfo(np.float32).max)]
+    x = np.array(rows, np.float32)
+    q, s, _ = run_rows(m, x, fmt, "f32")
+    wq, ws, _ = ref.quant_rows(x, fmt)
+    assert np.array_equal(s.cpu().numpy(), ws)
+    same(host(q), wq)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_quant_rows_gather(m, dtype, weighted):
+    rng = np.random.default_rng(5)
+    src, width, div, rows = 37, 272, 3, 150
+    x = rng.standard_normal((src, width))
+    x = bf16(x) if dtype == "bf16" else x.astype(np.float32)
+    gather = rng.integers(-2, src * div, rows)
+    gather[:4] = [-1, src * div - 1, 0, src * div]       # none, last, first, past the source
+    gather[4] = 2**31 - 1
+    w = rng.standard_normal(src * div).astype(np.float32) if weighted else None
+    q, s, c = run_rows(m, x, "e4m3", dtype, gather, div, w, copy=True)
+    wq, ws, rowsv = ref.quant_rows(x, "e4m3", gather, div, w)
+    assert np.array_equal(s.cpu().numpy(), ws)
+    same(host(q), wq)
+    assert np.array_equal(host(c), (bf16(rowsv) if dtype == "bf16" else rowsv).astype(np.float64))
+
+
+def test_quant_rows_weighted_in_place_order(m):
+    x = bf16(np.random.default_rng(1).standard_normal((9, 160)))
+    w = np.linspace(-2, 2, 9).astype(np.float32)
+    q, s, _ = run_rows(m, x, "e5m2", "bf16", row_scale=w)
+    wq, ws, _ = ref.quant_rows(x, "e5m2", row_scale=w)
+    assert np.array_equal(s.cpu().numpy(), ws)
+    same(host(q), wq)
+
+
+# ---- weights -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,K,N", [(1, 16, 16), (2, 128, 128), (3, 144, 272), (1, 400, 2064), (1, 2064, 48)])
+def test_quant_weight(m, dtype, G, K, N):
+    rng = np.random.default_rng(G * K + N)
+    w = rng.standard_normal((G, K, N)) * 2.0 ** rng.integers(-8, 8, (G, K, 1))
+    w[0, :16, :16] = 0.0
+    w = bf16(w) if dtype == "bf16" else w.astype(np.float32)
+    w[-1, K // 2, N // 2] = np.nan
+    w[0, 0, N - 1] = np.inf
+    wt = torch.from_numpy(w).to(TORCH[dtype]).cuda()
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    q = torch.full((G, K, N), 1, **u8).view(FP8["e4m3"])
+    qt = torch.full((G, N, K), 1, **u8).view(FP8["e4m3"])
+    qs = torch.full((G, -(-K // 128), m.scale_row_bytes(N)), 5, **u8)
+    ts = torch.full((G, -(-N // 128), m.scale_row_bytes(K)), 5, **u8)
+    m.moe_quant_weight(wt, q, qs, qt, ts)
+    wq, wqs, wqt, wts = ref.quant_weight(w)
+    same(host(q), wq)
+    same(host(qt), wqt)
+    assert np.array_equal(qs.cpu().numpy(), wqs)
+    assert np.array_equal(ts.cpu().numpy(), wts)
+    # either pair alone
+    q2, t2 = torch.zeros_like(q.view(torch.uint8)).view(FP8["e4m3"]), torch.zeros_like(qt.view(torch.uint8)).view(FP8["e4m3"])
+    qs2, ts2 = torch.zeros_like(qs), torch.zeros_like(ts)
+    m.moe_quant_weight(wt, q2, qs2)
+    m.moe_quant_weight(wt, qt=t2, qt_scale=ts2)
+    assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(qs2, qs)
+    assert torch.equal(t2.view(torch.uint8), qt.view(torch.uint8)) and torch.equal(ts2, ts)
+
+
+# ---- product -------------------------------------------------------------------------------------
+
+SEGMENTS = {
+    "one_row": [1], "one_each": [1] * 9, "empty_ends": [0, 0, 5, 0, 17, 0], "sixteen": [16, 16, 0, 32],
+    "uneven": [3, 0, 130, 1, 64, 0, 65, 257], "one_expert": [0, 0, 0, 300, 0], "none": [0, 0, 0],
+}
+
+
+@pytest.mark.parametrize("name", list(SEGMENTS))
+@pytest.mark.parametrize("K,C", [(16, 16), (128, 48), (144, 272), (1408, 128), (528, 400)])
+def test_product(m, name, K, C):
+    lens = SEGMENTS[name]
+    ops = Operands(K + C, lens, len(lens), K, C, tail=3)
+    got = host(ops.run(m))
+    want, mag, top = ops.expected()
+    end = int(ops.cu[-1])
+    assert (np.abs(got - want) <= bound(K, want, mag, top))[:end].all()
+    assert (got[end:] == -7.0).all()      # rows behind the last segment stay
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("K,C,lens", [(2048, 256, [100, 0, 29, 300]), (1040, 528, [700, 1, 40]),
+                                      (2064, 2064, [5, 0, 2]), (4112, 16, [31, 33])])
+def test_product_integers(m, fmt, grad, K, C, lens):
+    """Integers times powers of two: every partial sum is exact (the products of a group of 8 span
+    2^4, the scales 2^12), so the one rounding to bf16 is all that happens, bit for bit."""
+    ops = Operands(3, lens, len(lens), K, C, fmt, ints=True, first=2)
+    got = host(ops.run(m, grad))
+    want = bf16(ops.expected()[0].astype(np.float32))
+    assert np.array_equal(got[2:], want[2:])
+    assert (got[:2] == -7.0).all()        # rows ahead of the first segment stay
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_product_scale_range(m, fmt):
+    """Scales from the smallest to large ones, one block far above the others."""
+    ops = Operands(11, [20, 7], 2, 640, 144, fmt)
+    ops.a_scale[:, :5] = [0, 60, 127, 190, 20]
+    ops.b_scale[:, :, :5] = [130, 127, 127, 100, 254]
+    got = host(ops.run(m))
+    want, mag, top = ops.expected()
+    assert (np.abs(got - want) <= bound(640, want, mag, top)).all()
+
+
+def test_product_nan_stays_in_its_row(m):
+    """A NaN in one row of a (or an infinity in e5m2) reaches that row's results only, a NaN weight
+    its column's only."""
+    for fmt, byte in (("e4m3", 0x7F), ("e5m2", 0x7C)):
+        ops = Operands(12, [20, 40], 2, 272, 144, fmt)
+        ops.a[25, 200] = byte
+        ops.b[1, 77, 3] = 0x7F
+        got = host(ops.run(m))
+        bad = ~np.isfinite(got)
+        want = np.zeros_like(bad)
+        want[25] = True
+        want[20:, 77] = True
+        assert np.array_equal(bad, want)
+
+
+def test_product_bad_cu(m):
+    """cu_seqlens outside the rows is cut to them; nothing outside out is written."""
+    ops = Operands(13, [16, 16, 16], 3, 256, 64)
+    want, mag, top = ops.expected()
+    ops.cu = np.array([-5, 16, 32, 999], np.int32)
+    got = host(ops.run(m))
+    assert (np.abs(got - want) <= bound(256, want, mag, top)).all()
+
+
+def test_product_strided_stream(m):
+    """A call on a side stream, ordered by events."""
+    ops = Operands(14, [50, 3], 2, 384, 96)
+    side = torch.cuda.Stream()
+    a, sa, b, sb, cu = ops.on_gpu()
+    o = torch.zeros((ops.M, ops.C), dtype=torch.bfloat16, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    m.moe_group_gemm_scaled(m.GEMM_FWD, a, sa, b, sb, cu, o, ops.K, ops.C, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    want, mag, top = ops.expected()
+    assert (np.abs(host(o) - want) <= bound(384, want, mag, top)).all()
