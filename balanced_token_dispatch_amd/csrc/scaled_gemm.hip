@@ -20,14 +20,15 @@
 
 namespace moe {
 
-constexpr int kScMaxDim = 1 << 22;  // largest Kd and N (offsets within a tile stay in 32 bits)
+constexpr int kScMaxDim = 1 << 21;  // largest Kd and N (offsets within a tile stay in 32 bits)
 constexpr int kScMaxG = 1088;
 
 // ---- Few rows -----------------------------------------------------------------------------
-// 16 rows of one segment x 16 output columns per workgroup of 4 waves; wave w takes the blocks
-// kb = w, w + 4, ... of the contraction, straight from memory into v_mfma_scale_f32_16x16x128,
-// and the four sums are added in wave order through LDS.
-constexpr int kFewRows = 16, kFewCols = 16, kFewWaves = 4, kFewThreads = 64 * kFewWaves;
+// 16 rows of one segment x 16 output columns per workgroup of W waves; wave w takes the blocks
+// kb = w, w + W, ... of the contraction, D of them in flight, straight from memory into
+// v_mfma_scale_f32_16x16x128 (every weight byte is used once per 16 rows, so staging it in LDS would
+// gain nothing), and the W sums are added in wave order through LDS.
+constexpr int kFewRows = 16, kFewCols = 16;
 
 // Segment table in LDS: sCu (clamped to [0, M_total]) and sStart[rho] = first tile of `tile`
 // rows of segment rho; returns the number of tiles.
@@ -80,55 +81,568 @@ __device__ inline i32x8 join(u32x4 a, u32x4 b) {
   return (i32x8){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
-template <int FMT>
-__global__ __launch_bounds__(kFewThreads) void k_scaled_few(
+constexpr int kOutside = 0x7FFFFFF0;  // an offset past every buffer: the load returns zero
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void *base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, bytes, 0x00020000);
+}
+
+template <int FMT, int W, int CT, int D>
+__global__ __launch_bounds__(64 * W) void k_scaled_few(
     const uint8_t *__restrict__ a, const uint8_t *__restrict__ a_scale,
     const uint8_t *__restrict__ b, const uint8_t *__restrict__ b_scale,
     const int32_t *__restrict__ cu, uint16_t *__restrict__ out, int G, int M_total, int K, int N) {
   __shared__ int sCu[kScMaxG + 1], sStart[kScMaxG + 1];
-  __shared__ f32x4 part[kFewWaves][64];
-  const int n_rt = sc_build_tiles<kFewThreads>(cu, G, M_total, kFewRows, sCu, sStart);
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  const int n_ct = (N + kFewCols - 1) / kFewCols, nblk = (K + kBlock - 1) / kBlock;
-  const long long pitch = scale_pitch(K), total = (long long)n_rt * n_ct;
-  const int nnb = (N + kBlock - 1) / kBlock;
+  __shared__ f32x4 part[W][CT][64];
+  const int n_rt = sc_build_tiles<64 * W>(cu, G, M_total, kFewRows, sCu, sStart);
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n_ct = (N + kFewCols * CT - 1) / (kFewCols * CT), nblk = (K + kBlock - 1) / kBlock;
+  const int pitch = (int)scale_pitch(K), nnb = (N + kBlock - 1) / kBlock;
+  const long long total = (long long)n_rt * n_ct;
+  // lane l holds bytes 16 (l / 16) .. + 16 and 64 more on of row l % 16: each load takes whole
+  // half lines of 16 rows, and the order of the contraction is the same for both operands
+  const int r = lane & 15, kq = 16 * (lane >> 4), off = r * K + kq;
   for (long long t = blockIdx.x; t < total; t += gridDim.x) {
-    const int rt = (int)(t / n_ct), ct = (int)(t % n_ct);
-    const int g = sc_find_seg(sStart, G, rt);
-    const int m0 = sCu[g] + (rt - sStart[g]) * kFewRows, n0 = ct * kFewCols;
-    const int m = m0 + (lane & 15), n = n0 + (lane & 15);
-    const bool mok = m < sCu[g + 1], nok = n < N;
-    const uint8_t *ar = a + (long long)m * K, *br = b + ((long long)g * N + n) * K;
-    const uint8_t *as = a_scale + m * pitch;
-    const uint8_t *bs = b_scale + ((long long)g * nnb + n0 / kBlock) * pitch;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int kb = wid; kb < nblk; kb += kFewWaves) {
-      const int k = kb * kBlock + 32 * (lane >> 4);
-      const u32x4 z = {0, 0, 0, 0};
-      const u32x4 a0 = mok && k < K ? *(const u32x4 *)(ar + k) : z;
-      const u32x4 a1 = mok && k + 16 < K ? *(const u32x4 *)(ar + k + 16) : z;
-      const u32x4 b0 = nok && k < K ? *(const u32x4 *)(br + k) : z;
-      const u32x4 b1 = nok && k + 16 < K ? *(const u32x4 *)(br + k + 16) : z;
-      const int sa = mok ? as[kb] : kUnitScale, sb = bs[kb];
-      // weights as the first operand: each lane ends with 4 consecutive columns of one row
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(b0, b1), join(a0, a1), acc, 0,
-                                                             FMT == MOE_E5M2 ? 1 : 0, 0, sb, 0, sa);
-    }
-    part[wid][lane] = acc;
-    __syncthreads();
-    if (wid == 0) {
-      f32x4 v = part[0][lane];
+    const int rt = (int)(t / n_ct), n0 = (int)(t % n_ct) * kFewCols * CT;
+    const int g = __builtin_amdgcn_readfirstlane(sc_find_seg(sStart, G, rt));
+    const int m0 = __builtin_amdgcn_readfirstlane(sCu[g] + (rt - sStart[g]) * kFewRows);
+    const int rows = __builtin_amdgcn_readfirstlane(min(kFewRows, sCu[g + 1] - m0));
+    const int cols = min(kFewCols * CT, N - n0);
+    // rows past the segment and weights past N lie past their buffers
+    const __amdgpu_buffer_rsrc_t ra = buffer_of(a + (long long)m0 * K, rows * K);
+    const __amdgpu_buffer_rsrc_t rb = buffer_of(b + ((long long)g * N + n0) * K, cols * K);
+    const __amdgpu_buffer_rsrc_t rsa = buffer_of(a_scale + (long long)m0 * pitch, rows * pitch);
+    const __amdgpu_buffer_rsrc_t rsb = buffer_of(b_scale + ((long long)g * nnb + n0 / kBlock) * pitch, pitch);
+    f32x4 acc[CT];
 #pragma unroll
-      for (int w = 1; w < kFewWaves; ++w) v += part[w][lane];
-      const int c = n0 + 4 * (lane >> 4);
-      if (mok && c < N) {
+    for (int c = 0; c < CT; ++c) acc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int k0 = wid; k0 < nblk; k0 += W * D) {
+      u32x4 x[D][2 + 2 * CT];
+      int sa[D], sb[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int kb = k0 + d * W, k = kb * kBlock;
+        const int o0 = k + kq < K ? off : kOutside, o1 = k + kq + 64 < K ? off + 64 : kOutside;
+        const int so = kb < nblk ? k : 0;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          x[d][2 + 2 * c] = __builtin_amdgcn_raw_buffer_load_b128(rb, o0 + c * kFewCols * K, so, 0);
+          x[d][3 + 2 * c] = __builtin_amdgcn_raw_buffer_load_b128(rb, o1 + c * kFewCols * K, so, 0);
+        }
+        x[d][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, o0, so, 0);
+        x[d][1] = __builtin_amdgcn_raw_buffer_load_b128(ra, o1, so, 0);
+        sa[d] = __builtin_amdgcn_raw_buffer_load_b8(rsa, kb < nblk ? r * pitch + kb : kOutside, 0, 0);
+        sb[d] = __builtin_amdgcn_raw_buffer_load_b8(rsb, kb < nblk ? kb : kOutside, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // all of them in flight before the first is used
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+          // weights as the first operand: each lane ends with 4 consecutive columns of one row
+          acc[c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              join(x[d][2 + 2 * c], x[d][3 + 2 * c]), join(x[d][0], x[d][1]), acc[c], 0,
+              FMT == MOE_E5M2 ? 1 : 0, 0, sb[d], 0, sa[d]);
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) part[wid][c][lane] = acc[c];
+    __syncthreads();
+    if (wid < CT) {
+      f32x4 v = part[0][wid][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v += part[w][wid][lane];
+      const int c = wid * kFewCols + 4 * (lane >> 4);
+      if (r < rows && c < cols) {
         uint2 o;
         o.x = pack_bf16x2(v[0], v[1]);
         o.y = pack_bf16x2(v[2], v[3]);
-        *(uint2 *)(out + (long long)m * N + c) = o;
+        *(uint2 *)(out + (long long)(m0 + r) * N + n0 + c) = o;
       }
     }
     __syncthreads();
+  }
+}
+
+// ---- Many rows ------------------------------------------------------------------------------
+// Output tiles of 64 TM x 64 TN on a persistent grid, 4 waves (one per SIMD) of 32 TM x 32 TN each
+// in v_mfma_scale_f32_32x32x64 blocks.  A stage is 128 of the contraction (one scale block): whole
+// 128-byte lines of each operand's rows, loaded straight into LDS (buffer_load .. lds), in a ring of
+// R stages.
+constexpr int kTileThreads = 256, kTileWaves = 4;
+// Scales come in pieces of 16 stages: 16 bytes of each of the tile's rows and then of its column
+// blocks (a load writes 64 such rows).
+constexpr int kScaleStages = 16;
+constexpr int kGroupRows = 8, kXcdCount = 8;
+
+template <int TM_, int TN_, int R_>
+struct Tile {
+  static constexpr int TM = TM_, TN = TN_, R = R_;
+  static constexpr int rows = 64 * TM, cols = 64 * TN;
+  static constexpr int a_bytes = rows * kBlock, stage = (rows + cols) * kBlock;
+  static constexpr int a_loads = 2 * TM, b_loads = 2 * TN;  // 1-KB loads per wave and stage
+  static constexpr int scale_bytes = (rows + 64) * 16;      // of one piece
+  static constexpr int ring = R * stage;
+  static constexpr bool whole = TM * TN <= 4;
+  static constexpr int stores = 2 * TM * TN;                // of one wave's part of the tile
+};
+
+typedef __attribute__((address_space(3))) void *lds_ptr;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+
+__device__ inline uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(lds_ptr)p; }
+
+// 16 bytes per lane from buffer offset off + soff to LDS at m0 + 16 * lane.  Written as asm so that
+// the compiler does not track it (its alias analysis cannot tell the ring's stages apart and would
+// drain every load at each barrier): no register result, so nothing in flight can overwrite a
+// register, and completion is ordered by the explicit waits and barriers of the stage loop alone.
+// One wait state separates the write of M0 from its use.
+__device__ inline void load_to_lds(int off, __amdgpu_buffer_rsrc_t rs, int soff, uint32_t m0) {
+  asm volatile(
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off),
+      "s"(rs), "s"(soff), "{m0}"(m0)
+      : "memory");
+}
+
+// Every wave's LDS reads are done and every wave is here.  Not __syncthreads: that also waits for the
+// stores of the tile before.
+__device__ inline void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int N>
+__device__ inline void wait_loads() {  // at most N vector-memory operations in flight
+  static_assert(N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
+// An operand's rows of K bytes go out 32 a round of loads: load u of wave w covers rows
+// 32 u + 8 w .. + 8, 8 lanes a row.  The 16-byte chunk k (0..7) of row r lies at position
+// k ^ ((r >> 1) & 7) of its LDS row, which keeps the fragment reads free of bank conflicts.  The byte
+// offsets hold for both operands and every stage: a stage moves the scalar offset by 128, which
+// the buffer's range check does not look at, so rows past the operand read as zeros.  RAGGED: so does
+// what lies past K in the last stage.
+template <int LOADS>
+struct Offsets {
+  int off[LOADS];  // of load u
+  int k;           // this lane's contraction index within a stage
+};
+
+template <int LOADS>
+__device__ inline Offsets<LOADS> offsets(int K) {
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, r = wid * 8 + (lane >> 3);
+  Offsets<LOADS> o;
+  o.k = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+#pragma unroll
+  for (int u = 0; u < LOADS; ++u) o.off[u] = (r + 32 * u) * K + o.k;
+  return o;
+}
+
+template <bool RAGGED, int LOADS>
+__device__ inline void op_load(const Offsets<LOADS> &o, __amdgpu_buffer_rsrc_t rs, int s, int K,
+                               uint32_t lds, int u) {
+  int off = o.off[u];
+  if (RAGGED) off = s * kBlock + o.k < K ? off : kOutside;
+  load_to_lds(off, rs, s * kBlock, lds + u * kTileWaves * 1024);
+}
+
+// As load_to_lds where `skip` is 0; a branch inside the asm, because a branch of the compiler's would cut the
+// stage in two blocks of code, and it moves the matrix instructions of the first behind the cut.
+__device__ inline void load_to_lds_unless(int skip, int off, __amdgpu_buffer_rsrc_t rs, int soff, uint32_t m0) {
+  asm volatile(
+      "s_cmp_lg_u32 %3, 0\n\t"
+      "s_cbranch_scc1 .Lskip%=\n\t"
+      "buffer_load_dwordx4 %0, %1, %2 offen lds\n"
+      ".Lskip%=:" ::"v"(off),
+      "s"(rs), "s"(soff), "s"(skip), "{m0}"(m0)
+      : "memory", "scc");
+}
+
+// At most N operations in flight, or MORE more where `few` is 0.
+template <int N, int MORE>
+__device__ inline void wait_loads_or(int few) {
+  static_assert(N + MORE < 64, "vmcnt range");
+  asm volatile(
+      "s_cmp_lg_u32 %0, 0\n\t"
+      "s_cbranch_scc1 .Lfew%=\n\t"
+      "s_waitcnt vmcnt(%1)\n\t"
+      "s_branch .Ldone%=\n"
+      ".Lfew%=:\n\t"
+      "s_waitcnt vmcnt(%2)\n"
+      ".Ldone%=:" ::"s"(few),
+      "n"(N + MORE), "n"(N)
+      : "memory", "scc");
+}
+
+// Fragment of 32 rows (first row `row`) for sub-step ks of a stage: 32 bytes per lane, chunks
+// 4 ks + h and 4 ks + 2 + h of half-wave h.  Both operands use the same chunks, and a scale spans
+// the stage, so which 64 of the contraction a sub-step takes does not matter.
+__device__ inline i32x8 read_fragment(const uint8_t *op, int row, int lane, int ks) {
+  const int r = row + (lane & 31), h = lane >> 5, x = (r >> 1) & 7;
+  const u32x4 lo = *(const u32x4 *)(op + r * kBlock + ((4 * ks + h) ^ x) * 16);
+  const u32x4 hi = *(const u32x4 *)(op + r * kBlock + ((4 * ks + 2 + h) ^ x) * 16);
+  return join(lo, hi);
+}
+
+template <class T>
+struct Fragments {
+  i32x8 a[T::TM], b[T::TN];
+  // item i of the fragments of sub-step ks: b's first, as every matrix instruction order needs them
+  __device__ inline void read(int i, const uint8_t *stage, int wi, int wj, int lane, int ks) {
+    if (i < T::TN)
+      b[i] = read_fragment(stage + T::a_bytes, wj + 32 * i, lane, ks);
+    else
+      a[i - T::TN] = read_fragment(stage, wi + 32 * (i - T::TN), lane, ks);
+  }
+};
+
+template <int FMT>
+__device__ inline f32x16 mma(i32x8 b, i32x8 a, f32x16 c, int sb, int sa) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, FMT == MOE_E5M2 ? 1 : 0, 0, sb, 0,
+                                                         sa);
+}
+
+// The tile as bf16, straight from the accumulators: of each 32 x 32 block a lane holds 4 consecutive
+// columns of one row in 4 groups; swapping half-waves between two groups leaves it 8 consecutive
+// ones, so a store writes 32 bytes of each of 32 rows.  Every store is issued (a lane past the tile's
+// rows or columns has an offset past the buffer), because the waits of the next tile count them.
+// cols is a multiple of 16.
+template <class T>
+__device__ inline void tile_out(const f32x16 (&acc)[T::TM][T::TN], uint16_t *out, int ld, int rows,
+                                int cols) {
+  const int wid = threadIdx.x >> 6;
+  int lane = threadIdx.x & 63;
+  // the offsets are worked out per tile, not kept across the stages
+  asm volatile("" : "+v"(lane));
+  asm volatile("" : "+s"(ld));
+  const int wi = (wid >> 1) * 32 * T::TM + (lane & 31), wj = (wid & 1) * 32 * T::TN + (lane >> 5) * 8;
+  const __amdgpu_buffer_rsrc_t rs = buffer_of(out, ((rows - 1) * ld + cols) * 2);
+  const int off = (wi * ld + wj) * 2;
+#pragma unroll
+  for (int tm = 0; tm < T::TM; ++tm)
+#pragma unroll
+    for (int tn = 0; tn < T::TN; ++tn) {
+      f32x16 v = acc[tm][tn];
+      asm volatile("" : "+a"(v));  // out of its accumulators here, not all blocks at once
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        u32x4 o;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const auto w = __builtin_amdgcn_permlane32_swap(
+              pack_bf16x2(v[8 * g + 2 * h], v[8 * g + 2 * h + 1]),
+              pack_bf16x2(v[8 * g + 4 + 2 * h], v[8 * g + 4 + 2 * h + 1]), false, false);
+          o[h] = w[0];
+          o[2 + h] = w[1];
+        }
+        const bool in = wi + tm * 32 < rows && wj + tn * 32 + g * 16 < cols;
+        __builtin_amdgcn_raw_buffer_store_b128(o, rs, in ? off : kOutside,
+                                               (tm * 32 * ld + tn * 32 + g * 16) * 2, 0);
+        __builtin_amdgcn_sched_barrier(0);  // one store's registers at a time
+      }
+    }
+}
+
+// Where a tile lies; all in scalar registers.
+struct Place {
+  const uint8_t *a, *b, *sa, *sb;  // first byte of its rows, weights and their scales
+  int m0, rows, j0, cols;          // first row, rows (0: no tile), first column, columns
+};
+
+template <class T, int FMT, bool RAGGED>
+__global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
+    const uint8_t *__restrict__ a, const uint8_t *__restrict__ a_scale,
+    const uint8_t *__restrict__ b, const uint8_t *__restrict__ b_scale,
+    const int32_t *__restrict__ cu, uint16_t *__restrict__ out, int G, int M_total, int K, int N) {
+  constexpr int TM = T::TM, TN = T::TN, R = T::R, NM = TM * TN, H = NM / 2, NF = TM + TN;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[T::ring];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[2 * T::scale_bytes];
+  __shared__ int sCu[kScMaxG + 1], sStart[kScMaxG + 1];
+  const int n_rt =
+      __builtin_amdgcn_readfirstlane(sc_build_tiles<kTileThreads>(cu, G, M_total, T::rows, sCu, sStart));
+  const int n_ct = (N + T::cols - 1) / T::cols;
+  const int nnb = (N + kBlock - 1) / kBlock, pitch = (int)scale_pitch(K);
+  const long long total = (long long)n_rt * n_ct;
+  // each XCD takes neighbouring tiles, walked in groups of 8 row tiles: shared panels in its L2
+  const int grid = gridDim.x;
+  const int lb = grid % kXcdCount ? blockIdx.x : blockIdx.x % kXcdCount * (grid / kXcdCount) + blockIdx.x / kXcdCount;
+  auto place = [&](long long t) {
+    Place p = {a, b, a_scale, b_scale, 0, 0, 0, 0};
+    if (t >= total) return p;
+    const int per = kGroupRows * n_ct, grp = (int)(t / per), r = (int)(t - (long long)grp * per);
+    const int gm = min(kGroupRows, n_rt - grp * kGroupRows);
+    const int rt = grp * kGroupRows + r % gm;
+    // read from LDS, so uniform only to us: the operands' buffers need them in scalar registers
+    const int g = __builtin_amdgcn_readfirstlane(sc_find_seg(sStart, G, rt));
+    p.m0 = __builtin_amdgcn_readfirstlane(sCu[g] + (rt - sStart[g]) * T::rows);
+    p.rows = __builtin_amdgcn_readfirstlane(min(T::rows, sCu[g + 1] - p.m0));
+    p.j0 = r / gm * T::cols;
+    p.cols = min(T::cols, N - p.j0);
+    p.a = a + (long long)p.m0 * K;
+    p.b = b + ((long long)g * N + p.j0) * K;
+    p.sa = a_scale + (long long)p.m0 * pitch;
+    p.sb = b_scale + ((long long)g * nnb + p.j0 / kBlock) * pitch;
+    return p;
+  };
+  long long t = lb;
+  if (t >= total) return;
+  Place at = place(t), next = place(t + grid);
+
+  // The workgroup's tiles are one stream of stages, nk a tile, in ring slots 0, 1, .. R - 1, 0, ..:
+  // near a tile's end the loads that run ahead are the next tile's, so its first stages arrive while
+  // the last ones are multiplied and the results stored.  (nk is at least R, so that loads never run
+  // past the next tile; stages past the contraction load zeros.)
+  //
+  // A stage s is two sub-steps of TM TN matrix instructions; behind each the wave issues a few memory
+  // operations for later:
+  //   sub-step 0: reads the fragments of sub-step 1 and the scales of stage s + 1; issues b's loads of
+  //     stage s + R - 1 (R > 2); asks for the next piece of scales;
+  //   wait until only the loads of stages s + 2 .. s + R - 1 are in flight (stage s + 1 has landed),
+  //   barrier (every wave has read all of stage s);
+  //   sub-step 1: reads the fragments of stage s + 1's sub-step 0; issues a's loads of stage s + R (and
+  //     b's, R = 2: a later issue would be waited for at once) into slot s % R.
+  // Loads and stores complete in order, so where the stores of the tile before came after the loads
+  // waited for (stage 0), they are counted in; the loads of the scales only make a wait stricter.
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  const int wi = (wid >> 1) * 32 * TM, wj = (wid & 1) * 32 * TN;
+  const uint32_t wave_lds = __builtin_amdgcn_readfirstlane(wid) * 1024;
+  const uint32_t ring_lds = lds_addr(ring) + wave_lds, scales_lds = lds_addr(scales);
+  const int kblocks = (K + kBlock - 1) / kBlock, nk = max(kblocks, R);
+  constexpr int kAhead = (R - 2) * (T::a_loads + T::b_loads);
+  constexpr bool kSplit = R > 2 && !T::whole;
+  constexpr int kLoads = T::a_loads > T::b_loads ? T::a_loads : T::b_loads;
+  const Offsets<kLoads> lo = offsets<kLoads>(K);
+
+  // Piece `piece` of a tile's scales (16 stages) into LDS buffer `buf`, where `skip` is 0: wave
+  // w < TM loads a's rows 64 w .. + 64, and wave 0 the rows of b's column blocks.
+  const int w = __builtin_amdgcn_readfirstlane(wid), scale_off = (lane + 64 * (w / TM ? 0 : w)) * pitch;
+  auto load_scales = [&](int skip, const Place &p, int piece, int buf) {
+    const uint32_t to = scales_lds + buf * T::scale_bytes;
+    load_to_lds_unless(skip | w / TM, scale_off, buffer_of(p.sa, p.rows * pitch), piece * 16, to + w * 1024);
+    load_to_lds_unless(skip | w, scale_off, buffer_of(p.sb, (p.cols + kBlock - 1) / kBlock * pitch),
+                       piece * 16, to + T::rows * 16);
+  };
+  load_scales(0, at, 0, 0);
+#pragma unroll
+  for (int s = 0; s < R; ++s) {
+    const __amdgpu_buffer_rsrc_t ra = buffer_of(at.a, s < kblocks ? at.rows * K : 0);
+    const __amdgpu_buffer_rsrc_t rb = buffer_of(at.b, s < kblocks ? at.cols * K : 0);
+#pragma unroll
+    for (int u = 0; u < T::a_loads; ++u) op_load<RAGGED>(lo, ra, s, K, ring_lds + s * T::stage, u);
+    if (kSplit && s == R - 1) break;  // b's go out in stage 0
+#pragma unroll
+    for (int u = 0; u < T::b_loads; ++u)
+      op_load<RAGGED>(lo, rb, s, K, ring_lds + s * T::stage + T::a_bytes, u);
+  }
+  wait_loads<kAhead + T::a_loads + (kSplit ? 0 : T::b_loads)>();
+  lds_barrier();
+  Fragments<T> f[2], g[2];  // of sub-steps 0 and 1
+#pragma unroll
+  for (int i = 0; i < (T::whole ? 2 : 1) * NF; ++i) f[i / NF].read(i % NF, ring, wi, wj, lane, i / NF);
+  // scale bytes of this lane's rows and of the wave's column block: stage q of the piece in buffer buf;
+  // mask 0 for a stage past the contraction, whose bytes may be anything (2^-127 times zeros)
+  auto scale_at = [&](int buf, int q, int row, int mask) {
+    return scales[buf * T::scale_bytes + row * 16 + q] & mask;
+  };
+  int sa[TM], sb, buf = 0;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) sa[i] = scale_at(0, 0, wi + 32 * i + (lane & 31), 255);
+  sb = scale_at(0, 0, T::rows + (wj >> 7), 255);
+  int cur = 0;         // ring slot of stage s
+  int settled = 1;     // 0: the stores of the tile before may be in flight
+  for (;;) {
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) acc[i / TN][i % TN] = (f32x16){};
+    if constexpr (T::whole) {
+      auto stage = [&](int s, Fragments<T> (&f)[2], Fragments<T> (&g)[2]) {
+        const int nxt = cur + 1 == R ? 0 : cur + 1;
+        const uint8_t *ns = ring + nxt * T::stage;
+        const int q = s % kScaleStages;
+        const bool turn = q == kScaleStages - 1 || s == nk - 1;
+        const int nbuf = turn ? buf ^ 1 : buf, nq = turn ? 0 : q + 1;
+        const int mask = s == nk - 1 || s + 1 < kblocks ? 255 : 0;
+        const int ls = s + R < nk ? s + R : s + R - nk;
+        const Place &lp = s + R < nk ? at : next;
+        const __amdgpu_buffer_rsrc_t ra = buffer_of(lp.a, ls < kblocks ? lp.rows * K : 0);
+        const __amdgpu_buffer_rsrc_t rb = buffer_of(lp.b, ls < kblocks ? lp.cols * K : 0);
+        const bool same = s + kScaleStages < nk;
+        wait_loads_or<kAhead, T::stores>(s | settled);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        int na[TM];
+#pragma unroll
+        for (int j = 0; j < 2 * NF; ++j) g[j / NF].read(j % NF, ns, wi, wj, lane, j / NF);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) na[j] = scale_at(nbuf, nq, wi + 32 * j + (lane & 31), mask);
+        const int nb = scale_at(nbuf, nq, T::rows + (wj >> 7), mask);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 2 * NM; ++i) {
+          const int tm = i % NM / TN, tn = i % TN;
+          acc[tm][tn] = mma<FMT>(f[i / NM].b[tn], f[i / NM].a[tm], acc[tm][tn], sb, sa[tm]);
+#pragma unroll
+          for (int u = 0; u < T::a_loads + T::b_loads; ++u)
+            if (u * 2 * NM / (T::a_loads + T::b_loads) == i) {
+              if (u < T::a_loads)
+                op_load<RAGGED>(lo, ra, ls, K, ring_lds + cur * T::stage, u);
+              else
+                op_load<RAGGED>(lo, rb, ls, K, ring_lds + cur * T::stage + T::a_bytes, u - T::a_loads);
+            }
+          if (i == NM) load_scales(q, same ? at : next, same ? s / kScaleStages + 1 : 0, buf ^ 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa[i] = na[i];
+        sb = nb;
+        buf = nbuf;
+        cur = nxt;
+      };
+      int s = 0;
+#pragma clang loop unroll(disable)
+      for (; s + 2 <= nk; s += 2) {
+        stage(s, f, g);
+        stage(s + 1, g, f);
+      }
+      if (s < nk) {
+        stage(s, f, g);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) f[h] = g[h];
+      }
+    } else {
+#pragma clang loop unroll(disable)
+    for (int s = 0; s < nk; ++s) {
+      const int nxt = cur + 1 == R ? 0 : cur + 1, prv = cur == 0 ? R - 1 : cur - 1;
+      const uint8_t *cs = ring + cur * T::stage, *ns = ring + nxt * T::stage;
+      int na[TM], nb = 0;
+      const int q = s % kScaleStages;
+      // the next piece: this tile's next 16 stages, or the next tile's first
+      const bool turn = q == kScaleStages - 1 || s == nk - 1;
+      const int nbuf = turn ? buf ^ 1 : buf, nq = turn ? 0 : q + 1;
+      const int mask = s == nk - 1 || s + 1 < kblocks ? 255 : 0;
+      // b's loads in sub-step 0: of stage s + R - 1, this tile's or, past its end, the next one's
+      const int bs = s + R - 1 < nk ? s + R - 1 : s + R - 1 - nk;
+      const Place &bp = s + R - 1 < nk ? at : next;
+      const __amdgpu_buffer_rsrc_t rb0 = buffer_of(bp.b, bs < kblocks ? bp.cols * K : 0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {  // sub-step 0
+        const int tm = i / TN, tn = i % TN;
+        acc[tm][tn] = mma<FMT>(f[0].b[tn], f[0].a[tm], acc[tm][tn], sb, sa[tm]);
+        // the fragments in the first half (or, where there are few slots, in all of them)
+        constexpr int FS = NM > NF ? NM / 2 : NM;
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+          if (j * FS / NF == i) f[1].read(j, cs, wi, wj, lane, 1);
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+          if (H + j * (NM - H) / TM == i) na[j] = scale_at(nbuf, nq, wi + 32 * j + (lane & 31), mask);
+        if (i == NM - 1) nb = scale_at(nbuf, nq, T::rows + (wj >> 7), mask);
+#pragma unroll
+        for (int u = 0; u < T::b_loads; ++u)
+          if (kSplit && u * NM / T::b_loads == i)
+            op_load<RAGGED>(lo, rb0, bs, K, ring_lds + prv * T::stage + T::a_bytes, u);
+        if (i == H) {
+          const bool same = s + kScaleStages < nk;
+          load_scales(q, same ? at : next, same ? s / kScaleStages + 1 : 0, buf ^ 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // loads of stage s + R: this tile's or, past its end, the next one's
+      const int ls = s + R < nk ? s + R : s + R - nk;
+      const Place &lp = s + R < nk ? at : next;
+      const __amdgpu_buffer_rsrc_t ra = buffer_of(lp.a, ls < kblocks ? lp.rows * K : 0);
+      const __amdgpu_buffer_rsrc_t rb = buffer_of(lp.b, ls < kblocks ? lp.cols * K : 0);
+      wait_loads_or<kAhead, T::stores>(s | settled);
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {  // sub-step 1
+        const int tm = i / TN, tn = i % TN;
+        acc[tm][tn] = mma<FMT>(f[1].b[tn], f[1].a[tm], acc[tm][tn], sb, sa[tm]);
+        constexpr int FS = NM > NF ? NM / 2 : NM;
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+          if (j * FS / NF == i) f[0].read(j, ns, wi, wj, lane, 0);
+#pragma unroll
+        for (int u = 0; u < T::a_loads + (kSplit ? 0 : T::b_loads); ++u)
+          if (u * NM / (T::a_loads + (kSplit ? 0 : T::b_loads)) == i) {
+            if (u < T::a_loads)
+              op_load<RAGGED>(lo, ra, ls, K, ring_lds + cur * T::stage, u);
+            else
+              op_load<RAGGED>(lo, rb, ls, K, ring_lds + cur * T::stage + T::a_bytes, u - T::a_loads);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) sa[i] = na[i];
+      sb = nb;
+      buf = nbuf;
+      cur = nxt;
+    }
+    }
+    tile_out<T>(acc, out + (long long)at.m0 * N + at.j0, N, at.rows, at.cols);
+    __builtin_amdgcn_sched_barrier(0);
+    settled = 0;
+    t += grid;
+    if (t >= total) break;
+    at = next;
+    next = place(t + grid);
+  }
+  wait_loads<0>();  // the loads past the last tile write this workgroup's LDS
+}
+
+template <class T, int FMT>
+static void launch_tiles(const uint8_t *a, const uint8_t *as, const uint8_t *b,
+                         const uint8_t *bs, const int32_t *cu, uint16_t *out, int G, int M_total, int K,
+                         int N, hipStream_t stream) {
+  const dim3 grid(device_cu_count()), block(kTileThreads);
+  if (K % kBlock)
+    hipLaunchKernelGGL((k_scaled_tiles<T, FMT, true>), grid, block, 0, stream, a, as, b, bs, cu, out, G,
+                       M_total, K, N);
+  else
+    hipLaunchKernelGGL((k_scaled_tiles<T, FMT, false>), grid, block, 0, stream, a, as, b, bs, cu, out, G,
+                       M_total, K, N);
+}
+
+// Which kernel: by the rows a segment has on average and by how many tiles of a size there are
+// likely to be (a full tile for each of its rows, and half a tile more for each segment), since the
+// segments themselves are only known on the device.  Measured, us a launch (rows, segments,
+// contraction x columns; few rows / 64 x 64 / 64 x 128 / 128 x 256 / 256 x 256 tiles):
+//   6, 68, 2048x1408          8.2 /  9.9 / 11.6 / 17.6 / 24
+//   16, 1, 7168x7168           17 /   22 /   27 /   44 / 68
+//   512, 264, 7168x2048       545 /  544 /  542 /  541 / 658
+//   256, 1, 4096x4096          53 / 15.3 / 17.8 / 30.1 / 45
+//   1000, 16, 1024x1024        18 / 11.5 /  9.2 / 14.3 / 17.3
+//   1024, 68, 2048x1408        53 /   43 /   40 /   43 / 55
+//   4096, 264, 7168x2048      971 /  661 /  666 /  693 / 826
+//   5003, 18, 1408x2064         - /   55 /   35 /   28 / 39
+//   24576, 68, 1408x2048        - /  232 /  159 /  114 / 118
+//   32768, 264, 7168x2048       - / 1474 / 1111 /  826 / 942
+//   2000, 1, 7168x7168          - /  252 /  155 /  100 / 92
+//   32768, 1, 7168x2048         - / 1146 /  734 /  446 / 405
+template <int FMT>
+static void launch_scaled(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
+                          const int32_t *cu, uint16_t *out, int G, int M_total, int K, int N,
+                          hipStream_t stream) {
+  const long long cus = device_cu_count(), segs = G < M_total ? G : M_total;
+  auto tiles = [&](int rows, int cols) {
+    return ((long long)M_total * 2 / rows + segs + 1) / 2 * ((N + cols - 1) / cols);
+  };
+  if (M_total <= kFewRows || M_total <= 8LL * G) {
+    const long long most = (segs + M_total / kFewRows) * ceil_div(N, kFewCols * 2);
+    hipLaunchKernelGGL((k_scaled_few<FMT, 4, 2, 2>), dim3((unsigned)(most < cus * 8 ? most : cus * 8)),
+                       dim3(256), 0, stream, a, as, b, bs, cu, out, G, M_total, K, N);
+  } else if (M_total >= 512LL * G && tiles(256, 256) * 4 >= cus * 3) {
+    launch_tiles<Tile<4, 4, 2>, FMT>(a, as, b, bs, cu, out, G, M_total, K, N, stream);
+  } else if (M_total > 64LL * G && tiles(128, 256) * 4 >= cus * 3) {
+    launch_tiles<Tile<2, 4, 3>, FMT>(a, as, b, bs, cu, out, G, M_total, K, N, stream);
+  } else if (tiles(64, 64) * 4 <= cus * 5) {  // about one tile a compute unit
+    launch_tiles<Tile<1, 1, 8>, FMT>(a, as, b, bs, cu, out, G, M_total, K, N, stream);
+  } else {
+    launch_tiles<Tile<1, 2, 6>, FMT>(a, as, b, bs, cu, out, G, M_total, K, N, stream);
   }
 }
 
@@ -155,14 +669,11 @@ extern "C" moe_status_t moe_group_gemm_scaled(moe_gemm_op op, moe_fp8 a_fmt, int
     return MOE_EINVAL;
   // both operands end contiguous along the contraction: FWD contracts Kd, DGRAD contracts N
   const int K = op == MOE_GEMM_FWD ? Kd : N, C = op == MOE_GEMM_FWD ? N : Kd;
-  const dim3 grid(device_cu_count() * 8), block(kFewThreads);
   const uint8_t *a8 = (const uint8_t *)a, *b8 = (const uint8_t *)b;
   const uint8_t *as = (const uint8_t *)a_scale, *bs = (const uint8_t *)b_scale;
   if (a_fmt == MOE_E4M3)
-    hipLaunchKernelGGL(k_scaled_few<MOE_E4M3>, grid, block, 0, stream, a8, as, b8, bs, cu_seqlens,
-                       (uint16_t *)out, G, M_total, K, C);
+    launch_scaled<MOE_E4M3>(a8, as, b8, bs, cu_seqlens, (uint16_t *)out, G, M_total, K, C, stream);
   else
-    hipLaunchKernelGGL(k_scaled_few<MOE_E5M2>, grid, block, 0, stream, a8, as, b8, bs, cu_seqlens,
-                       (uint16_t *)out, G, M_total, K, C);
+    launch_scaled<MOE_E5M2>(a8, as, b8, bs, cu_seqlens, (uint16_t *)out, G, M_total, K, C, stream);
   return launch_status();
 }

@@ -383,7 +383,7 @@ moe_status_t moe_replica_grad_fold(const moe_dims *dims, int32_t rank, const int
  * scale; a NaN stays NaN, an infinity becomes NaN in e4m3.
  *   Rows of scales hold one byte for each 128 columns, and are
  * moe_scale_row_bytes(columns) = 16 ceil(columns / 2048) bytes long; bytes
- * past the last block are written 127.  A last block of fewer than 128 columns
+ * past the last block are written 127 and never used.  A last block of fewer than 128 columns
  * has a scale of its own.  The pages name no 8-bit path; block scales are the
  * usual framework variant of the expert GEMMs.
  * ------------------------------------------------------------------------- */

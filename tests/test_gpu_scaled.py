@@ -224,3 +224,48 @@ def test_product_strided_stream(m):
     torch.cuda.current_stream().wait_stream(side)
     want, mag, top = ops.expected()
     assert (np.abs(host(o) - want) <= bound(384, want, mag, top)).all()
+
+
+# sizes that reach each kernel (see launch_scaled): segments, contraction, columns
+KERNELS = {
+    "few_rows": ([3, 0, 5, 1, 0, 2], 1296, 272), "few_rows_long": ([16], 7184, 1040),
+    "tiles_64x64": ([40, 0, 65, 0], 2176, 528), "tiles_64x128": ([200, 33, 0, 90], 640, 4112),
+    "tiles_64x128_short": ([130, 500], 16, 2064),
+    "tiles_128x256": ([300, 0, 129, 127, 511], 1424, 8192), "tiles_128x256_short": ([700, 300], 272, 8208),
+    "tiles_256x256": ([1500, 1700], 2176, 4112), "tiles_256x256_short": ([1025], 112, 16400),
+    "tiles_256x256_many": ([5000], 528, 8208),
+}
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("name", list(KERNELS))
+def test_product_kernels(m, name, fmt, grad):
+    """Every kernel, on integers times powers of two (scales within 2^6, so that sums over the whole
+    contraction stay exact in fp32): equal to the float64 product rounded once."""
+    lens, K, C = KERNELS[name]
+    gen = torch.Generator(device="cuda").manual_seed(K + C)
+    M, G, tail = sum(lens) + 5, len(lens), 3
+    ints = lambda *s: torch.randint(-1, 2, s, device="cuda", generator=gen).float()  # noqa: E731
+    a, b = ints(M + tail, K).to(FP8[fmt]), ints(G, C, K).to(FP8["e4m3"])
+
+    def scales(*rows):
+        s = torch.full(rows + (m.scale_row_bytes(K),), 255, dtype=torch.uint8, device="cuda")
+        s[..., :-(-K // 128)] = torch.randint(126, 129, rows + (-(-K // 128),), device="cuda", generator=gen).byte()
+        return s
+
+    sa, sb = scales(M + tail), scales(G, -(-C // 128))
+    cu = torch.tensor(np.concatenate([[5], 5 + np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    out = torch.full((M + tail, C), -7.0, dtype=torch.bfloat16, device="cuda")
+    op, kd, n = (m.GEMM_DGRAD, C, K) if grad else (m.GEMM_FWD, K, C)
+    m.moe_group_gemm_scaled(op, a, sa, b, sb, cu, out, kd, n)
+    want = torch.full_like(out, -7.0)
+    kb = torch.arange(K, device="cuda") // 128
+    two = lambda s: torch.exp2((s.double() - 127))[..., kb]  # noqa: E731
+    at = 5
+    for g, n_rows in enumerate(lens):
+        rows = slice(at, at + n_rows)
+        w = b[g].double() * two(sb[g]).repeat_interleave(128, 0)[:C]
+        want[rows] = (a[rows].double() * two(sa[rows])).mm(w.t().contiguous()).bfloat16()
+        at += n_rows
+    assert torch.equal(out, want)
