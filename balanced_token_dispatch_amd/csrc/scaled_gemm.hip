@@ -411,7 +411,13 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
   const uint32_t ring_lds = lds_addr(ring) + wave_lds, scales_lds = lds_addr(scales);
   const int kblocks = (K + kBlock - 1) / kBlock, nk = max(kblocks, R);
   constexpr int kAhead = (R - 2) * (T::a_loads + T::b_loads);
+  constexpr int kAll = T::a_loads + T::b_loads;
+  // R > 2: b's loads go out in sub-step 0, one stage later than a's
   constexpr bool kSplit = R > 2 && !T::whole;
+  // R = 2: the loads of stage s + 2 go out from the matrix instruction on before which another barrier
+  // frees the slot, evenly to the stage's end; kEarly of them before the wait
+  constexpr int kFree = H + 2, kSpan = T::whole ? 1 : 2 * NM - kFree;
+  constexpr int kEarly = T::whole || kSplit ? 0 : ((NM - kFree) * kAll + kSpan - 1) / kSpan;
   constexpr int kLoads = T::a_loads > T::b_loads ? T::a_loads : T::b_loads;
   const Offsets<kLoads> lo = offsets<kLoads>(K);
 
@@ -431,7 +437,7 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
     const __amdgpu_buffer_rsrc_t rb = buffer_of(at.b, s < kblocks ? at.cols * K : 0);
 #pragma unroll
     for (int u = 0; u < T::a_loads; ++u) op_load<RAGGED>(lo, ra, s, K, ring_lds + s * T::stage, u);
-    if (kSplit && s == R - 1) break;  // b's go out in stage 0
+    if (kSplit && s == R - 1) break;
 #pragma unroll
     for (int u = 0; u < T::b_loads; ++u)
       op_load<RAGGED>(lo, rb, s, K, ring_lds + s * T::stage + T::a_bytes, u);
@@ -522,60 +528,54 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
       const bool turn = q == kScaleStages - 1 || s == nk - 1;
       const int nbuf = turn ? buf ^ 1 : buf, nq = turn ? 0 : q + 1;
       const int mask = s == nk - 1 || s + 1 < kblocks ? 255 : 0;
-      // b's loads in sub-step 0: of stage s + R - 1, this tile's or, past its end, the next one's
-      const int bs = s + R - 1 < nk ? s + R - 1 : s + R - 1 - nk;
-      const Place &bp = s + R - 1 < nk ? at : next;
-      const __amdgpu_buffer_rsrc_t rb0 = buffer_of(bp.b, bs < kblocks ? bp.cols * K : 0);
+      // loads of stage s + R (b's of s + R - 1 where they are split): this tile's or, past its end,
+      // the next one's
+      const int as = s + R < nk ? s + R : s + R - nk;
+      const Place &ap = s + R < nk ? at : next;
+      const __amdgpu_buffer_rsrc_t ra = buffer_of(ap.a, as < kblocks ? ap.rows * K : 0);
+      const int bn = s + R - (kSplit ? 1 : 0), bs = bn < nk ? bn : bn - nk;
+      const Place &bp = bn < nk ? at : next;
+      const __amdgpu_buffer_rsrc_t rb = buffer_of(bp.b, bs < kblocks ? bp.cols * K : 0);
+      const uint32_t to_a = ring_lds + cur * T::stage, to_b = ring_lds + (kSplit ? prv : cur) * T::stage + T::a_bytes;
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < NM; ++i) {  // sub-step 0
-        const int tm = i / TN, tn = i % TN;
-        acc[tm][tn] = mma<FMT>(f[0].b[tn], f[0].a[tm], acc[tm][tn], sb, sa[tm]);
-        // the fragments in the first half (or, where there are few slots, in all of them)
-        constexpr int FS = NM > NF ? NM / 2 : NM;
+      // matrix instruction i of the stage's 2 NM, and what is issued behind it
+      auto slot = [&](int i) __attribute__((always_inline)) {
+        const int tm = i % NM / TN, tn = i % TN, h = i / NM;
+        acc[tm][tn] = mma<FMT>(f[h].b[tn], f[h].a[tm], acc[tm][tn], sb, sa[tm]);
 #pragma unroll
         for (int j = 0; j < NF; ++j)
-          if (j * FS / NF == i) f[1].read(j, cs, wi, wj, lane, 1);
+          if (j * H / NF == i % NM) f[1 - h].read(j, h ? ns : cs, wi, wj, lane, 1 - h);
 #pragma unroll
         for (int j = 0; j < TM; ++j)
           if (H + j * (NM - H) / TM == i) na[j] = scale_at(nbuf, nq, wi + 32 * j + (lane & 31), mask);
         if (i == NM - 1) nb = scale_at(nbuf, nq, T::rows + (wj >> 7), mask);
 #pragma unroll
+        for (int u = 0; u < T::a_loads; ++u)
+          if ((kSplit ? NM + u * NM / T::a_loads : kFree + u * kSpan / kAll) == i)
+            op_load<RAGGED>(lo, ra, as, K, to_a, u);
+#pragma unroll
         for (int u = 0; u < T::b_loads; ++u)
-          if (kSplit && u * NM / T::b_loads == i)
-            op_load<RAGGED>(lo, rb0, bs, K, ring_lds + prv * T::stage + T::a_bytes, u);
+          if ((kSplit ? u * NM / T::b_loads : kFree + (T::a_loads + u) * kSpan / kAll) == i)
+            op_load<RAGGED>(lo, rb, bs, K, to_b, u);
         if (i == H) {
           const bool same = s + kScaleStages < nk;
           load_scales(q, same ? at : next, same ? s / kScaleStages + 1 : 0, buf ^ 1);
         }
         __builtin_amdgcn_sched_barrier(0);
+      };
+#pragma unroll
+      for (int i = 0; i < kFree; ++i) slot(i);
+      if (!kSplit) {
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
       }
-      // loads of stage s + R: this tile's or, past its end, the next one's
-      const int ls = s + R < nk ? s + R : s + R - nk;
-      const Place &lp = s + R < nk ? at : next;
-      const __amdgpu_buffer_rsrc_t ra = buffer_of(lp.a, ls < kblocks ? lp.rows * K : 0);
-      const __amdgpu_buffer_rsrc_t rb = buffer_of(lp.b, ls < kblocks ? lp.cols * K : 0);
-      wait_loads_or<kAhead, T::stores>(s | settled);
+#pragma unroll
+      for (int i = kFree; i < NM; ++i) slot(i);
+      wait_loads_or<kAhead + kEarly, T::stores>(s | settled);
       lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < NM; ++i) {  // sub-step 1
-        const int tm = i / TN, tn = i % TN;
-        acc[tm][tn] = mma<FMT>(f[1].b[tn], f[1].a[tm], acc[tm][tn], sb, sa[tm]);
-        constexpr int FS = NM > NF ? NM / 2 : NM;
-#pragma unroll
-        for (int j = 0; j < NF; ++j)
-          if (j * FS / NF == i) f[0].read(j, ns, wi, wj, lane, 0);
-#pragma unroll
-        for (int u = 0; u < T::a_loads + (kSplit ? 0 : T::b_loads); ++u)
-          if (u * NM / (T::a_loads + (kSplit ? 0 : T::b_loads)) == i) {
-            if (u < T::a_loads)
-              op_load<RAGGED>(lo, ra, ls, K, ring_lds + cur * T::stage, u);
-            else
-              op_load<RAGGED>(lo, rb, ls, K, ring_lds + cur * T::stage + T::a_bytes, u - T::a_loads);
-          }
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      for (int i = NM; i < 2 * NM; ++i) slot(i);
 #pragma unroll
       for (int i = 0; i < TM; ++i) sa[i] = na[i];
       sb = nb;
