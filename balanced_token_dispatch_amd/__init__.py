@@ -7,6 +7,7 @@ hipStream_t.  Importing it fails loudly when the library is not built.
 """
 import ctypes
 import os
+from array import array
 
 import torch
 
@@ -109,8 +110,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # the current stream's handle, without building a Stream object (3 us a call)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _check(rc, name):
@@ -247,18 +249,27 @@ _SCALE = (torch.uint8, torch.float8_e8m0fnu)
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 
 
-def _take(name, t, dtypes, numel):
-    """The address of tensor t, refused unless it is on the current device, contiguous, of one of
-    the dtypes and (numel not None) of that many elements."""
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _current(name, t):
+    """The current device, refused unless tensor t is on it."""
+    d = t.get_device()
+    if d < 0 or d != torch._C._cuda_getDevice():
+        raise MoeError(f"{name}: tensor on {t.device}, not on the current GPU")
+    return d
+
+
+def _take(dev, name, t, dtypes, numel):
+    """The address of tensor t, refused unless it is on device dev, contiguous, of one of the dtypes and
+    (numel not None) of that many elements."""
+    if (t.get_device() == dev and t.dtype in dtypes and t.is_contiguous()
+            and (numel is None or t.numel() == numel)):
+        return t.data_ptr()
+    if t.get_device() != dev:
         raise MoeError(f"{name}: tensor on {t.device}, not on the current GPU")
     if t.dtype not in dtypes:
         raise MoeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if not t.is_contiguous():
         raise MoeError(f"{name}: not contiguous")
-    if numel is not None and t.numel() != numel:
-        raise MoeError(f"{name}: shape {tuple(t.shape)}, expected {numel} elements")
-    return t.data_ptr()
+    raise MoeError(f"{name}: shape {tuple(t.shape)}, expected {numel} elements")
 
 
 def scale_row_bytes(columns):
@@ -271,18 +282,19 @@ def moe_quant_rows(x, q, scale, gather=None, gather_div=1, row_scale=None, copy=
     128 columns; optionally gathered (x[gather[i] // gather_div]), weighted, and kept in `copy`."""
     if x.dim() != 2:
         raise MoeError(f"moe_quant_rows: x has {x.dim()} dimensions, expected 2")
+    dev = _current("x", x)
     src_rows, width = x.shape
     rows = src_rows if gather is None else gather.numel()
-    xp = _take("x", x, _FLOATS, None)
-    qp = _take("q", q, _FP8, rows * width)
-    sp = _take("scale", scale, _SCALE, rows * scale_row_bytes(width))
-    gp = None if gather is None else _take("gather", gather, (torch.int32,), None)
+    xp = _take(dev, "x", x, _FLOATS, None)
+    qp = _take(dev, "q", q, _FP8, rows * width)
+    sp = _take(dev, "scale", scale, _SCALE, rows * scale_row_bytes(width))
+    gp = None if gather is None else _take(dev, "gather", gather, (torch.int32,), None)
     wp = None
     if row_scale is not None:
-        wp = _take("row_scale", row_scale, (torch.float32,), None)
+        wp = _take(dev, "row_scale", row_scale, (torch.float32,), None)
         if row_scale.numel() < (rows if gather is None else src_rows * gather_div):
             raise MoeError("row_scale: fewer entries than rows (or gather entries) to weight")
-    cp = None if copy is None else _take("copy", copy, (x.dtype,), rows * width)
+    cp = None if copy is None else _take(dev, "copy", copy, (x.dtype,), rows * width)
     _check(_lib.moe_quant_rows(_FLOATS[x.dtype], _FP8[q.dtype], rows, width, xp, src_rows, gp,
                                gather_div, wp, qp, sp, cp, _stream(stream)), "moe_quant_rows")
 
@@ -292,12 +304,13 @@ def moe_quant_weight(w, q=None, q_scale=None, qt=None, qt_scale=None, stream=Non
     operand) and qt [G, N, Kd] (FWD's); either pair may be left out."""
     if w.dim() != 3:
         raise MoeError(f"moe_quant_weight: w has {w.dim()} dimensions, expected 3")
+    dev = _current("w", w)
     G, Kd, N = w.shape
     e4 = (torch.float8_e4m3fn,)
-    p = [None if t is None else _take(n, t, d, c) for n, t, d, c in (
+    p = [None if t is None else _take(dev, n, t, d, c) for n, t, d, c in (
         ("q", q, e4, G * Kd * N), ("q_scale", q_scale, _SCALE, G * -(-Kd // 128) * scale_row_bytes(N)),
         ("qt", qt, e4, G * Kd * N), ("qt_scale", qt_scale, _SCALE, G * -(-N // 128) * scale_row_bytes(Kd)))]
-    _check(_lib.moe_quant_weight(_dtype(w), G, Kd, N, _take("w", w, _FLOATS, None), *p,
+    _check(_lib.moe_quant_weight(_dtype(w), G, Kd, N, _take(dev, "w", w, _FLOATS, None), *p,
                                  _stream(stream)), "moe_quant_weight")
 
 
@@ -308,15 +321,16 @@ def group_gemm_scaled_workspace_bytes():
 def moe_group_gemm_scaled(op, a, a_scale, b, b_scale, cu_seqlens, out, Kd, N, ws=None, stream=None):
     """moe_group_gemm (FWD or DGRAD) on 8-bit operands: a from moe_quant_rows, b = qt (FWD) or q
     (DGRAD) of moe_quant_weight; out bf16."""
+    dev = _current("a", a)
     G, M = cu_seqlens.numel() - 1, a.shape[0]
     K, C = (Kd, N) if op == GEMM_FWD else (N, Kd)
-    ap = _take("a", a, _FP8, M * K)
-    asp = _take("a_scale", a_scale, _SCALE, M * scale_row_bytes(K))
-    bp = _take("b", b, (torch.float8_e4m3fn,), G * K * C)
-    bsp = _take("b_scale", b_scale, _SCALE, G * -(-C // 128) * scale_row_bytes(K))
-    cp = _take("cu_seqlens", cu_seqlens, (torch.int32,), None)
-    op_ = _take("out", out, (torch.bfloat16,), M * C)
-    wp, wn = (None, 0) if ws is None or ws.numel() == 0 else (_take("ws", ws, (ws.dtype,), None),
+    ap = _take(dev, "a", a, _FP8, M * K)
+    asp = _take(dev, "a_scale", a_scale, _SCALE, M * scale_row_bytes(K))
+    bp = _take(dev, "b", b, (torch.float8_e4m3fn,), G * K * C)
+    bsp = _take(dev, "b_scale", b_scale, _SCALE, G * -(-C // 128) * scale_row_bytes(K))
+    cp = _take(dev, "cu_seqlens", cu_seqlens, (torch.int32,), None)
+    op_ = _take(dev, "out", out, (torch.bfloat16,), M * C)
+    wp, wn = (None, 0) if ws is None or ws.numel() == 0 else (_take(dev, "ws", ws, (ws.dtype,), None),
                                                               ws.numel() * ws.element_size())
     _check(_lib.moe_group_gemm_scaled(op, _FP8[a.dtype], G, M, Kd, N, ap, asp, bp, bsp, cp,
                                       op_, wp, wn, _stream(stream)),
@@ -334,13 +348,14 @@ def moe_router_topk(logits, topk_idx, topk_w, score="softmax_topk", bias=None, f
     """The K = topk_idx.shape[-1] experts of each token and their weights, from logits [T, E]."""
     if logits.dim() != 2:
         raise MoeError(f"moe_router_topk: logits has {logits.dim()} dimensions, expected 2")
+    dev = _current("logits", logits)
     T, E = logits.shape
     K = topk_idx.shape[-1]
-    bp = None if bias is None else _take("bias", bias, (torch.float32,), E)
+    bp = None if bias is None else _take(dev, "bias", bias, (torch.float32,), E)
     _check(_lib.moe_router_topk(_dtype(logits), _score(score), T, E, K,
-                                _take("logits", logits, _FLOATS, None), bp, factor,
-                                _take("topk_idx", topk_idx, (torch.int32,), T * K),
-                                _take("topk_w", topk_w, (torch.float32,), T * K),
+                                _take(dev, "logits", logits, _FLOATS, None), bp, factor,
+                                _take(dev, "topk_idx", topk_idx, (torch.int32,), T * K),
+                                _take(dev, "topk_w", topk_w, (torch.float32,), T * K),
                                 _stream(stream)), "moe_router_topk")
 
 
@@ -349,13 +364,14 @@ def moe_router_backward(logits, topk_idx, dtopk_w, dlogits, score="softmax_topk"
     """dlogits [T, E] from the gradient of the router weights, the choice held fixed."""
     if logits.dim() != 2:
         raise MoeError(f"moe_router_backward: logits has {logits.dim()} dimensions, expected 2")
+    dev = _current("logits", logits)
     T, E = logits.shape
     K = topk_idx.shape[-1]
     _check(_lib.moe_router_backward(_dtype(logits), _score(score), T, E, K,
-                                    _take("logits", logits, _FLOATS, None),
-                                    _take("topk_idx", topk_idx, (torch.int32,), T * K),
-                                    _take("dtopk_w", dtopk_w, (torch.float32,), T * K), factor,
-                                    _take("dlogits", dlogits, (logits.dtype,), T * E),
+                                    _take(dev, "logits", logits, _FLOATS, None),
+                                    _take(dev, "topk_idx", topk_idx, (torch.int32,), T * K),
+                                    _take(dev, "dtopk_w", dtopk_w, (torch.float32,), T * K), factor,
+                                    _take(dev, "dlogits", dlogits, (logits.dtype,), T * E),
                                     _stream(stream)), "moe_router_backward")
 
 
@@ -363,31 +379,42 @@ def grad_sumsq_workspace_bytes():
     return _lib.moe_grad_sumsq_workspace_bytes()
 
 
-def _table(grads):
-    """Host tables of a list of gradients: count, addresses, element counts, types."""
-    n = len(grads)
-    return (n, (ctypes.c_void_p * n)(*[_take("gradient", g, _FLOATS, None) for g in grads]),
-            (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
-            (ctypes.c_int * n)(*[_FLOATS[g.dtype] for g in grads]))
+def _table(dev, grads):
+    """Host tables of a list of gradients: addresses, element counts and types (a call's worth of
+    checks on many tensors, so attribute by attribute)."""
+    dt = [_FLOATS.get(g.dtype, -1) for g in grads]
+    if -1 in dt or any(g.get_device() != dev for g in grads) or not all([g.is_contiguous() for g in grads]):
+        for g in grads:  # says which
+            _take(dev, "gradient", g, _FLOATS, None)
+    return (array("Q", [g.data_ptr() for g in grads]), array("q", [g.numel() for g in grads]),
+            array("i", dt))
+
+
+def _at(table):
+    return ctypes.c_void_p(table.buffer_info()[0])
 
 
 def moe_grad_sumsq(grads, sumsq, ws, stream=None):
     """sumsq (one float64) = the sum of squares over a list of gradients (fp32 or bf16)."""
-    n, ptr, numel, dt = _table(grads)
-    _check(_lib.moe_grad_sumsq(n, ptr, numel, dt, _take("sumsq", sumsq, (torch.float64,), 1),
-                               _take("ws", ws, (ws.dtype,), None), ws.numel() * ws.element_size(),
+    dev = _current("sumsq", sumsq)
+    ptr, numel, dt = _table(dev, grads)
+    _check(_lib.moe_grad_sumsq(len(grads), _at(ptr), _at(numel), _at(dt),
+                               _take(dev, "sumsq", sumsq, (torch.float64,), 1),
+                               _take(dev, "ws", ws, (ws.dtype,), None), ws.numel() * ws.element_size(),
                                _stream(stream)), "moe_grad_sumsq")
 
 
 def moe_grad_clip(grads, sumsq, max_norm, norm=None, out=None, stream=None):
     """Scales a list of gradients by min(1, max_norm / (sqrt(sumsq) + 1e-6)), in place or into the
     tensors of `out`; norm (one float32, optional) receives sqrt(sumsq)."""
-    n, ptr, numel, dt = _table(grads)
+    dev = _current("sumsq", sumsq)
+    ptr, numel, dt = _table(dev, grads)
     optr = ptr
     if out is not None:
-        if len(out) != n:
-            raise MoeError(f"out: {len(out)} tensors for {n} gradients")
-        optr = (ctypes.c_void_p * n)(*[_take("out", o, (g.dtype,), g.numel()) for o, g in zip(out, grads)])
-    np_ = None if norm is None else _take("norm", norm, (torch.float32,), 1)
-    _check(_lib.moe_grad_clip(n, ptr, numel, dt, _take("sumsq", sumsq, (torch.float64,), 1),
-                              max_norm, np_, optr, _stream(stream)), "moe_grad_clip")
+        optr, onumel, odt = _table(dev, out)
+        if onumel != numel or odt != dt:
+            raise MoeError("out: not one tensor of the type and size of each gradient")
+    np_ = None if norm is None else _take(dev, "norm", norm, (torch.float32,), 1)
+    _check(_lib.moe_grad_clip(len(grads), _at(ptr), _at(numel), _at(dt),
+                              _take(dev, "sumsq", sumsq, (torch.float64,), 1), max_norm, np_, _at(optr),
+                              _stream(stream)), "moe_grad_clip")

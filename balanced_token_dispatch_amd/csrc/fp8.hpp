@@ -42,19 +42,49 @@ __device__ inline int block_exponent(uint32_t mag) {
   return e < -127 ? -127 : e;
 }
 
-// Four values, already scaled, as 8-bit bytes (round to nearest even; a NaN stays NaN, an
-// infinity becomes NaN in e4m3, which has none).
+// 2^e as the conversions below take it (a scale byte's value: 2^-127 is the subnormal).
+__device__ inline float exponent_scale(int e) {
+  return __builtin_bit_cast(float, e == -127 ? 0x00400000u : (uint32_t)(e + 127) << 23);
+}
+
+typedef __attribute__((ext_vector_type(2))) short i16x2;
+
+// Four values divided by `scale` (a power of two) as 8-bit bytes, rounded to nearest even; a NaN stays
+// NaN, an infinity becomes NaN in e4m3, which has none.
 template <int FMT>
-__device__ inline uint32_t pack_fp8x4(float a, float b, float c, float d) {
-  int r = 0;
+__device__ inline uint32_t pack_fp8x4(float a, float b, float c, float d, float scale) {
+  i16x2 r = {0, 0};
   if constexpr (FMT == MOE_E5M2) {
-    r = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, r, false);
-    r = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
+    r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, a, b, scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, c, d, scale, true);
   } else {
-    r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
-    r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, true);
   }
-  return (uint32_t)r;
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// The same from two words of two bf16 values.
+template <int FMT>
+__device__ inline uint32_t pack_fp8x4(uint32_t ab, uint32_t cd, float scale) {
+  i16x2 r = {0, 0};
+  const bf16x2 lo = __builtin_bit_cast(bf16x2, ab), hi = __builtin_bit_cast(bf16x2, cd);
+  if constexpr (FMT == MOE_E5M2) {
+    r = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(r, lo, scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(r, hi, scale, true);
+  } else {
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, lo, scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, hi, scale, true);
+  }
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
+
+// The larger magnitude of each half of two words of bf16 values.
+__device__ inline uint32_t mag_max2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b & 0x7FFF7FFFu)));
 }
 
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }

@@ -32,6 +32,21 @@ __device__ inline int grad_tensor(const GradBatch &b, int c) {
   return lo;
 }
 
+// 16 bytes of a gradient as fp32 values: 4 of fp32, 8 of bf16.
+template <bool BF16>
+__device__ inline void widen(u32x4 t, float (&v)[8]) {
+  const f32x4 f = __builtin_bit_cast(f32x4, t);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (BF16) {
+      v[2 * q] = bf16_lo(t[q]);
+      v[2 * q + 1] = bf16_hi(t[q]);
+    } else {
+      v[q] = f[q];
+    }
+  }
+}
+
 __device__ inline float grad_at(const void *g, bool bf16, long long i) {
   return bf16 ? __builtin_bit_cast(float, (uint32_t)((const uint16_t *)g)[i] << 16) : ((const float *)g)[i];
 }
@@ -51,6 +66,36 @@ __device__ inline double block_sum(double v) {
   return s;
 }
 
+constexpr int kGradFlight = 4;  // 16-byte loads a thread has in flight
+
+// This thread's squares of one chunk whose address is a multiple of 16: whole vectors, then the rest.
+template <bool BF16>
+__device__ inline double chunk_squares(const char *g, int n, double s) {
+  constexpr int V = BF16 ? 8 : 4;
+  const u32x4 *p = (const u32x4 *)g;
+  const int vecs = n / V;
+  for (int i = threadIdx.x; i < vecs; i += kGradThreads * kGradFlight) {
+    u32x4 t[kGradFlight];
+#pragma unroll
+    for (int u = 0; u < kGradFlight; ++u) {
+      t[u] = (u32x4){0, 0, 0, 0};
+      if (i + u * kGradThreads < vecs) t[u] = p[i + u * kGradThreads];
+    }
+#pragma unroll
+    for (int u = 0; u < kGradFlight; ++u) {
+      float v[8];
+      widen<BF16>(t[u], v);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s = fma((double)v[e], (double)v[e], s);
+    }
+  }
+  for (int i = vecs * V + threadIdx.x; i < n; i += kGradThreads) {
+    const double v = grad_at(g, BF16, i);
+    s = fma(v, v, s);
+  }
+  return s;
+}
+
 // parts[blockIdx] += the squares of every gridDim-th chunk of the batch; the parts from `have`
 // on are set instead (no earlier launch of the call wrote them).
 __global__ __launch_bounds__(kGradThreads) void k_grad_sumsq(GradBatch b, double *__restrict__ parts,
@@ -61,9 +106,14 @@ __global__ __launch_bounds__(kGradThreads) void k_grad_sumsq(GradBatch b, double
     const long long i0 = (long long)(c - b.first[t]) * kGradChunk;
     const int n = (int)min((long long)kGradChunk, b.n[t] - i0);
     const bool bf = b.bf16[t];
-    for (int i = threadIdx.x; i < n; i += kGradThreads) {
-      const double v = grad_at(b.g[t], bf, i0 + i);
-      s = fma(v, v, s);
+    const char *g = (const char *)b.g[t] + i0 * (bf ? 2 : 4);
+    if ((uintptr_t)g % 16 == 0) {
+      s = bf ? chunk_squares<true>(g, n, s) : chunk_squares<false>(g, n, s);
+    } else {
+      for (int i = threadIdx.x; i < n; i += kGradThreads) {
+        const double v = grad_at(g, bf, i);
+        s = fma(v, v, s);
+      }
     }
   }
   s = block_sum<kGradThreads>(s);
@@ -85,22 +135,61 @@ __device__ inline float clip_coef(double sumsq, double max_norm) {
   return c >= 1.0 ? 1.0f : (float)c;
 }
 
+template <bool BF16>
+__device__ inline void chunk_scale(const char *g, char *o, int n, float coef) {
+  constexpr int V = BF16 ? 8 : 4;
+  const u32x4 *p = (const u32x4 *)g;
+  u32x4 *d = (u32x4 *)o;
+  const int vecs = n / V;
+  for (int i = threadIdx.x; i < vecs; i += kGradThreads * kGradFlight) {
+    u32x4 t[kGradFlight];
+#pragma unroll
+    for (int u = 0; u < kGradFlight; ++u)
+      if (i + u * kGradThreads < vecs) t[u] = __builtin_nontemporal_load(p + i + u * kGradThreads);
+#pragma unroll
+    for (int u = 0; u < kGradFlight; ++u) {
+      if (i + u * kGradThreads >= vecs) break;
+      float v[8];
+      widen<BF16>(t[u], v);
+      u32x4 r;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        r[q] = BF16 ? pack_bf16x2(coef * v[2 * q], coef * v[2 * q + 1]) : __builtin_bit_cast(uint32_t, coef * v[q]);
+      __builtin_nontemporal_store(r, d + i + u * kGradThreads);
+    }
+  }
+  for (int i = vecs * V + threadIdx.x; i < n; i += kGradThreads) {
+    const float v = coef * grad_at(g, BF16, i);
+    if (BF16)
+      ((uint16_t *)o)[i] = (uint16_t)pack_bf16x2(v, 0.0f);
+    else
+      ((float *)o)[i] = v;
+  }
+}
+
+// Chunks from the last to the first: the sum read the last ones last, so they may still be cached.
 __global__ __launch_bounds__(kGradThreads) void k_grad_clip(GradBatch b, const double *__restrict__ sumsq,
                                                            double max_norm, float *__restrict__ norm) {
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)sqrt(*sumsq);
   const float coef = clip_coef(*sumsq, max_norm);
-  for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x) {
+  for (int c = b.first[b.count] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int t = grad_tensor(b, c);
     if (coef == 1.0f && b.g[t] == b.o[t]) continue;
     const long long i0 = (long long)(c - b.first[t]) * kGradChunk;
     const int n = (int)min((long long)kGradChunk, b.n[t] - i0);
     const bool bf = b.bf16[t];
-    for (int i = threadIdx.x; i < n; i += kGradThreads) {
-      const float v = coef * grad_at(b.g[t], bf, i0 + i);
-      if (bf)
-        ((uint16_t *)b.o[t])[i0 + i] = (uint16_t)pack_bf16x2(v, 0.0f);
-      else
-        ((float *)b.o[t])[i0 + i] = v;
+    const char *g = (const char *)b.g[t] + i0 * (bf ? 2 : 4);
+    char *o = (char *)b.o[t] + i0 * (bf ? 2 : 4);
+    if (((uintptr_t)g | (uintptr_t)o) % 16 == 0) {
+      bf ? chunk_scale<true>(g, o, n, coef) : chunk_scale<false>(g, o, n, coef);
+    } else {
+      for (int i = threadIdx.x; i < n; i += kGradThreads) {
+        const float v = coef * grad_at(g, bf, i);
+        if (bf)
+          ((uint16_t *)o)[i] = (uint16_t)pack_bf16x2(v, 0.0f);
+        else
+          ((float *)o)[i] = v;
+      }
     }
   }
 }

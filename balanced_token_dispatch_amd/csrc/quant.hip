@@ -7,37 +7,102 @@
 namespace moe {
 
 constexpr int kQuantMaxThreads = 1024;
-constexpr int kQuantPer = 16;  // values per thread: one 16-byte store of 8-bit values
+constexpr int kQuantPer = 16;  // values per thread
 constexpr int kQuantLanes = kBlock / kQuantPer;  // threads per block of 128
 constexpr int kQuantMaxGridX = 1 << 20;
 
-// This thread's 16 values of a row (bf16 or fp32), widened.
+// A thread's 16 values of a row: 8 from column 8 l of the block (l = its place among the block's 8
+// threads) and 8 from column 64 + 8 l, so that each load and store of a wave covers whole runs of 64
+// values.  bf16 values stay packed as loaded; Row<false> holds fp32 (an fp32 row, or a weighted one).
+template <bool PACKED>
+struct Row;
+
+template <>
+struct Row<true> {
+  u32x4 t[2];
+  __device__ inline void zero() { t[0] = t[1] = (u32x4){0, 0, 0, 0}; }
+  // Bits of the largest finite magnitude, as fp32 bits.
+  __device__ inline uint32_t mag() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) m = mag_max2(m, t[h][q]);
+    m = max(m << 16, m & 0xFFFF0000u);
+    if (m >= 0x7F800000u) {  // an infinity or NaN among them: value by value
+      m = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m = max(m, max(finite_mag(bf16_lo(t[h][q])), finite_mag(bf16_hi(t[h][q]))));
+    }
+    return m;
+  }
+  template <int FMT>
+  __device__ inline uint2 pack(int h, float scale) const {
+    uint2 o;
+    o.x = pack_fp8x4<FMT>(t[h][0], t[h][1], scale);
+    o.y = pack_fp8x4<FMT>(t[h][2], t[h][3], scale);
+    return o;
+  }
+  __device__ inline u32x4 bf16(int h) const { return t[h]; }
+};
+
+template <>
+struct Row<false> {
+  float v[16];
+  __device__ inline void zero() {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+  }
+  __device__ inline uint32_t mag() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = max(m, finite_mag(v[e]));
+    return m;
+  }
+  template <int FMT>
+  __device__ inline uint2 pack(int h, float scale) const {
+    uint2 o;
+    o.x = pack_fp8x4<FMT>(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3], scale);
+    o.y = pack_fp8x4<FMT>(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7], scale);
+    return o;
+  }
+  __device__ inline u32x4 bf16(int h) const {
+    u32x4 t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = pack_bf16x2(v[8 * h + 2 * e], v[8 * h + 2 * e + 1]);
+    return t;
+  }
+};
+
+// 8 values from index i of the source, as part h of a row.
 template <bool BF16>
-__device__ inline void load16(const void *p, long long i, float (&v)[kQuantPer]) {
+__device__ inline void load_part(Row<true> &r, int h, const void *x, long long i, float) {
+  r.t[h] = *(const u32x4 *)((const uint16_t *)x + i);
+}
+
+template <bool BF16>
+__device__ inline void load_part(Row<false> &r, int h, const void *x, long long i, float w) {
   if constexpr (BF16) {
-    const u32x4 *s = (const u32x4 *)((const uint16_t *)p + i);
+    const u32x4 t = *(const u32x4 *)((const uint16_t *)x + i);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const u32x4 t = s[h];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[8 * h + 2 * q] = bf16_lo(t[q]);
-        v[8 * h + 2 * q + 1] = bf16_hi(t[q]);
-      }
+    for (int q = 0; q < 4; ++q) {
+      r.v[8 * h + 2 * q] = w * bf16_lo(t[q]);
+      r.v[8 * h + 2 * q + 1] = w * bf16_hi(t[q]);
     }
   } else {
-    const f32x4 *s = (const f32x4 *)((const float *)p + i);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const f32x4 t = s[h];
+    for (int p = 0; p < 2; ++p) {
+      const f32x4 t = *(const f32x4 *)((const float *)x + i + 4 * p);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[4 * h + q] = t[q];
+      for (int q = 0; q < 4; ++q) r.v[8 * h + 4 * p + q] = w * t[q];
     }
   }
 }
 
-// One row per grid x step, kQuantPer values per thread, 8 threads per block of 128.
-template <bool BF16, int FMT>
+// One row per grid x step.
+template <bool BF16, int FMT, bool WEIGHTED>
 __global__ __launch_bounds__(kQuantMaxThreads) void k_quant_rows(
     const void *__restrict__ x, long long src_rows, const int32_t *__restrict__ gather, int div,
     const float *__restrict__ row_scale, uint8_t *__restrict__ q, uint8_t *__restrict__ scale,
@@ -50,52 +115,65 @@ __global__ __launch_bounds__(kQuantMaxThreads) void k_quant_rows(
       const int c = gather[i];
       src = c < 0 ? -1 : c / div;
       if (src >= src_rows) src = -1;
-      if (row_scale && src >= 0) w = row_scale[c];
-    } else if (row_scale) {
+      if (WEIGHTED && src >= 0) w = row_scale[c];
+    } else if (WEIGHTED) {
       w = row_scale[i];
     }
-    for (int u = blockIdx.y * blockDim.x + threadIdx.x; u < pitch * kQuantLanes;
-         u += gridDim.y * blockDim.x) {
-      const int b = u / kQuantLanes, c0 = u * kQuantPer;
-      float v[kQuantPer] = {};
-      if (src >= 0 && c0 < width) {
-        load16<BF16>(x, src * width + c0, v);
-        if (row_scale) {
+    for (int u = blockIdx.y * blockDim.x + threadIdx.x; u < nblk * kQuantLanes; u += gridDim.y * blockDim.x) {
+      const int b = u / kQuantLanes, c0 = b * kBlock + u % kQuantLanes * 8;
+      Row<BF16 && !WEIGHTED> r;
+      r.zero();
 #pragma unroll
-          for (int e = 0; e < kQuantPer; ++e) v[e] *= w;
-        }
-      }
-      uint32_t mag = 0;
-#pragma unroll
-      for (int e = 0; e < kQuantPer; ++e) mag = max(mag, finite_mag(v[e]));
+      for (int h = 0; h < 2; ++h)
+        if (src >= 0 && c0 + 64 * h < width) load_part<BF16>(r, h, x, src * width + c0 + 64 * h, w);
+      uint32_t mag = r.mag();
 #pragma unroll
       for (int off = 1; off < kQuantLanes; off <<= 1) mag = max(mag, (uint32_t)__shfl_xor((int)mag, off, kWave));
       const int ex = block_exponent<FMT>(mag);
-      if (u % kQuantLanes == 0)
-        scale[i * pitch + b] = (uint8_t)(b < nblk ? ex + 127 : kUnitScale);
-      if (c0 >= width) continue;
-      u32x4 o;
+      const float es = exponent_scale(ex);
+      if (u % kQuantLanes == 0) scale[i * pitch + b] = (uint8_t)(ex + 127);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = pack_fp8x4<FMT>(ldexpf(v[4 * e], -ex), ldexpf(v[4 * e + 1], -ex),
-                               ldexpf(v[4 * e + 2], -ex), ldexpf(v[4 * e + 3], -ex));
-      *(u32x4 *)(q + i * width + c0) = o;
-      if (copy) {
+      for (int h = 0; h < 2; ++h) {
+        const long long at = i * width + c0 + 64 * h;
+        if (c0 + 64 * h >= width) continue;
+        *(uint2 *)(q + at) = r.template pack<FMT>(h, es);
+        if (!copy) continue;
         if constexpr (BF16) {
-          u32x4 *d = (u32x4 *)((uint16_t *)copy + i * width + c0);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            u32x4 t;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = pack_bf16x2(v[8 * h + 2 * e], v[8 * h + 2 * e + 1]);
-            d[h] = t;
-          }
+          *(u32x4 *)((uint16_t *)copy + at) = r.bf16(h);
         } else {
-          f32x4 *d = (f32x4 *)((float *)copy + i * width + c0);
+          f32x4 *d = (f32x4 *)((float *)copy + at);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) d[h] = (f32x4){v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+          for (int p = 0; p < 2; ++p)
+            d[p] = (f32x4){r.v[8 * h + 4 * p], r.v[8 * h + 4 * p + 1], r.v[8 * h + 4 * p + 2], r.v[8 * h + 4 * p + 3]};
         }
       }
+    }
+    if (blockIdx.y == 0)
+      for (int b = nblk + threadIdx.x; b < pitch; b += blockDim.x) scale[i * pitch + b] = kUnitScale;
+  }
+}
+
+// N consecutive values from index i of a bf16 or fp32 array, widened.
+template <bool BF16, int N>
+__device__ inline void load_values(const void *p, long long i, float (&v)[N]) {
+  if constexpr (BF16) {
+    const u32x4 *s = (const u32x4 *)((const uint16_t *)p + i);
+#pragma unroll
+    for (int h = 0; h < N / 8; ++h) {
+      const u32x4 t = s[h];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[8 * h + 2 * q] = bf16_lo(t[q]);
+        v[8 * h + 2 * q + 1] = bf16_hi(t[q]);
+      }
+    }
+  } else {
+    const f32x4 *s = (const f32x4 *)((const float *)p + i);
+#pragma unroll
+    for (int h = 0; h < N / 4; ++h) {
+      const f32x4 t = s[h];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[4 * h + q] = t[q];
     }
   }
 }
@@ -126,7 +204,7 @@ __global__ __launch_bounds__(kWtThreads) void k_quant_weight(
       const int k = k0 + r0 + 32 * p, n = n0 + c0;
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[p][e] = 0.0f;
-      if (k < Kd && n < N) load16<BF16>(w, (g * Kd + k) * N + n, v[p]);
+      if (k < Kd && n < N) load_values<BF16>(w, (g * Kd + k) * N + n, v[p]);
 #pragma unroll
       for (int e = 0; e < 16; ++e) mag = max(mag, finite_mag(v[p][e]));
     }
@@ -137,6 +215,7 @@ __global__ __launch_bounds__(kWtThreads) void k_quant_weight(
 #pragma unroll
     for (int i = 0; i < kWtThreads / kWave; ++i) mag = max(mag, wave_mag[i]);
     const int ex = block_exponent<MOE_E4M3>(mag);
+    const float es = exponent_scale(ex);
     // each block writes its own byte; the last one of a row of scales pads the row
     if (q_scale) {
       uint8_t *s = q_scale + (g * kb_n + kb) * pq;
@@ -150,8 +229,7 @@ __global__ __launch_bounds__(kWtThreads) void k_quant_weight(
       u32x4 o;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        o[e] = pack_fp8x4<MOE_E4M3>(ldexpf(v[p][4 * e], -ex), ldexpf(v[p][4 * e + 1], -ex),
-                                    ldexpf(v[p][4 * e + 2], -ex), ldexpf(v[p][4 * e + 3], -ex));
+        o[e] = pack_fp8x4<MOE_E4M3>(v[p][4 * e], v[p][4 * e + 1], v[p][4 * e + 2], v[p][4 * e + 3], es);
       if (q && k < Kd && n0 + c0 < N) *(u32x4 *)(q + (g * Kd + k) * N + n0 + c0) = o;
 #pragma unroll
       for (int e = 0; e < 16; ++e) tile[(c0 + e) * kWtLd + r] = (uint8_t)(o[e >> 2] >> (8 * (e & 3)));
@@ -178,19 +256,19 @@ __global__ __launch_bounds__(kWtThreads) void k_quant_weight(
   }
 }
 
-template <bool BF16>
-static void launch_quant_rows(moe_fp8 fmt, dim3 grid, int threads, hipStream_t stream,
-                              const void *x, int64_t src_rows, const int32_t *gather, int div,
-                              const float *row_scale, void *q, void *scale, void *copy,
-                              int64_t rows, int64_t width, int pitch) {
-  if (fmt == MOE_E5M2)
-    hipLaunchKernelGGL((k_quant_rows<BF16, MOE_E5M2>), grid, dim3(threads), 0, stream, x, src_rows,
-                       gather, div, row_scale, (uint8_t *)q, (uint8_t *)scale, copy, rows,
-                       (int)width, pitch);
+template <bool BF16, int FMT>
+static void launch_quant_rows(dim3 grid, int threads, hipStream_t stream, const void *x,
+                              int64_t src_rows, const int32_t *gather, int div,
+                              const float *row_scale, void *q, void *scale, void *copy, int64_t rows,
+                              int64_t width, int pitch) {
+  if (row_scale)
+    hipLaunchKernelGGL((k_quant_rows<BF16, FMT, true>), grid, dim3(threads), 0, stream, x, src_rows,
+                       gather, div, row_scale, (uint8_t *)q, (uint8_t *)scale, copy, rows, (int)width,
+                       pitch);
   else
-    hipLaunchKernelGGL((k_quant_rows<BF16, MOE_E4M3>), grid, dim3(threads), 0, stream, x, src_rows,
-                       gather, div, row_scale, (uint8_t *)q, (uint8_t *)scale, copy, rows,
-                       (int)width, pitch);
+    hipLaunchKernelGGL((k_quant_rows<BF16, FMT, false>), grid, dim3(threads), 0, stream, x, src_rows,
+                       gather, div, row_scale, (uint8_t *)q, (uint8_t *)scale, copy, rows, (int)width,
+                       pitch);
 }
 
 }  // namespace moe
@@ -214,16 +292,14 @@ extern "C" moe_status_t moe_quant_rows(moe_dtype dtype, moe_fp8 fmt, int64_t row
   if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale) || !aligned16(copy))
     return MOE_EINVAL;
   const int pitch = (int)scale_pitch(width);
-  const int units = pitch * kQuantLanes;  // threads of one row, the padding of its scales included
-  const int threads = units < kQuantMaxThreads ? units : kQuantMaxThreads;
+  const int units = ceil_div(width, kBlock) * kQuantLanes;  // threads of one row
+  const int threads = units < kQuantMaxThreads ? (units + kWave - 1) / kWave * kWave : kQuantMaxThreads;
   const dim3 grid((unsigned)(rows < kQuantMaxGridX ? rows : kQuantMaxGridX),
                   (unsigned)ceil_div(units, threads));
-  if (dtype == MOE_BF16)
-    launch_quant_rows<true>(fmt, grid, threads, stream, x, src_rows, gather, gather_div, row_scale,
-                            q, scale, copy, rows, width, pitch);
-  else
-    launch_quant_rows<false>(fmt, grid, threads, stream, x, src_rows, gather, gather_div, row_scale,
-                             q, scale, copy, rows, width, pitch);
+  const auto launch = dtype == MOE_BF16
+                          ? (fmt == MOE_E4M3 ? launch_quant_rows<true, MOE_E4M3> : launch_quant_rows<true, MOE_E5M2>)
+                          : (fmt == MOE_E4M3 ? launch_quant_rows<false, MOE_E4M3> : launch_quant_rows<false, MOE_E5M2>);
+  launch(grid, threads, stream, x, src_rows, gather, gather_div, row_scale, q, scale, copy, rows, width, pitch);
   return launch_status();
 }
 
