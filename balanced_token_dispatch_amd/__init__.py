@@ -197,10 +197,7 @@ def moe_group_gemm_gather(op, x_src, gather, gather_div, b, cu_seqlens, out, Kd,
     _check(_lib.moe_group_gemm_gather(op, _dtype(x_src), G, gather.numel(), Kd, N, _ptr(x_src),
                                       x_src.shape[0], _ptr(gather), gather_div, _ptr(b),
                                       _ptr(cu_seqlens), _ptr(out), wp, wn, _stream(stream)),
-           "moe_group_gemm_gather", "moe_scale_row_bytes", "moe_quant_rows", "moe_quant_weight",
-           "moe_group_gemm_scaled_workspace_bytes", "moe_group_gemm_scaled", "moe_router_topk",
-           "moe_router_backward", "moe_grad_sumsq_workspace_bytes", "moe_grad_sumsq",
-           "moe_grad_clip")
+           "moe_group_gemm_gather")
 
 
 def moe_group_gemm_swiglu(a, b, cu_seqlens, z, h, Kd, N, ws=None, stream=None):

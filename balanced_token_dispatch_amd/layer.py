@@ -36,22 +36,57 @@ The activation between the projections is the identity, or, with
 2H' columns holding (gate, up) pairs, its GEMM writes both the pre-activation
 h and z = silu(gate) * up, and the backward turns dz into dh with the gated
 unit's derivative before the up projection's DGRAD and WGRAD.
+With ``gemm="scaled"`` (bf16, identity) the forward and input-gradient GEMMs run on 8-bit operands
+with a scale for each block of 128 (moe_group_gemm_scaled): quantise_weights() puts the home
+experts' weights into 8 bits once per weight update, the prefetch copies their 8-bit rows into the
+slots, the permutes write 8-bit rows beside the 16-bit ones, and z and dz are quantised between the
+projections.  The weight gradients stay on the 16-bit rows.
+Around the step: route() makes this rank's expert ids and weights from its gate's logits,
+route_backward() the logits' gradient from the step's router-weight gradient, and clip_gradients()
+scales the expert gradients (and any others given) to a largest global norm.
 """
 from dataclasses import dataclass
 
 import torch
 
 from . import (GEMM_DGRAD, GEMM_FWD, GEMM_WGRAD, dims as _mk_dims, dispatch_layout_workspace_bytes,
+               grad_sumsq_workspace_bytes, group_gemm_scaled_workspace_bytes,
                group_gemm_workspace_bytes, moe_combine, moe_combine_weight_grad,
-               moe_dispatch_layout, moe_group_gemm, moe_group_gemm_gather, moe_group_gemm_swiglu,
+               moe_dispatch_layout, moe_grad_clip, moe_grad_sumsq, moe_group_gemm,
+               moe_group_gemm_gather, moe_group_gemm_scaled, moe_group_gemm_swiglu,
                moe_permute, moe_plan, moe_plan_noalloc,
-               moe_prefetch, moe_replica_grad_fold, moe_swiglu_backward, moe_unpermute_reduce,
-               plan_words, plan_workspace_bytes)
+               moe_prefetch, moe_quant_rows, moe_quant_weight, moe_replica_grad_fold,
+               moe_router_backward, moe_router_topk, moe_swiglu_backward, moe_unpermute_reduce,
+               plan_words, plan_workspace_bytes, scale_row_bytes)
 
 
 # S*K*H*H' from which the backward uses its second stream by default (the R32 S4096 K8 H7168
 # H'2048 step has 4.8e11; its DGRADs take ~0.8 ms each)
 kOverlapMinWork = 1e11
+
+
+class QuantWeights:
+    """One projection's weights [G, Kd, N] in 8 bits, in the order DGRAD contracts (q) and the order FWD
+    contracts (qt), each with its scales."""
+
+    def __init__(self, w):
+        G, Kd, N = w.shape
+        u8 = dict(dtype=torch.uint8, device=w.device)
+        self.q = torch.zeros((G, Kd, N), **u8).view(torch.float8_e4m3fn)
+        self.qt = torch.zeros((G, N, Kd), **u8).view(torch.float8_e4m3fn)
+        self.q_scale = torch.full((G, -(-Kd // 128), scale_row_bytes(N)), 127, **u8)
+        self.qt_scale = torch.full((G, -(-N // 128), scale_row_bytes(Kd)), 127, **u8)
+
+    def tensors(self):
+        return self.q, self.q_scale, self.qt, self.qt_scale
+
+
+class QuantRows:
+    """A buffer of rows in 8 bits with their scales."""
+
+    def __init__(self, rows, width, dtype, device):
+        self.q = torch.zeros((rows, width), dtype=torch.uint8, device=device).view(dtype)
+        self.scale = torch.full((rows, scale_row_bytes(width)), 127, dtype=torch.uint8, device=device)
 
 
 @dataclass
@@ -76,12 +111,22 @@ class Shape:
 class LayerStep:
     def __init__(self, shape: Shape, rank: int = 0, dtype=torch.bfloat16, device="cuda",
                  backward: bool = True, activation: str = "identity", fused_gather: bool = False,
-                 plan_noalloc: bool = False, overlap=None):
+                 plan_noalloc: bool = False, overlap=None, gemm: str = "bf16",
+                 grad_format=torch.float8_e4m3fn):
         s = shape
         if activation not in ("identity", "swiglu"):
             raise ValueError(f"activation {activation!r}")
         if fused_gather and (activation != "identity" or dtype != torch.bfloat16):
             raise ValueError("the gathered (permute-fused) up projection is bf16, identity only")
+        if gemm not in ("bf16", "scaled"):
+            raise ValueError(f"gemm {gemm!r}")
+        if gemm == "scaled" and (activation != "identity" or dtype != torch.bfloat16 or fused_gather):
+            raise ValueError("8-bit GEMMs are for bf16 layers, identity activation, unfused permute")
+        if gemm == "scaled" and (s.H % 16 or s.Hp % 16):
+            raise ValueError("8-bit GEMMs need H and H' to be multiples of 16")
+        if grad_format not in (torch.float8_e4m3fn, torch.float8_e5m2):
+            raise ValueError(f"grad_format {grad_format}")
+        self.scaled = gemm == "scaled"
         self.fused_gather = fused_gather
         # plan with the library's static scratch (moe_plan_noalloc) instead of the workspace
         self.plan_noalloc = plan_noalloc
@@ -117,6 +162,12 @@ class LayerStep:
         self.hpre = torch.zeros((s.SK, self.up_cols), **act) if activation == "swiglu" else None
         self.y_all = torch.zeros((s.R * s.SK, s.H), **act)
         self.out = torch.zeros((s.S, s.H), **act)
+        if self.scaled:
+            self.q_up, self.q_down = QuantWeights(self.w_up), QuantWeights(self.w_down)
+            e4 = torch.float8_e4m3fn
+            self.xq, self.zq = QuantRows(s.SK, s.H, e4, device), QuantRows(s.SK, s.Hp, e4, device)
+            self.scaled_ws = torch.empty(group_gemm_scaled_workspace_bytes(), dtype=torch.uint8,
+                                         device=device)
         self.backward_enabled = backward
         # the backward's side stream (default priority) and its fork/join events; by default
         # only where the GEMMs are long enough for the kernels beside them to gain more than
@@ -139,6 +190,13 @@ class LayerStep:
             self.dtopk_w = torch.zeros(s.SK, **f32)
             self.dw_up = torch.zeros((s.G, s.H, self.up_cols), **f32)
             self.dw_down = torch.zeros((s.G, s.Hp, s.H), **f32)
+            if self.scaled:
+                self.dyq = QuantRows(s.SK, s.H, grad_format, device)
+                self.dzq = QuantRows(s.SK, s.Hp, grad_format, device)
+            # clip_gradients(): the sum of squares, the norm, scratch
+            self.sumsq = torch.zeros(1, dtype=torch.float64, device=device)
+            self.grad_norm = torch.zeros(1, **f32)
+            self.clip_ws = torch.empty(grad_sumsq_workspace_bytes(), dtype=torch.uint8, device=device)
 
     @property
     def dxp(self):
@@ -151,6 +209,36 @@ class LayerStep:
         """This rank's slice of the expert-output buffer (the down GEMM writes here)."""
         r, SK = self.rank, self.s.SK
         return self.y_all[r * SK:(r + 1) * SK]
+
+    def quantise_weights(self):
+        """The home experts' weights into 8 bits (gemm="scaled"): after every change of w_up or w_down.
+        The slots' rows follow by the step's prefetch."""
+        E = self.s.E
+        for w, qw in ((self.w_up, self.q_up), (self.w_down, self.q_down)):
+            moe_quant_weight(w[:E], *(t[:E] for t in qw.tensors()))
+
+    def route(self, logits, score="softmax_topk", bias=None, factor=1.0):
+        """This rank's expert ids and router weights (its rows of topk_idx and topk_w) from its gate's
+        logits [S, E]."""
+        moe_router_topk(logits, self.topk_idx[self.rank], self.topk_w[self.rank], score, bias, factor)
+
+    def route_backward(self, logits, dlogits, score="softmax_topk", factor=1.0):
+        """dlogits [S, E] from the router-weight gradient of the last backward."""
+        moe_router_backward(logits, self.topk_idx[self.rank],
+                            self.dtopk_w.view(self.s.S, self.s.K), dlogits, score, factor)
+
+    def clip_gradients(self, max_norm, others=(), group=None):
+        """Scales the home experts' weight gradients, and the gradients in `others`, in place to a
+        global norm of at most max_norm; returns the norm before (a one-element tensor).  With a
+        process group the norm is over the gradients of all its ranks.  After backward(), whose fold
+        leaves the slots' rows zero."""
+        E = self.s.E
+        grads = [self.dw_up[:E], self.dw_down[:E], *others]
+        moe_grad_sumsq(grads, self.sumsq, self.clip_ws)
+        if group is not None:
+            torch.distributed.all_reduce(self.sumsq, group=group)
+        moe_grad_clip(grads, self.sumsq, max_norm, self.grad_norm)
+        return self.grad_norm
 
     @staticmethod
     def _call(timer, name, fn, *args):
@@ -169,6 +257,19 @@ class LayerStep:
               self.status, self.ws)
         c(timer, "dispatch_layout", moe_dispatch_layout, self.d, r, self.topk_idx, self.plan,
           self.cu, self.dest, self.src, self.ws)
+        if self.scaled:
+            for qw in (self.q_up, self.q_down):
+                for t in qw.tensors() if self.backward_enabled else (qw.qt, qw.qt_scale):
+                    c(timer, "prefetch", moe_prefetch, self.d, r, self.plan, t)
+            c(timer, "permute_quant", self._quant_rows, self.x_all, self.xq, self.xp, None)
+            c(timer, "gemm_fwd_scaled", moe_group_gemm_scaled, GEMM_FWD, self.xq.q, self.xq.scale,
+              self.q_up.qt, self.q_up.qt_scale, self.cu, self.z, s.H, s.Hp, self.scaled_ws)
+            c(timer, "quant", moe_quant_rows, self.z, self.zq.q, self.zq.scale)
+            c(timer, "gemm_fwd_scaled", moe_group_gemm_scaled, GEMM_FWD, self.zq.q, self.zq.scale,
+              self.q_down.qt, self.q_down.qt_scale, self.cu, self.y, s.Hp, s.H, self.scaled_ws)
+            c(timer, "combine", moe_combine, self.d, r, self.y_all, self.dest,
+              self.topk_w.view(-1), self.out)
+            return
         c(timer, "prefetch", moe_prefetch, self.d, r, self.plan, self.w_up)
         c(timer, "prefetch", moe_prefetch, self.d, r, self.plan, self.w_down)
         if self.fused_gather:   # up projection reading the token rows through src_flat
@@ -187,10 +288,37 @@ class LayerStep:
         c(timer, "combine", moe_combine, self.d, r, self.y_all, self.dest,
           self.topk_w.view(-1), self.out)
 
+    def _quant_rows(self, x, to, copy, row_scale):
+        """Token rows in expert order, in 8 bits and (copy) in 16."""
+        moe_quant_rows(x, to.q, to.scale, gather=self.src, gather_div=self.s.K, row_scale=row_scale,
+                       copy=copy)
+
+    def _down_dgrad(self, timer):
+        s = self.s
+        if self.scaled:
+            return (timer, "gemm_dgrad_scaled", moe_group_gemm_scaled, GEMM_DGRAD, self.dyq.q,
+                    self.dyq.scale, self.q_down.q, self.q_down.q_scale, self.cu, self.dz, s.Hp, s.H,
+                    self.scaled_ws)
+        return (timer, "gemm_dgrad", moe_group_gemm, GEMM_DGRAD, self.dy, self.w_down, self.cu, self.dz,
+                s.Hp, s.H, self.gemm_ws)
+
+    def _up_dgrad(self, timer, dup):
+        s = self.s
+        if self.scaled:
+            return (timer, "gemm_dgrad_scaled", moe_group_gemm_scaled, GEMM_DGRAD, self.dzq.q,
+                    self.dzq.scale, self.q_up.q, self.q_up.q_scale, self.cu, self.dxp, s.H, s.Hp,
+                    self.scaled_ws)
+        return (timer, "gemm_dgrad", moe_group_gemm, GEMM_DGRAD, dup, self.w_up, self.cu, self.dxp,
+                s.H, self.up_cols, self.gemm_ws)
+
     def backward(self, timer=None):
         s, r, c = self.s, self.rank, self._call
-        c(timer, "permute_weighted", moe_permute, self.d, self.dout_all, self.src, self.dy,
-          self.topk_w.view(-1))
+        if self.scaled:
+            c(timer, "permute_weighted_quant", self._quant_rows, self.dout_all, self.dyq, self.dy,
+              self.topk_w.view(-1))
+        else:
+            c(timer, "permute_weighted", moe_permute, self.d, self.dout_all, self.src, self.dy,
+              self.topk_w.view(-1))
         cwgrad = (timer, "combine_wgrad", moe_combine_weight_grad, self.d, r, self.y_all,
                   self.dest, self.dout_all[r * s.S:(r + 1) * s.S], self.dtopk_w)
         if self.overlap:
@@ -198,8 +326,7 @@ class LayerStep:
             self.ev_fork.record(main)
         else:
             c(*cwgrad)
-        c(timer, "gemm_dgrad", moe_group_gemm, GEMM_DGRAD, self.dy, self.w_down, self.cu, self.dz,
-          s.Hp, s.H, self.gemm_ws)
+        c(*self._down_dgrad(timer))
         if self.overlap:  # beside the down DGRAD: it reads only forward results and dout
             self.side.wait_event(self.ev_fork)
             with torch.cuda.stream(self.side):
@@ -210,8 +337,9 @@ class LayerStep:
         if self.activation == "swiglu":
             c(timer, "swiglu_bwd", moe_swiglu_backward, self.hpre, self.dz, self.dh)
             dup = self.dh
-        up_dgrad = (timer, "gemm_dgrad", moe_group_gemm, GEMM_DGRAD, dup, self.w_up, self.cu,
-                    self.dxp, s.H, self.up_cols, self.gemm_ws)
+        if self.scaled:
+            c(timer, "quant", moe_quant_rows, self.dz, self.dzq.q, self.dzq.scale)
+        up_dgrad = self._up_dgrad(timer, dup)
         if not self.overlap:
             c(*up_dgrad)
         if self.fused_gather:
