@@ -170,8 +170,9 @@ __global__ __launch_bounds__(64 * W) void k_scaled_few(
 // R stages.
 constexpr int kTileThreads = 256, kTileWaves = 4;
 // Scales come in pieces of 16 stages: 16 bytes of each of the tile's rows and then of its column
-// blocks (a load writes 64 such rows).
-constexpr int kScaleStages = 16;
+// blocks, in three buffers in turn (a tile's last piece may be too short a time to fetch the next
+// tile's first in, so that one is fetched during the piece before).
+constexpr int kScaleStages = 16, kScaleBufs = 3;
 constexpr int kGroupRows = 8, kXcdCount = 8;
 
 template <int TM_, int TN_, int R_>
@@ -180,7 +181,7 @@ struct Tile {
   static constexpr int rows = 64 * TM, cols = 64 * TN;
   static constexpr int a_bytes = rows * kBlock, stage = (rows + cols) * kBlock;
   static constexpr int a_loads = 2 * TM, b_loads = 2 * TN;  // 1-KB loads per wave and stage
-  static constexpr int scale_bytes = (rows + 64) * 16;      // of one piece
+  static constexpr int scale_bytes = rows * 16 + 256;       // of one piece
   static constexpr int ring = R * stage;
   static constexpr bool whole = TM * TN <= 4;
   static constexpr int stores = 2 * TM * TN;                // of one wave's part of the tile
@@ -255,6 +256,18 @@ __device__ inline void load_to_lds_unless(int skip, int off, __amdgpu_buffer_rsr
       "s_cmp_lg_u32 %3, 0\n\t"
       "s_cbranch_scc1 .Lskip%=\n\t"
       "buffer_load_dwordx4 %0, %1, %2 offen lds\n"
+      ".Lskip%=:" ::"v"(off),
+      "s"(rs), "s"(soff), "s"(skip), "{m0}"(m0)
+      : "memory", "scc");
+}
+
+// 4 bytes per lane, the same way.
+__device__ inline void load4_to_lds_unless(int skip, int off, __amdgpu_buffer_rsrc_t rs, int soff,
+                                           uint32_t m0) {
+  asm volatile(
+      "s_cmp_lg_u32 %3, 0\n\t"
+      "s_cbranch_scc1 .Lskip%=\n\t"
+      "buffer_load_dword %0, %1, %2 offen lds\n"
       ".Lskip%=:" ::"v"(off),
       "s"(rs), "s"(soff), "s"(skip), "{m0}"(m0)
       : "memory", "scc");
@@ -358,7 +371,7 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
     const int32_t *__restrict__ cu, uint16_t *__restrict__ out, int G, int M_total, int K, int N) {
   constexpr int TM = T::TM, TN = T::TN, R = T::R, NM = TM * TN, H = NM / 2, NF = TM + TN;
   __shared__ __attribute__((aligned(16))) uint8_t ring[T::ring];
-  __shared__ __attribute__((aligned(16))) uint8_t scales[2 * T::scale_bytes];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[kScaleBufs * T::scale_bytes];
   __shared__ int sCu[kScMaxG + 1], sStart[kScMaxG + 1];
   const int n_rt =
       __builtin_amdgcn_readfirstlane(sc_build_tiles<kTileThreads>(cu, G, M_total, T::rows, sCu, sStart));
@@ -424,11 +437,28 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
   // Piece `piece` of a tile's scales (16 stages) into LDS buffer `buf`, where `skip` is 0: wave
   // w < TM loads a's rows 64 w .. + 64, and wave 0 the rows of b's column blocks.
   const int w = __builtin_amdgcn_readfirstlane(wid), scale_off = (lane + 64 * (w / TM ? 0 : w)) * pitch;
+  const int block_off = (lane >> 2) * pitch + (lane & 3) * 4;
   auto load_scales = [&](int skip, const Place &p, int piece, int buf) {
     const uint32_t to = scales_lds + buf * T::scale_bytes;
     load_to_lds_unless(skip | w / TM, scale_off, buffer_of(p.sa, p.rows * pitch), piece * 16, to + w * 1024);
-    load_to_lds_unless(skip | w, scale_off, buffer_of(p.sb, (p.cols + kBlock - 1) / kBlock * pitch),
-                       piece * 16, to + T::rows * 16);
+    load4_to_lds_unless(skip | w, block_off, buffer_of(p.sb, (p.cols + kBlock - 1) / kBlock * pitch),
+                        piece * 16, to + T::rows * 16);
+  };
+  // What to fetch at stage s (q: its place in its piece, in buffer buf).  At the start of a piece, the
+  // piece after it: the tile's own, or after its last one the next tile's first.  A last piece of
+  // fewer than R stages is over before a load then issued is sure to have landed; what follows it is
+  // fetched from stage kSecond of the piece before, into the buffer after next.
+  constexpr int kSecond = T::whole ? 8 : 14;
+  auto next_scales = [&](int s, int q, int nk, int buf) {
+    const int rest = nk - (s + kScaleStages - q);  // stages of the tile after this piece
+    // each 0 where it holds (as numbers: truth values would go through vector registers): a piece
+    // starts that is not a short last one; place kSecond, and the piece after this one is a short last
+    const int first = q | max(R - (nk - s), 0);
+    const int second = (q ^ kSecond) | max(rest - R + 1, 0) | max(1 - rest, 0);
+    const bool own = q == 0 && rest > 0;
+    const int to = buf + (second == 0 ? 2 : 1);
+    load_scales(first * second, own ? at : next, own ? s / kScaleStages + 1 : 0,
+                to >= kScaleBufs ? to - kScaleBufs : to);
   };
   load_scales(0, at, 0, 0);
 #pragma unroll
@@ -468,13 +498,12 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
         const uint8_t *ns = ring + nxt * T::stage;
         const int q = s % kScaleStages;
         const bool turn = q == kScaleStages - 1 || s == nk - 1;
-        const int nbuf = turn ? buf ^ 1 : buf, nq = turn ? 0 : q + 1;
+        const int nbuf = !turn ? buf : buf + 1 == kScaleBufs ? 0 : buf + 1, nq = turn ? 0 : q + 1;
         const int mask = s == nk - 1 || s + 1 < kblocks ? 255 : 0;
         const int ls = s + R < nk ? s + R : s + R - nk;
         const Place &lp = s + R < nk ? at : next;
         const __amdgpu_buffer_rsrc_t ra = buffer_of(lp.a, ls < kblocks ? lp.rows * K : 0);
         const __amdgpu_buffer_rsrc_t rb = buffer_of(lp.b, ls < kblocks ? lp.cols * K : 0);
-        const bool same = s + kScaleStages < nk;
         wait_loads_or<kAhead, T::stores>(s | settled);
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -497,7 +526,7 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
               else
                 op_load<RAGGED>(lo, rb, ls, K, ring_lds + cur * T::stage + T::a_bytes, u - T::a_loads);
             }
-          if (i == NM) load_scales(q, same ? at : next, same ? s / kScaleStages + 1 : 0, buf ^ 1);
+          if (i == NM) next_scales(s, q, nk, buf);
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -526,7 +555,7 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
       const int q = s % kScaleStages;
       // the next piece: this tile's next 16 stages, or the next tile's first
       const bool turn = q == kScaleStages - 1 || s == nk - 1;
-      const int nbuf = turn ? buf ^ 1 : buf, nq = turn ? 0 : q + 1;
+      const int nbuf = !turn ? buf : buf + 1 == kScaleBufs ? 0 : buf + 1, nq = turn ? 0 : q + 1;
       const int mask = s == nk - 1 || s + 1 < kblocks ? 255 : 0;
       // loads of stage s + R (b's of s + R - 1 where they are split): this tile's or, past its end,
       // the next one's
@@ -557,10 +586,7 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
         for (int u = 0; u < T::b_loads; ++u)
           if ((kSplit ? u * NM / T::b_loads : kFree + (T::a_loads + u) * kSpan / kAll) == i)
             op_load<RAGGED>(lo, rb, bs, K, to_b, u);
-        if (i == H) {
-          const bool same = s + kScaleStages < nk;
-          load_scales(q, same ? at : next, same ? s / kScaleStages + 1 : 0, buf ^ 1);
-        }
+        if (i == H) next_scales(s, q, nk, buf);
         __builtin_amdgcn_sched_barrier(0);
       };
 #pragma unroll

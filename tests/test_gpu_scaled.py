@@ -234,6 +234,11 @@ KERNELS = {
     "tiles_128x256": ([300, 0, 129, 127, 511], 1424, 8192), "tiles_128x256_short": ([700, 300], 272, 8208),
     "tiles_256x256": ([1500, 1700], 2176, 4112), "tiles_256x256_short": ([1025], 112, 16400),
     "tiles_256x256_many": ([5000], 528, 8208),
+    # several tiles a workgroup and a last piece of scales (16 blocks of the contraction) of 1 to 7 blocks
+    "stream_64x64": ([576], 2176, 2048), "stream_64x128": ([60] * 40, 2064, 2064),
+    "stream_64x128_3": ([60] * 40, 2352, 2064), "stream_64x128_6": ([60] * 40, 2800, 2064),
+    "stream_128x256": ([300] * 12, 2176, 8208), "stream_128x256_2": ([300] * 12, 2304, 8208),
+    "stream_256x256": ([5000], 2064, 8208), "stream_256x256_2": ([5000], 4352, 8208),
 }
 
 
