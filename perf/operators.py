@@ -304,8 +304,7 @@ def _own(st):
         # the input gradient contracts the weights' columns: [Kd, N] rows of N, out Kd wide
         kind = m.GEMM_DGRAD if st["grad"] else m.GEMM_FWD
         kd, n = (st["columns"], st["contraction"]) if st["grad"] else (st["contraction"], st["columns"])
-        ws = empty(m.group_gemm_scaled_workspace_bytes(), dtype=torch.uint8)
-        m.moe_group_gemm_scaled(kind, st["a"], st["a_scale"], st["b"], st["b_scale"], st["cu"], out, kd, n, ws)
+        m.moe_group_gemm_scaled(kind, st["a"], st["a_scale"], st["b"], st["b_scale"], st["cu"], out, kd, n)
         return out
     if op == "quantise_rows":
         rows, width = st["rows"] if st["gather"] is not None else st["source"], st["width"]
