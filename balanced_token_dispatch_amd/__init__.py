@@ -31,7 +31,7 @@ EXPORTS = ("moe_status_string", "moe_plan_words", "moe_plan_workspace_bytes", "m
            "moe_unpermute_reduce", "moe_combine_weight_grad", "moe_group_gemm_swiglu",
            "moe_swiglu_backward", "moe_group_gemm_workspace_bytes", "moe_plan_noalloc",
            "moe_group_gemm_gather", "moe_scale_row_bytes", "moe_quant_rows", "moe_quant_weight",
-           "moe_group_gemm_scaled_workspace_bytes", "moe_group_gemm_scaled", "moe_router_topk",
+           "moe_group_gemm_scaled", "moe_router_topk",
            "moe_router_backward", "moe_grad_sumsq_workspace_bytes", "moe_grad_sumsq",
            "moe_grad_clip")
 
@@ -72,14 +72,13 @@ _lib.moe_group_gemm_swiglu.argtypes = [ctypes.c_int, _I32, _I32, _I32, _I32, _P,
 _lib.moe_swiglu_backward.argtypes = [ctypes.c_int, _I64, _I64, _P, _P, _P, _P]
 _lib.moe_scale_row_bytes.restype = _SZ
 _lib.moe_scale_row_bytes.argtypes = [_I64]
-for _n in ("moe_group_gemm_scaled_workspace_bytes", "moe_grad_sumsq_workspace_bytes"):
-    getattr(_lib, _n).restype = _SZ
-    getattr(_lib, _n).argtypes = []
+_lib.moe_grad_sumsq_workspace_bytes.restype = _SZ
+_lib.moe_grad_sumsq_workspace_bytes.argtypes = []
 _lib.moe_quant_rows.argtypes = [ctypes.c_int, ctypes.c_int, _I64, _I64, _P, _I64, _P, _I32, _P, _P,
                                 _P, _P, _P]
 _lib.moe_quant_weight.argtypes = [ctypes.c_int, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P]
-_lib.moe_group_gemm_scaled.argtypes = [ctypes.c_int, ctypes.c_int, _I32, _I32, _I32, _I32,
-                                       _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+_lib.moe_group_gemm_scaled.argtypes = [ctypes.c_int, ctypes.c_int, _I32, _I32, _I32, _I32, _P, _P,
+                                       _P, _P, _P, _P, _P]
 _lib.moe_router_topk.argtypes = [ctypes.c_int, ctypes.c_int, _I64, _I32, _I32, _P, _P,
                                  ctypes.c_float, _P, _P, _P]
 _lib.moe_router_backward.argtypes = [ctypes.c_int, ctypes.c_int, _I64, _I32, _I32, _P, _P, _P,
@@ -311,11 +310,7 @@ def moe_quant_weight(w, q=None, q_scale=None, qt=None, qt_scale=None, stream=Non
                                  _stream(stream)), "moe_quant_weight")
 
 
-def group_gemm_scaled_workspace_bytes():
-    return _lib.moe_group_gemm_scaled_workspace_bytes()
-
-
-def moe_group_gemm_scaled(op, a, a_scale, b, b_scale, cu_seqlens, out, Kd, N, ws=None, stream=None):
+def moe_group_gemm_scaled(op, a, a_scale, b, b_scale, cu_seqlens, out, Kd, N, stream=None):
     """moe_group_gemm (FWD or DGRAD) on 8-bit operands: a from moe_quant_rows, b = qt (FWD) or q
     (DGRAD) of moe_quant_weight; out bf16."""
     dev = _current("a", a)
@@ -327,10 +322,8 @@ def moe_group_gemm_scaled(op, a, a_scale, b, b_scale, cu_seqlens, out, Kd, N, ws
     bsp = _take(dev, "b_scale", b_scale, _SCALE, G * -(-C // 128) * scale_row_bytes(K))
     cp = _take(dev, "cu_seqlens", cu_seqlens, (torch.int32,), None)
     op_ = _take(dev, "out", out, (torch.bfloat16,), M * C)
-    wp, wn = (None, 0) if ws is None or ws.numel() == 0 else (_take(dev, "ws", ws, (ws.dtype,), None),
-                                                              ws.numel() * ws.element_size())
     _check(_lib.moe_group_gemm_scaled(op, _FP8[a.dtype], G, M, Kd, N, ap, asp, bp, bsp, cp,
-                                      op_, wp, wn, _stream(stream)),
+                                      op_, _stream(stream)),
            "moe_group_gemm_scaled")
 
 

@@ -434,31 +434,40 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
   constexpr int kLoads = T::a_loads > T::b_loads ? T::a_loads : T::b_loads;
   const Offsets<kLoads> lo = offsets<kLoads>(K);
 
-  // Piece `piece` of a tile's scales (16 stages) into LDS buffer `buf`, where `skip` is 0: wave
+  // The piece of a tile's scales from byte `at` on into LDS buffer `buf`, where `skip` is 0: wave
   // w < TM loads a's rows 64 w .. + 64, and wave 0 the rows of b's column blocks.
   const int w = __builtin_amdgcn_readfirstlane(wid), scale_off = (lane + 64 * (w / TM ? 0 : w)) * pitch;
   const int block_off = (lane >> 2) * pitch + (lane & 3) * 4;
-  auto load_scales = [&](int skip, const Place &p, int piece, int buf) {
+  auto load_scales = [&](int skip, const Place &p, int at, int buf) {
     const uint32_t to = scales_lds + buf * T::scale_bytes;
-    load_to_lds_unless(skip | w / TM, scale_off, buffer_of(p.sa, p.rows * pitch), piece * 16, to + w * 1024);
+    load_to_lds_unless(skip | w / TM, scale_off, buffer_of(p.sa, p.rows * pitch), at, to + w * 1024);
     load4_to_lds_unless(skip | w, block_off, buffer_of(p.sb, (p.cols + kBlock - 1) / kBlock * pitch),
-                        piece * 16, to + T::rows * 16);
+                        at, to + T::rows * 16);
   };
   // What to fetch at stage s (q: its place in its piece, in buffer buf).  At the start of a piece, the
   // piece after it: the tile's own, or after its last one the next tile's first.  A last piece of
   // fewer than R stages is over before a load then issued is sure to have landed; what follows it is
   // fetched from stage kSecond of the piece before, into the buffer after next.
   constexpr int kSecond = T::whole ? 8 : 14;
+  struct Fetch {
+    int skip, at, to;  // 0: fetch; first byte of the rows of scales; LDS buffer
+    bool own;
+  };
   auto next_scales = [&](int s, int q, int nk, int buf) {
     const int rest = nk - (s + kScaleStages - q);  // stages of the tile after this piece
     // each 0 where it holds (as numbers: truth values would go through vector registers): a piece
     // starts that is not a short last one; place kSecond, and the piece after this one is a short last
     const int first = q | max(R - (nk - s), 0);
     const int second = (q ^ kSecond) | max(rest - R + 1, 0) | max(1 - rest, 0);
-    const bool own = q == 0 && rest > 0;
+    Fetch f;
+    f.own = q == 0 && rest > 0;
+    f.skip = first * second;
+    f.at = f.own ? s + kScaleStages : 0;
     const int to = buf + (second == 0 ? 2 : 1);
-    load_scales(first * second, own ? at : next, own ? s / kScaleStages + 1 : 0,
-                to >= kScaleBufs ? to - kScaleBufs : to);
+    f.to = to >= kScaleBufs ? to - kScaleBufs : to;
+    if constexpr (!T::whole)  // worked out where it is called, some matrix instructions ahead of its use
+      asm volatile("" : "+s"(f.skip), "+s"(f.at), "+s"(f.to));
+    return f;
   };
   load_scales(0, at, 0, 0);
 #pragma unroll
@@ -526,7 +535,10 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
               else
                 op_load<RAGGED>(lo, rb, ls, K, ring_lds + cur * T::stage + T::a_bytes, u - T::a_loads);
             }
-          if (i == NM) next_scales(s, q, nk, buf);
+          if (i == NM) {
+            const Fetch fe = next_scales(s, q, nk, buf);
+            load_scales(fe.skip, fe.own ? at : next, fe.at, fe.to);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -567,6 +579,7 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
       const __amdgpu_buffer_rsrc_t rb = buffer_of(bp.b, bs < kblocks ? bp.cols * K : 0);
       const uint32_t to_a = ring_lds + cur * T::stage, to_b = ring_lds + (kSplit ? prv : cur) * T::stage + T::a_bytes;
       __builtin_amdgcn_sched_barrier(0);
+      Fetch fe;
       // matrix instruction i of the stage's 2 NM, and what is issued behind it
       auto slot = [&](int i) __attribute__((always_inline)) {
         const int tm = i % NM / TN, tn = i % TN, h = i / NM;
@@ -586,7 +599,8 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
         for (int u = 0; u < T::b_loads; ++u)
           if ((kSplit ? u * NM / T::b_loads : kFree + (T::a_loads + u) * kSpan / kAll) == i)
             op_load<RAGGED>(lo, rb, bs, K, to_b, u);
-        if (i == H) next_scales(s, q, nk, buf);
+        if (i == H / 2) fe = next_scales(s, q, nk, buf);
+        if (i == H) load_scales(fe.skip, fe.own ? at : next, fe.at, fe.to);
         __builtin_amdgcn_sched_barrier(0);
       };
 #pragma unroll
@@ -676,22 +690,18 @@ static void launch_scaled(const uint8_t *a, const uint8_t *as, const uint8_t *b,
 
 using namespace moe;
 
-extern "C" size_t moe_group_gemm_scaled_workspace_bytes(void) { return 0; }
-
 extern "C" moe_status_t moe_group_gemm_scaled(moe_gemm_op op, moe_fp8 a_fmt, int32_t G, int32_t M_total, int32_t Kd, int32_t N,
                                               const void *a, const void *a_scale, const void *b,
                                               const void *b_scale, const int32_t *cu_seqlens,
-                                              void *out, void *ws, size_t ws_bytes,
-                                              hipStream_t stream) {
+                                              void *out, hipStream_t stream) {
   if (op != MOE_GEMM_FWD && op != MOE_GEMM_DGRAD) return MOE_EINVAL;
   if (a_fmt != MOE_E4M3 && a_fmt != MOE_E5M2) return MOE_EINVAL;
   if (G < 1 || G > kScMaxG || M_total < 0 || Kd < 16 || N < 16 || Kd % 16 || N % 16) return MOE_EINVAL;
   if (Kd > kScMaxDim || N > kScMaxDim) return MOE_EINVAL;
-  if (ws && ws_bytes < moe_group_gemm_scaled_workspace_bytes()) return MOE_ENOSPACE;
   if (M_total == 0) return MOE_OK;
   if (!a || !a_scale || !b || !b_scale || !cu_seqlens || !out) return MOE_EINVAL;
   if (!aligned16(a) || !aligned16(a_scale) || !aligned16(b) || !aligned16(b_scale) ||
-      !aligned16(out) || !aligned16(ws) || ((uintptr_t)cu_seqlens & 3))
+      !aligned16(out) || ((uintptr_t)cu_seqlens & 3))
     return MOE_EINVAL;
   // both operands end contiguous along the contraction: FWD contracts Kd, DGRAD contracts N
   const int K = op == MOE_GEMM_FWD ? Kd : N, C = op == MOE_GEMM_FWD ? N : Kd;

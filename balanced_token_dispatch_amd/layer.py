@@ -50,8 +50,7 @@ from dataclasses import dataclass
 import torch
 
 from . import (GEMM_DGRAD, GEMM_FWD, GEMM_WGRAD, dims as _mk_dims, dispatch_layout_workspace_bytes,
-               grad_sumsq_workspace_bytes, group_gemm_scaled_workspace_bytes,
-               group_gemm_workspace_bytes, moe_combine, moe_combine_weight_grad,
+               grad_sumsq_workspace_bytes, group_gemm_workspace_bytes, moe_combine, moe_combine_weight_grad,
                moe_dispatch_layout, moe_grad_clip, moe_grad_sumsq, moe_group_gemm,
                moe_group_gemm_gather, moe_group_gemm_scaled, moe_group_gemm_swiglu,
                moe_permute, moe_plan, moe_plan_noalloc,
@@ -166,8 +165,6 @@ class LayerStep:
             self.q_up, self.q_down = QuantWeights(self.w_up), QuantWeights(self.w_down)
             e4 = torch.float8_e4m3fn
             self.xq, self.zq = QuantRows(s.SK, s.H, e4, device), QuantRows(s.SK, s.Hp, e4, device)
-            self.scaled_ws = torch.empty(group_gemm_scaled_workspace_bytes(), dtype=torch.uint8,
-                                         device=device)
         self.backward_enabled = backward
         # the backward's side stream (default priority) and its fork/join events; by default
         # only where the GEMMs are long enough for the kernels beside them to gain more than
@@ -263,10 +260,10 @@ class LayerStep:
                     c(timer, "prefetch", moe_prefetch, self.d, r, self.plan, t)
             c(timer, "permute_quant", self._quant_rows, self.x_all, self.xq, self.xp, None)
             c(timer, "gemm_fwd_scaled", moe_group_gemm_scaled, GEMM_FWD, self.xq.q, self.xq.scale,
-              self.q_up.qt, self.q_up.qt_scale, self.cu, self.z, s.H, s.Hp, self.scaled_ws)
+              self.q_up.qt, self.q_up.qt_scale, self.cu, self.z, s.H, s.Hp)
             c(timer, "quant", moe_quant_rows, self.z, self.zq.q, self.zq.scale)
             c(timer, "gemm_fwd_scaled", moe_group_gemm_scaled, GEMM_FWD, self.zq.q, self.zq.scale,
-              self.q_down.qt, self.q_down.qt_scale, self.cu, self.y, s.Hp, s.H, self.scaled_ws)
+              self.q_down.qt, self.q_down.qt_scale, self.cu, self.y, s.Hp, s.H)
             c(timer, "combine", moe_combine, self.d, r, self.y_all, self.dest,
               self.topk_w.view(-1), self.out)
             return
@@ -297,8 +294,7 @@ class LayerStep:
         s = self.s
         if self.scaled:
             return (timer, "gemm_dgrad_scaled", moe_group_gemm_scaled, GEMM_DGRAD, self.dyq.q,
-                    self.dyq.scale, self.q_down.q, self.q_down.q_scale, self.cu, self.dz, s.Hp, s.H,
-                    self.scaled_ws)
+                    self.dyq.scale, self.q_down.q, self.q_down.q_scale, self.cu, self.dz, s.Hp, s.H)
         return (timer, "gemm_dgrad", moe_group_gemm, GEMM_DGRAD, self.dy, self.w_down, self.cu, self.dz,
                 s.Hp, s.H, self.gemm_ws)
 
@@ -306,8 +302,7 @@ class LayerStep:
         s = self.s
         if self.scaled:
             return (timer, "gemm_dgrad_scaled", moe_group_gemm_scaled, GEMM_DGRAD, self.dzq.q,
-                    self.dzq.scale, self.q_up.q, self.q_up.q_scale, self.cu, self.dxp, s.H, s.Hp,
-                    self.scaled_ws)
+                    self.dzq.scale, self.q_up.q, self.q_up.q_scale, self.cu, self.dxp, s.H, s.Hp)
         return (timer, "gemm_dgrad", moe_group_gemm, GEMM_DGRAD, dup, self.w_up, self.cu, self.dxp,
                 s.H, self.up_cols, self.gemm_ws)
 

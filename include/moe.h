@@ -433,18 +433,14 @@ moe_status_t moe_quant_weight(moe_dtype dtype, int32_t G, int32_t Kd, int32_t N,
  *   DGRAD: a [M_total, N],  b = q  [G, Kd, N]  -> out [M_total, Kd]
  *   a in a_fmt with a_scale [M_total, moe_scale_row_bytes(contraction)], b in
  *   e4m3 with the scales moe_quant_weight wrote beside it; out bf16.
- *   Kd % 16 == 0, N % 16 == 0, both <= 2^22; all 16-byte aligned.  WGRAD is
+ *   Kd % 16 == 0, N % 16 == 0, both <= 2^21; all 16-byte aligned.  WGRAD is
  *   MOE_EINVAL (its contraction runs over the rows; it takes the 16-bit rows
  *   through moe_group_gemm).
- *   ws: optional device scratch (NULL: none) of at least
- *   moe_group_gemm_scaled_workspace_bytes() bytes, else MOE_ENOSPACE, used as
- *   moe_group_gemm's.
  * ------------------------------------------------------------------------- */
-size_t moe_group_gemm_scaled_workspace_bytes(void);
 moe_status_t moe_group_gemm_scaled(moe_gemm_op op, moe_fp8 a_fmt, int32_t G, int32_t M_total,
                                    int32_t Kd, int32_t N, const void *a, const void *a_scale,
                                    const void *b, const void *b_scale, const int32_t *cu_seqlens,
-                                   void *out, void *ws, size_t ws_bytes, hipStream_t stream);
+                                   void *out, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * moe_router_topk -- the K experts of each token, and their weights, from the

@@ -53,11 +53,11 @@ class Operands:
         return (dev(self.a).view(FP8[self.fmt]), dev(self.a_scale), dev(self.b).view(FP8["e4m3"]),
                 dev(self.b_scale), dev(self.cu))
 
-    def run(self, m, grad=False, ws=None, poison=-7.0):
+    def run(self, m, grad=False, poison=-7.0):
         a, sa, b, sb, cu = self.on_gpu()
         o = torch.full((self.M, self.C), poison, dtype=torch.bfloat16, device="cuda")
         op, kd, n = (m.GEMM_DGRAD, self.C, self.K) if grad else (m.GEMM_FWD, self.K, self.C)
-        m.moe_group_gemm_scaled(op, a, sa, b, sb, cu, o, kd, n, ws)
+        m.moe_group_gemm_scaled(op, a, sa, b, sb, cu, o, kd, n)
         return o
 
 
