@@ -8,6 +8,7 @@ hipStream_t.  Importing it fails loudly when the library is not built.
 import ctypes
 import os
 from array import array
+from operator import attrgetter
 
 import torch
 
@@ -369,15 +370,18 @@ def grad_sumsq_workspace_bytes():
     return _lib.moe_grad_sumsq_workspace_bytes()
 
 
+_dtype_of = attrgetter("dtype")
+
+
 def _table(dev, grads):
-    """Host tables of a list of gradients: addresses, element counts and types (a call's worth of
-    checks on many tensors, so attribute by attribute)."""
-    dt = [_FLOATS.get(g.dtype, -1) for g in grads]
-    if -1 in dt or any(g.get_device() != dev for g in grads) or not all([g.is_contiguous() for g in grads]):
+    """Host tables of a list of gradients: addresses, element counts and types.  A call may bring
+    hundreds of tensors, so each attribute is one map over all of them."""
+    dt = array("i", [_FLOATS.get(t, -1) for t in map(_dtype_of, grads)])
+    T = torch.Tensor
+    if -1 in dt or not set(map(T.get_device, grads)) <= {dev} or not all(map(T.is_contiguous, grads)):
         for g in grads:  # says which
             _take(dev, "gradient", g, _FLOATS, None)
-    return (array("Q", [g.data_ptr() for g in grads]), array("q", [g.numel() for g in grads]),
-            array("i", dt))
+    return array("Q", map(T.data_ptr, grads)), array("q", map(T.numel, grads)), dt
 
 
 def _at(table):
