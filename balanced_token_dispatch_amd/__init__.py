@@ -408,6 +408,9 @@ def moe_grad_clip(grads, sumsq, max_norm, norm=None, out=None, stream=None):
         optr, onumel, odt = _table(dev, out)
         if onumel != numel or odt != dt:
             raise MoeError("out: not one tensor of the type and size of each gradient")
+    written = [p for p, n in zip(optr, numel) if n]
+    if len(set(written)) != len(written):
+        raise MoeError("moe_grad_clip: a tensor is listed twice")
     np_ = None if norm is None else _take(dev, "norm", norm, (torch.float32,), 1)
     _check(_lib.moe_grad_clip(len(grads), _at(ptr), _at(numel), _at(dt),
                               _take(dev, "sumsq", sumsq, (torch.float64,), 1), max_norm, np_, _at(optr),

@@ -297,7 +297,8 @@ extern "C" moe_status_t moe_quant_rows(moe_dtype dtype, moe_fp8 fmt, int64_t row
   if (src_rows < 1 || src_rows >= (1LL << 31) || gather_div < 1) return MOE_EINVAL;
   if (!gather && rows > src_rows) return MOE_EINVAL;
   if (rows == 0) return MOE_OK;
-  if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale) || !aligned16(copy))
+  if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale) || !aligned16(copy) ||
+      (uintptr_t)gather % 4 || (uintptr_t)row_scale % 4)
     return MOE_EINVAL;
   const int pitch = (int)scale_pitch(width);
   const int units = ceil_div(width, kBlock) * kQuantLanes;  // threads of one row

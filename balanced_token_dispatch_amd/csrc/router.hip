@@ -386,6 +386,8 @@ static bool router_args_ok(moe_dtype dtype, moe_score score, int64_t T, int32_t 
   return factor == factor && factor - factor == 0.0f;  // finite
 }
 
+static bool misaligned(const void *p, size_t n) { return (uintptr_t)p % n != 0; }
+
 static dim3 router_grid(int64_t T) {
   const int64_t b = (T + kRtThreads / kWave - 1) / (kRtThreads / kWave);
   return dim3((unsigned)(b < (1 << 22) ? b : (1 << 22)));
@@ -402,6 +404,9 @@ extern "C" moe_status_t moe_router_topk(moe_dtype dtype, moe_score score, int64_
   if (!router_args_ok(dtype, score, T, E, K, factor)) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
   if (!logits || !topk_idx || !topk_w) return MOE_EINVAL;
+  if (misaligned(logits, dtype == MOE_BF16 ? 2 : 4) || misaligned(bias, 4) || misaligned(topk_idx, 4) ||
+      misaligned(topk_w, 4))
+    return MOE_EINVAL;
   with_shape(E, dtype == MOE_BF16, [&](auto r) {
     r.topk(score, router_grid(T), stream, logits, bias, topk_idx, topk_w, T, E, K, factor,
            rows_of_4(dtype, E, logits));
@@ -416,6 +421,10 @@ extern "C" moe_status_t moe_router_backward(moe_dtype dtype, moe_score score, in
   if (!router_args_ok(dtype, score, T, E, K, factor)) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
   if (!logits || !topk_idx || !dtopk_w || !dlogits || logits == dlogits) return MOE_EINVAL;
+  const size_t size = dtype == MOE_BF16 ? 2 : 4;
+  if (misaligned(logits, size) || misaligned(dlogits, size) || misaligned(topk_idx, 4) ||
+      misaligned(dtopk_w, 4))
+    return MOE_EINVAL;
   with_shape(E, dtype == MOE_BF16, [&](auto r) {
     r.bwd(score, router_grid(T), stream, logits, topk_idx, dtopk_w, dlogits, T, E, K, factor,
           rows_of_4(dtype, E, logits) && rows_of_4(dtype, E, dlogits));

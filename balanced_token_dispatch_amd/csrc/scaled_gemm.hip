@@ -122,15 +122,16 @@ __global__ __launch_bounds__(64 * W) void k_scaled_few(
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         const int kb = k0 + d * W, k = kb * kBlock;
-        const int o0 = k + kq < K ? off : kOutside, o1 = k + kq + 64 < K ? off + 64 : kOutside;
+        const bool in0 = k + kq < K, in1 = k + kq + 64 < K;
         const int so = kb < nblk ? k : 0;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          x[d][2 + 2 * c] = __builtin_amdgcn_raw_buffer_load_b128(rb, o0 + c * kFewCols * K, so, 0);
-          x[d][3 + 2 * c] = __builtin_amdgcn_raw_buffer_load_b128(rb, o1 + c * kFewCols * K, so, 0);
+          const int oc = off + c * kFewCols * K;
+          x[d][2 + 2 * c] = __builtin_amdgcn_raw_buffer_load_b128(rb, in0 ? oc : kOutside, so, 0);
+          x[d][3 + 2 * c] = __builtin_amdgcn_raw_buffer_load_b128(rb, in1 ? oc + 64 : kOutside, so, 0);
         }
-        x[d][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, o0, so, 0);
-        x[d][1] = __builtin_amdgcn_raw_buffer_load_b128(ra, o1, so, 0);
+        x[d][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, in0 ? off : kOutside, so, 0);
+        x[d][1] = __builtin_amdgcn_raw_buffer_load_b128(ra, in1 ? off + 64 : kOutside, so, 0);
         sa[d] = __builtin_amdgcn_raw_buffer_load_b8(rsa, kb < nblk ? r * pitch + kb : kOutside, 0, 0);
         sb[d] = __builtin_amdgcn_raw_buffer_load_b8(rsb, kb < nblk ? kb : kOutside, 0, 0);
       }

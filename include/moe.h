@@ -484,8 +484,8 @@ moe_status_t moe_router_backward(moe_dtype dtype, moe_score score, int64_t T, in
  * moe_grad_clip -- outs[i] = grads[i] * min(1, max_norm / (sqrt(*sumsq) + 1e-6))
  * (fp32 product, one rounding), and *norm = sqrt(*sumsq) (norm may be NULL).
  * outs[i] has the type and size of grads[i] and is grads[i] itself or does not
- * overlap any tensor; a tensor clipped in place is left alone where the factor
- * is 1.  A NaN sum gives NaN gradients.  max_norm >= 0.
+ * overlap any tensor; no tensor is listed twice.  A tensor clipped in place is left alone where the
+ * factor is 1.  A NaN sum gives NaN gradients.  max_norm >= 0.
  * ------------------------------------------------------------------------- */
 size_t moe_grad_sumsq_workspace_bytes(void);
 moe_status_t moe_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,

@@ -127,3 +127,16 @@ def test_over_32_bits(m):
     m.moe_grad_clip([g], s, 6.5, norm)
     assert norm.item() == 13.0
     assert [g[0].item(), g[n // 2].item(), g[n - 1].item(), g[n - 2].item()] == [1.5, 2.0, 6.0, 0.0]
+
+
+def test_refused_lists(m):
+    """A tensor listed twice to be clipped, outputs of another type or number, a strided gradient."""
+    g = tensors(4, [100, 200], [F])
+    s = sumsq_of(m, g + g)            # the sum may count a tensor twice
+    for grads, out in ((g + g[:1], None), (g, [g[0], g[0]]), (g, g[:1]), (g, [g[0].bfloat16(), g[1]]), (g, [g[0], g[1][:10]])):
+        with pytest.raises(m.MoeError):
+            m.moe_grad_clip(grads, s, 1.0, out=out)
+    with pytest.raises(m.MoeError):
+        m.moe_grad_sumsq([g[0][::2]], s, torch.empty(m.grad_sumsq_workspace_bytes(), dtype=torch.uint8, device="cuda"))
+    with pytest.raises(m.MoeError):
+        m.moe_grad_sumsq(g, s, torch.empty(8, dtype=torch.uint8, device="cuda"))

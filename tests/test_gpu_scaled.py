@@ -274,3 +274,60 @@ def test_product_kernels(m, name, fmt, grad):
         want[rows] = (a[rows].double() * two(sa[rows])).mm(w.t().contiguous()).bfloat16()
         at += n_rows
     assert torch.equal(out, want)
+
+
+def test_over_32_bits(m):
+    """Operands of more than 2^32 bytes, results in their last rows: the same bits as from small ones."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    M, G, K, C, n = 600000, 270, 8192, 2048, 100
+    last_a = torch.randint(-1, 2, (n, K), device="cuda", generator=gen).float().to(FP8["e4m3"])
+    last_b = torch.randint(-1, 2, (C, K), device="cuda", generator=gen).float().to(FP8["e4m3"])
+    want = (last_a.double() @ last_b.double().t().contiguous()).bfloat16()
+    a = torch.zeros((M, K), dtype=torch.uint8, device="cuda").view(FP8["e4m3"])
+    b = torch.zeros((G, C, K), dtype=torch.uint8, device="cuda").view(FP8["e4m3"])
+    a.view(torch.uint8)[M - n:] = last_a.view(torch.uint8)
+    b.view(torch.uint8)[G - 1] = last_b.view(torch.uint8)
+    sa = torch.full((M, m.scale_row_bytes(K)), 127, dtype=torch.uint8, device="cuda")
+    sb = torch.full((G, C // 128, m.scale_row_bytes(K)), 127, dtype=torch.uint8, device="cuda")
+    cu = torch.full((G + 1,), M - n, dtype=torch.int32, device="cuda")
+    cu[G] = M
+    out = torch.full((M, C), -7.0, dtype=torch.bfloat16, device="cuda")
+    m.moe_group_gemm_scaled(m.GEMM_FWD, a, sa, b, sb, cu, out, K, C)
+    assert torch.equal(out[M - n:], want) and (out[M - n - 1] == -7.0).all()
+    # the few-rows kernel: as many segments as make the rows few
+    few = torch.full((8, C), -7.0, dtype=torch.bfloat16, device="cuda")
+    cu8 = torch.zeros(G + 1, dtype=torch.int32, device="cuda")
+    cu8[G] = 8
+    m.moe_group_gemm_scaled(m.GEMM_FWD, a[M - n:M - n + 8].contiguous(), sa[:8], b, sb, cu8, few, K, C)
+    assert torch.equal(few, want[:8])
+    del a, b, out
+    x = torch.zeros((M, 4096), dtype=torch.bfloat16, device="cuda")
+    x[M - 1] = torch.randn(4096, device="cuda", generator=gen).bfloat16()
+    q = torch.full((M, 4096), 1, dtype=torch.uint8, device="cuda").view(FP8["e4m3"])
+    s = torch.full((M, m.scale_row_bytes(4096)), 9, dtype=torch.uint8, device="cuda")
+    copy = torch.empty_like(x)
+    m.moe_quant_rows(x, q, s, copy=copy)
+    wq, ws, _ = ref.quant_rows(host(x[M - 1:]), "e4m3")
+    assert np.array_equal(host(q[M - 1:]), wq) and np.array_equal(s[M - 1:].cpu().numpy(), ws)
+    assert torch.equal(copy[M - 1], x[M - 1]) and (q[M - 2].view(torch.uint8) == 0).all()
+    g = torch.tensor([(M - 1) * 3 + 2, -1], dtype=torch.int32, device="cuda")
+    m.moe_quant_rows(x, q[:2], s[:2], gather=g, gather_div=3)
+    assert np.array_equal(host(q[:1]), wq) and (q[1].view(torch.uint8) == 0).all()
+
+
+def test_weights_over_32_bits(m):
+    """moe_quant_weight past 2^32 bytes: the last expert as quantised alone."""
+    G, K, N = 130, 4096, 4112
+    w = torch.zeros((G, K, N), dtype=torch.bfloat16, device="cuda")
+    w[G - 1] = torch.randn((K, N), device="cuda").bfloat16()
+    u8 = dict(dtype=torch.uint8, device="cuda")
+
+    def quantise(w):
+        g = w.shape[0]
+        out = (torch.full((g, K, N), 1, **u8).view(FP8["e4m3"]), torch.full((g, K // 128, m.scale_row_bytes(N)), 5, **u8),
+               torch.full((g, N, K), 1, **u8).view(FP8["e4m3"]), torch.full((g, -(-N // 128), m.scale_row_bytes(K)), 5, **u8))
+        m.moe_quant_weight(w, *out)
+        return out
+
+    for big, alone in zip(quantise(w), quantise(w[G - 1:])):
+        assert torch.equal(big.view(torch.uint8)[G - 1:], alone.view(torch.uint8))

@@ -93,7 +93,7 @@ def test_scale_row_bytes(mod):
 
 
 P = ctypes.c_void_p(16)   # never dereferenced: every call below is refused before anything is launched
-ODD = ctypes.c_void_p(24)
+ODD, BYTE = ctypes.c_void_p(24), ctypes.c_void_p(17)
 
 
 def refused(fn, ok, **kw):
@@ -108,7 +108,8 @@ def test_quant_rows_refuses(mod):
     ok = (mod.BF16, mod.E4M3, 8, 256, P, 8, None, 1, None, P, P, None, None)
     for kw in (dict(a0=2), dict(a1=2), dict(a2=-1), dict(a2=1 << 31), dict(a3=0), dict(a3=24), dict(a3=(1 << 22) + 16),
                dict(a4=None), dict(a4=ODD), dict(a5=0), dict(a5=1 << 31), dict(a5=7), dict(a7=0), dict(a9=None),
-               dict(a9=ODD), dict(a10=None), dict(a10=ODD), dict(a11=ODD)):
+               dict(a9=ODD), dict(a10=None), dict(a10=ODD), dict(a11=ODD), dict(a6=BYTE),
+               dict(a8=BYTE)):
         assert refused(fn, ok, **kw) == bad, kw
     assert refused(fn, ok, a2=0) == mod.MOE_OK
 
@@ -137,12 +138,13 @@ def test_router_refuses(mod):
     lib, bad = mod.library(), mod.MOE_EINVAL
     ok = (mod.F32, 0, 4, 64, 8, P, None, 1.0, P, P, None)
     for kw in (dict(a0=2), dict(a1=3), dict(a1=-1), dict(a2=-1), dict(a2=1 << 31), dict(a3=0), dict(a3=1025), dict(a4=0),
-               dict(a4=65), dict(a5=None), dict(a7=float("nan")), dict(a7=float("inf")), dict(a8=None), dict(a9=None)):
+               dict(a4=65), dict(a5=None), dict(a7=float("nan")), dict(a7=float("inf")), dict(a8=None), dict(a9=None),
+               dict(a5=BYTE), dict(a6=BYTE), dict(a8=BYTE), dict(a9=BYTE)):
         assert refused(lib.moe_router_topk, ok, **kw) == bad, kw
     assert refused(lib.moe_router_topk, ok, a2=0) == mod.MOE_OK
     ok = (mod.F32, 0, 4, 64, 8, P, P, P, 1.0, ODD, None)
     for kw in (dict(a0=2), dict(a1=3), dict(a2=-1), dict(a3=1025), dict(a4=0), dict(a5=None), dict(a6=None), dict(a7=None),
-               dict(a8=float("inf")), dict(a9=None), dict(a9=P)):
+               dict(a8=float("inf")), dict(a9=None), dict(a9=P), dict(a5=BYTE), dict(a6=BYTE), dict(a7=BYTE), dict(a9=BYTE)):
         assert refused(lib.moe_router_backward, ok, **kw) == bad, kw
     assert refused(lib.moe_router_backward, ok, a2=0) == mod.MOE_OK
 
