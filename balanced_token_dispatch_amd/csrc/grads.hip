@@ -1,5 +1,8 @@
 // moe_grad_sumsq, moe_grad_clip: the sum of squares over many gradient tensors, and the
-// gradients scaled to a largest norm.  Both only stream the tensors: HBM-bound.
+// gradients scaled to a largest norm.  Both only stream the tensors: HBM-bound.  Two fp32
+// tensors of 285 M values together (3.4 GB: two reads and a write) take 565 us, 6.1 TB/s, where the best
+// copy reaches 5.9: part of the second read meets the memory-side cache (256 MB).  61 short ones (0.13 M
+// values) take 8 us in three launches.
 //
 // The tensors' addresses travel as kernel arguments, kGradBatch tensors a launch; each is cut
 // into chunks of kGradChunk elements.  Squares are summed in 64 bits: a square of a large

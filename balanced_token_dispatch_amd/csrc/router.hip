@@ -6,8 +6,8 @@
 // experts), so of equal values the lowest expert is in the first chunk, lowest lane, first place.
 //
 // Latency-bound at small T, and by the K rounds of selection (a lane-local maximum, six data-parallel
-// steps across the wave, one ballot) at large: 4096 x 256 logits, K = 8, in 5 us, launch included,
-// where reading them takes 0.7 us.
+// steps across the wave, one ballot) at large: 4096 x 256 fp32 logits, K = 8, in 5.6 us, launch included,
+// where reading them takes 0.8 us; the gradient of 8192 x 384 bf16 logits (6.3 MB written) in 7.
 #include <type_traits>
 
 #include "common.hpp"

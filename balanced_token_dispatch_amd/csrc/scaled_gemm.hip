@@ -24,10 +24,14 @@ constexpr int kScMaxDim = 1 << 21;  // largest Kd and N (offsets within a tile s
 constexpr int kScMaxG = 1088;
 
 // ---- Few rows -----------------------------------------------------------------------------
-// 16 rows of one segment x 16 output columns per workgroup of W waves; wave w takes the blocks
+// 16 rows of one segment x 16 CT output columns per workgroup of W waves; wave w takes the blocks
 // kb = w, w + W, ... of the contraction, D of them in flight, straight from memory into
 // v_mfma_scale_f32_16x16x128 (every weight byte is used once per 16 rows, so staging it in LDS would
 // gain nothing), and the W sums are added in wave order through LDS.
+//
+// Bound by the weights' bytes: 512 rows on 264 experts of 7168 x 2048 read 3.27 GB in 535 us, 6.1 TB/s,
+// where torch's copy of 4 GiB moves 4.8 TB/s.  With few weights, by the launch and two trips to memory:
+// 6 rows on 6 experts of 2048 x 1408 (17 MB, 3 us at that rate) take 8.2 us.
 constexpr int kFewRows = 16, kFewCols = 16;
 
 // Segment table in LDS: sCu (clamped to [0, M_total]) and sStart[rho] = first tile of `tile`
@@ -169,6 +173,15 @@ __global__ __launch_bounds__(64 * W) void k_scaled_few(
 // in v_mfma_scale_f32_32x32x64 blocks.  A stage is 128 of the contraction (one scale block): whole
 // 128-byte lines of each operand's rows, loaded straight into LDS (buffer_load .. lds), in a ring of
 // R stages.
+//
+// What bounds it.  32768 rows on 264 experts of 7168 x 2048 (4.24 GB) take 821 us, 5.2 TB/s: memory.
+// With one expert (32768 x 7168 x 2048, 256 x 256 tiles) 395 us, 2.44 PFLOP/s, where torch's library
+// product takes 309 us (3.11 PFLOP/s) and the bare matrix instructions reach 4.7-5.0: the chip holds
+// 1.80 GHz there, the matrix units are busy 62% of the cycles and a wave waits 16%; the same kernel
+// without its loads would take 304 us, with loads that all hit L2 345.  Between them, with 1408 of
+// contraction (24576 rows, 68 experts, 128 x 256 tiles: 112 us, floor 56), what costs is the tiles' last
+// rows (15% more than the rows there are), the last round of tiles (8 for 7.1) and 11 stages a tile
+// against one start of the ring and one store of the results.
 constexpr int kTileThreads = 256, kTileWaves = 4;
 // Scales come in pieces of 16 stages: 16 bytes of each of the tile's rows and then of its column
 // blocks, in three buffers in turn (a tile's last piece may be too short a time to fetch the next

@@ -27,9 +27,9 @@
  *
  * Conventions shared by every entry point
  *   - Every pointer argument is DEVICE memory owned by the caller, except
- *     `dims` and the tables of moe_grad_sumsq / moe_grad_clip (host).  The library allocates nothing; its only state is a
- *     per-device cache of device properties and the static per-GPU scratch of
- *     moe_plan_noalloc.  Calls only enqueue work on `stream` (0 = the null
+ *     `dims` and the tables of moe_grad_sumsq / moe_grad_clip (host).  The
+ *     library allocates nothing; its only state is a per-device cache of
+ *     device properties and the static per-GPU scratch of moe_plan_noalloc.  Calls only enqueue work on `stream` (0 = the null
  *     stream) and never synchronise with the host.
  *   - Host-side argument checks run before anything is enqueued and return
  *     MOE_EINVAL / MOE_ENOSPACE with nothing launched.  MOE_EHIP reports a
@@ -383,9 +383,9 @@ moe_status_t moe_replica_grad_fold(const moe_dims *dims, int32_t rank, const int
  * scale; a NaN stays NaN, an infinity becomes NaN in e4m3.
  *   Rows of scales hold one byte for each 128 columns, and are
  * moe_scale_row_bytes(columns) = 16 ceil(columns / 2048) bytes long; bytes
- * past the last block are written 127 and never used.  A last block of fewer than 128 columns
- * has a scale of its own.  The pages name no 8-bit path; block scales are the
- * usual framework variant of the expert GEMMs.
+ * past the last block are written 127 and never used.  A last block of fewer
+ * than 128 columns has a scale of its own.  The pages name no 8-bit path;
+ * block scales are the usual framework variant of the expert GEMMs.
  * ------------------------------------------------------------------------- */
 size_t moe_scale_row_bytes(int64_t columns);
 
@@ -402,7 +402,8 @@ size_t moe_scale_row_bytes(int64_t columns);
  *   copy  nullable, [rows, width] of dtype: the same rows unquantised (rounded
  *         once where weighted), as moe_permute writes them, for the weight
  *         gradient.
- *   width % 16 == 0, 16 <= width <= 2^22; x, q, scale, copy 16-byte aligned.
+ *   width % 16 == 0, 16 <= width <= 2^22; x, q, scale, copy 16-byte aligned;
+ *   the outputs overlap neither each other nor an input.
  * ------------------------------------------------------------------------- */
 moe_status_t moe_quant_rows(moe_dtype dtype, moe_fp8 fmt, int64_t rows, int64_t width,
                             const void *x, int64_t src_rows, const int32_t *gather,
@@ -417,7 +418,7 @@ moe_status_t moe_quant_rows(moe_dtype dtype, moe_fp8 fmt, int64_t rows, int64_t 
  *   w        [G, Kd, N] of dtype (bf16 or fp32).
  *   q        [G, Kd, N],  q_scale  [G, ceil(Kd/128), moe_scale_row_bytes(N)].
  *   qt       [G, N, Kd],  qt_scale [G, ceil(N/128), moe_scale_row_bytes(Kd)].
- *   Kd % 16 == 0, N % 16 == 0, both <= 2^22; all 16-byte aligned.
+ *   Kd % 16 == 0, N % 16 == 0, both <= 2^22; all 16-byte aligned, no overlap.
  * ------------------------------------------------------------------------- */
 moe_status_t moe_quant_weight(moe_dtype dtype, int32_t G, int32_t Kd, int32_t N, const void *w,
                               void *q, void *q_scale, void *qt, void *qt_scale,
@@ -484,8 +485,9 @@ moe_status_t moe_router_backward(moe_dtype dtype, moe_score score, int64_t T, in
  * moe_grad_clip -- outs[i] = grads[i] * min(1, max_norm / (sqrt(*sumsq) + 1e-6))
  * (fp32 product, one rounding), and *norm = sqrt(*sumsq) (norm may be NULL).
  * outs[i] has the type and size of grads[i] and is grads[i] itself or does not
- * overlap any tensor; no tensor is listed twice.  A tensor clipped in place is left alone where the
- * factor is 1.  A NaN sum gives NaN gradients.  max_norm >= 0.
+ * overlap any tensor; no tensor is listed twice.  A tensor clipped in place is
+ * left alone where the factor is 1.  A NaN sum gives NaN gradients.
+ * max_norm >= 0.
  * ------------------------------------------------------------------------- */
 size_t moe_grad_sumsq_workspace_bytes(void);
 moe_status_t moe_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,
