@@ -269,6 +269,13 @@ def _take(dev, name, t, dtypes, numel):
     raise MoeError(f"{name}: shape {tuple(t.shape)}, expected {numel} elements")
 
 
+def _int32(**sizes):
+    """Refuses sizes that the C interface's 32-bit arguments would wrap around."""
+    for name, v in sizes.items():
+        if not 0 <= v < 1 << 31:
+            raise MoeError(f"{name}: {v}, expected a number of 0 to 2^31 - 1")
+
+
 def scale_row_bytes(columns):
     """Bytes of one row of scales over `columns` columns."""
     return (columns + 2047) // 2048 * 16
@@ -292,6 +299,7 @@ def moe_quant_rows(x, q, scale, gather=None, gather_div=1, row_scale=None, copy=
         if row_scale.numel() < (rows if gather is None else src_rows * gather_div):
             raise MoeError("row_scale: fewer entries than rows (or gather entries) to weight")
     cp = None if copy is None else _take(dev, "copy", copy, (x.dtype,), rows * width)
+    _int32(gather_div=gather_div)
     _check(_lib.moe_quant_rows(_FLOATS[x.dtype], _FP8[q.dtype], rows, width, xp, src_rows, gp,
                                gather_div, wp, qp, sp, cp, _stream(stream)), "moe_quant_rows")
 
@@ -303,6 +311,7 @@ def moe_quant_weight(w, q=None, q_scale=None, qt=None, qt_scale=None, stream=Non
         raise MoeError(f"moe_quant_weight: w has {w.dim()} dimensions, expected 3")
     dev = _current("w", w)
     G, Kd, N = w.shape
+    _int32(G=G, Kd=Kd, N=N)
     e4 = (torch.float8_e4m3fn,)
     p = [None if t is None else _take(dev, n, t, d, c) for n, t, d, c in (
         ("q", q, e4, G * Kd * N), ("q_scale", q_scale, _SCALE, G * -(-Kd // 128) * scale_row_bytes(N)),
@@ -317,6 +326,7 @@ def moe_group_gemm_scaled(op, a, a_scale, b, b_scale, cu_seqlens, out, Kd, N, st
     dev = _current("a", a)
     G, M = cu_seqlens.numel() - 1, a.shape[0]
     K, C = (Kd, N) if op == GEMM_FWD else (N, Kd)
+    _int32(rows=M, Kd=Kd, N=N)
     ap = _take(dev, "a", a, _FP8, M * K)
     asp = _take(dev, "a_scale", a_scale, _SCALE, M * scale_row_bytes(K))
     bp = _take(dev, "b", b, (torch.float8_e4m3fn,), G * K * C)
@@ -342,6 +352,7 @@ def moe_router_topk(logits, topk_idx, topk_w, score="softmax_topk", bias=None, f
     dev = _current("logits", logits)
     T, E = logits.shape
     K = topk_idx.shape[-1]
+    _int32(experts=E, K=K)
     bp = None if bias is None else _take(dev, "bias", bias, (torch.float32,), E)
     _check(_lib.moe_router_topk(_dtype(logits), _score(score), T, E, K,
                                 _take(dev, "logits", logits, _FLOATS, None), bp, factor,
@@ -358,6 +369,7 @@ def moe_router_backward(logits, topk_idx, dtopk_w, dlogits, score="softmax_topk"
     dev = _current("logits", logits)
     T, E = logits.shape
     K = topk_idx.shape[-1]
+    _int32(experts=E, K=K)
     _check(_lib.moe_router_backward(_dtype(logits), _score(score), T, E, K,
                                     _take(dev, "logits", logits, _FLOATS, None),
                                     _take(dev, "topk_idx", topk_idx, (torch.int32,), T * K),

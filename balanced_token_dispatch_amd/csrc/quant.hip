@@ -296,9 +296,10 @@ extern "C" moe_status_t moe_quant_rows(moe_dtype dtype, moe_fp8 fmt, int64_t row
   if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_EINVAL;
   if (fmt != MOE_E4M3 && fmt != MOE_E5M2) return MOE_EINVAL;
   if (rows < 0 || rows >= (1LL << 31) || width < 16 || width % 16 || width > kMaxWidth) return MOE_EINVAL;
-  if (src_rows < 1 || src_rows >= (1LL << 31) || gather_div < 1) return MOE_EINVAL;
+  if (src_rows < 0 || src_rows >= (1LL << 31) || gather_div < 1) return MOE_EINVAL;
   if (!gather && rows > src_rows) return MOE_EINVAL;
   if (rows == 0) return MOE_OK;
+  if (src_rows == 0) return MOE_EINVAL;
   if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale) || !aligned16(copy) ||
       (uintptr_t)gather % 4 || (uintptr_t)row_scale % 4)
     return MOE_EINVAL;

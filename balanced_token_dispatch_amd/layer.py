@@ -163,6 +163,7 @@ class LayerStep:
         self.out = torch.zeros((s.S, s.H), **act)
         if self.scaled:
             self.q_up, self.q_down = QuantWeights(self.w_up), QuantWeights(self.w_down)
+            self.weights_quantised = False
             e4 = torch.float8_e4m3fn
             self.xq, self.zq = QuantRows(s.SK, s.H, e4, device), QuantRows(s.SK, s.Hp, e4, device)
         self.backward_enabled = backward
@@ -210,9 +211,12 @@ class LayerStep:
     def quantise_weights(self):
         """The home experts' weights into 8 bits (gemm="scaled"): after every change of w_up or w_down.
         The slots' rows follow by the step's prefetch."""
+        if not self.scaled:
+            raise ValueError("quantise_weights: the layer's GEMMs are not in 8 bits")
         E = self.s.E
         for w, qw in ((self.w_up, self.q_up), (self.w_down, self.q_down)):
             moe_quant_weight(w[:E], *(t[:E] for t in qw.tensors()))
+        self.weights_quantised = True
 
     def route(self, logits, score="softmax_topk", bias=None, factor=1.0):
         """This rank's expert ids and router weights (its rows of topk_idx and topk_w) from its gate's
@@ -246,6 +250,8 @@ class LayerStep:
 
     def forward(self, timer=None):
         s, r, c = self.s, self.rank, self._call
+        if self.scaled and not self.weights_quantised:
+            raise ValueError("forward: quantise_weights() has not put the weights into 8 bits yet")
         if self.plan_noalloc:
             c(timer, "plan", moe_plan_noalloc, self.d, self.topk_idx, self.counts, self.plan,
               self.status)

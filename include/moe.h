@@ -397,7 +397,7 @@ size_t moe_scale_row_bytes(int64_t columns);
  * gather entry, or by the row where there is no gather) each value is first
  * multiplied by it in fp32.
  *   x     [src_rows, width] of dtype (bf16 or fp32); without gather
- *         src_rows >= rows.
+ *         src_rows >= rows; src_rows 0 only where rows is 0.
  *   q     [rows, width] bytes, scale [rows, moe_scale_row_bytes(width)].
  *   copy  nullable, [rows, width] of dtype: the same rows unquantised (rounded
  *         once where weighted), as moe_permute writes them, for the weight

@@ -331,3 +331,23 @@ def test_weights_over_32_bits(m):
 
     for big, alone in zip(quantise(w), quantise(w[G - 1:])):
         assert torch.equal(big.view(torch.uint8)[G - 1:], alone.view(torch.uint8))
+
+
+def test_sizes_past_32_bits_are_refused(m):
+    """A size that would wrap around in a 32-bit argument: an error, nothing written."""
+    x = torch.randn(4, 64, device="cuda")
+    g = torch.zeros(4, dtype=torch.int32, device="cuda")
+    q = torch.full((4, 64), 7, dtype=torch.uint8, device="cuda")
+    s = torch.full((4, 16), 9, dtype=torch.uint8, device="cuda")
+    with pytest.raises(m.MoeError, match="gather_div"):
+        m.moe_quant_rows(x, q.view(FP8["e4m3"]), s, gather=g, gather_div=(1 << 32) + 1)
+    a = torch.empty((0, 64), dtype=torch.uint8, device="cuda").view(FP8["e4m3"])
+    with pytest.raises(m.MoeError):
+        m.moe_group_gemm_scaled(m.GEMM_FWD, a, s[:0], q.view(FP8["e4m3"]), s, g[:2],
+                                torch.empty((0, 4), dtype=torch.bfloat16, device="cuda"), (1 << 32) + 64, 4)
+    assert (q == 7).all() and (s == 9).all()
+
+
+def test_no_rows_and_no_source(m):
+    e = torch.empty((0, 64), device="cuda")
+    m.moe_quant_rows(e, e.to(FP8["e4m3"]), torch.empty((0, 16), dtype=torch.uint8, device="cuda"))

@@ -237,3 +237,12 @@ def test_refusals():
         m.moe_quant_rows(L.x_all, L.zq.q, L.xq.scale)
     with pytest.raises(m.MoeError):
         m.moe_group_gemm_scaled(m.GEMM_WGRAD, L.xq.q, L.xq.scale, L.q_up.qt, L.q_up.qt_scale, L.cu, L.z, H, Hp)
+
+
+def test_refuses_weights_not_quantised():
+    from balanced_token_dispatch_amd.layer import LayerStep, Shape
+    L = LayerStep(Shape(R, S, K, E, B, H, Hp), rank=RANK, gemm="scaled")
+    with pytest.raises(ValueError, match="quantise_weights"):
+        L.forward()
+    with pytest.raises(ValueError, match="8 bits"):
+        LayerStep(Shape(R, S, K, E, B, H, Hp), rank=RANK).quantise_weights()

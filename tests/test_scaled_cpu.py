@@ -112,6 +112,7 @@ def test_quant_rows_refuses(mod):
                dict(a8=BYTE)):
         assert refused(fn, ok, **kw) == bad, kw
     assert refused(fn, ok, a2=0) == mod.MOE_OK
+    assert refused(fn, ok, a2=0, a4=None, a5=0) == mod.MOE_OK   # a rank without tokens
 
 
 def test_quant_weight_refuses(mod):
