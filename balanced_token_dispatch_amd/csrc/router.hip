@@ -1,13 +1,11 @@
 // moe_router_topk, moe_router_backward: the K experts of each token and their weights from the
 // gate's logits, and the logits' gradient from the weights'.
 //
-// One wave per token.  Expert e sits in chunk c = e / (64 P), lane e / P % 64, place e % P of the lane
-// (P = 4, 16 bytes of fp32 a lane, so that a row moves as contiguous vectors; P = 1 up to 64
-// experts), so of equal values the lowest expert is in the first chunk, lowest lane, first place.
+// Forward, several tokens share a wave (16 lanes each up to 256 experts); backward, one wave has a token.
 //
-// Latency-bound at small T, and by the K rounds of selection (a lane-local maximum, six data-parallel
-// steps across the wave, one ballot) at large: 4096 x 256 fp32 logits, K = 8, in 5.6 us, launch included,
-// where reading them takes 0.8 us; the gradient of 8192 x 384 bf16 logits (6.3 MB written) in 7.
+// Latency-bound at small T (one token of 256 experts, K = 8: 3.8 us, launch included), and by the K rounds of
+// selection at large: 4096 x 256 fp32 logits 5.5 us where reading them takes 0.8, 65536 x 256 27 us where
+// it takes 11.  The gradient of 8192 x 384 bf16 logits (6.3 MB written) takes 7 us.
 #include <type_traits>
 
 #include "common.hpp"
@@ -23,6 +21,7 @@ template <int CTRL, int ROWS>
 __device__ inline uint32_t dpp_step(uint32_t keep, uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)keep, (int)v, CTRL, ROWS, 0xF, false);
 }
+constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;
 constexpr int kShr1 = 0x111, kShr2 = 0x112, kShr4 = 0x114, kShr8 = 0x118, kBcast15 = 0x142, kBcast31 = 0x143;
 
 __device__ inline uint32_t wave_max(uint32_t v) {
@@ -46,12 +45,6 @@ __device__ inline float wave_sum(float v) {
   return at((uint32_t)__builtin_amdgcn_readlane((int)__builtin_bit_cast(uint32_t, v), 63));
 }
 
-__device__ inline double wave_sum(double v) {
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) v += __shfl_xor(v, off, kWave);
-  return v;
-}
-
 // Keys whose unsigned order is the values' order: -0 and 0 are equal, a NaN is above all.
 // No key is 0 (0 marks a taken expert).
 __device__ inline uint32_t order_key(float v) {
@@ -68,18 +61,6 @@ __device__ inline unsigned long long order_key(double v) {
 // The value of a key of fp32 order (the largest logit, from its key).
 __device__ inline float key_value(uint32_t k) {
   return __builtin_bit_cast(float, k & 0x80000000u ? k ^ 0x80000000u : ~k);
-}
-
-__device__ inline uint32_t wave_max_hi(unsigned long long v, uint32_t *lo) {
-  // the high words' maximum, then the low words' among the lanes that have it
-  const uint32_t hi = wave_max((uint32_t)(v >> 32));
-  *lo = wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-  return hi;
-}
-__device__ inline unsigned long long wave_max(unsigned long long v) {
-  uint32_t lo;
-  const uint32_t hi = wave_max_hi(v, &lo);
-  return (unsigned long long)hi << 32 | lo;
 }
 
 template <bool BF16>
@@ -130,29 +111,85 @@ __device__ inline void load_row(const void *p, long long i, int E, bool vec, flo
 // 1 / (1 + exp(-x)); exp's overflow to infinity gives the right zero
 __device__ inline float logistic(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-template <int C, int P, bool BF16, int SCORE, bool BIAS>
+// Maximum and sum over the L lanes of a token, the same in all of them: rotations within 16 lanes,
+// then rows and halves of the wave swapped.
+template <int L>
+__device__ inline uint32_t token_max(uint32_t v) {
+  v = max(v, dpp_step<kRor8, 0xF>(v, v));
+  v = max(v, dpp_step<kRor4, 0xF>(v, v));
+  v = max(v, dpp_step<kRor2, 0xF>(v, v));
+  v = max(v, dpp_step<kRor1, 0xF>(v, v));
+  if (L >= 32) {
+    const auto w = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(w[0], w[1]);
+  }
+  if (L >= 64) {
+    const auto w = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(w[0], w[1]);
+  }
+  return v;
+}
+template <int L>
+__device__ inline unsigned long long token_max(unsigned long long v) {
+  // the high words' maximum, then the low words' among the lanes that have it
+  const uint32_t hi = token_max<L>((uint32_t)(v >> 32));
+  return (unsigned long long)hi << 32 | token_max<L>((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+}
+template <int L, class T>
+__device__ inline T token_sum(T v) {
+#pragma unroll
+  for (int off = 1; off < L; off <<= 1) v += __shfl_xor(v, off, kWave);
+  return v;
+}
+
+// L lanes per token, V = 4 G consecutive experts each, so that of equal values the lowest expert is in
+// the lowest lane, first place.  The keys lie in LDS, and a lane keeps the largest of each group of 4:
+// a round of the selection is a maximum over those and over the token's lanes, and only the lane that
+// has it goes back to the 4 keys of one group.  (Keys all in registers, looked through by every lane
+// each round, took 2 to 3 times as long: one token per wave, 43 us at 65536 x 256.)
+template <int L, int V, bool BF16, int SCORE, bool BIAS>
 __global__ __launch_bounds__(kRtThreads) void k_router_topk(
     const void *__restrict__ logits, const float *__restrict__ bias, int32_t *__restrict__ idx,
     float *__restrict__ w, long long T, int E, int K, float factor, int vec) {
-  constexpr int V = C * P;
+  constexpr int G = V / 4, kTokens = kWave / L;  // tokens per wave
   using Key = std::conditional_t<BIAS, unsigned long long, uint32_t>;
-  const int lane = threadIdx.x & 63;
+  typedef __attribute__((ext_vector_type(4))) Key Keys;
+  __shared__ Keys keys[kRtThreads][G];
+  __shared__ uint16_t chosen[kRtThreads * V];
+  const int lane = threadIdx.x & 63, l = lane % L, e0 = l * V;
   const float ninf = -__builtin_inff();
-  const long long waves = (long long)gridDim.x * (kRtThreads / kWave);
-  for (long long t = (long long)blockIdx.x * (kRtThreads / kWave) + (threadIdx.x >> 6); t < T;
-       t += waves) {
+  Keys *own = keys[threadIdx.x];
+  uint16_t *list = chosen + (threadIdx.x - l) * V;
+  for (long long t0 = ((long long)blockIdx.x * kRtThreads + (threadIdx.x & ~63)) / L; t0 < T;
+       t0 += (long long)gridDim.x * (kRtThreads / L)) {
+    const long long t = t0 + lane / L;
     float x[V];
-    Key key[V];
-    int rank[V];
-    load_row<C, P, BF16>(logits, t * E, E, vec, x);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int e = e0 + 4 * g;
+      float *v = x + 4 * g;
+      if (vec && t < T && e < E) {
+        if constexpr (BF16) {
+          const uint2 q = *(const uint2 *)((const uint16_t *)logits + t * E + e);
+          v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
+        } else {
+          const f32x4 q = *(const f32x4 *)((const float *)logits + t * E + e);
+          v[0] = q[0], v[1] = q[1], v[2] = q[2], v[3] = q[3];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = t < T && e + j < E ? load_logit<BF16>(logits, t * E + e + j) : ninf;
+      }
+    }
     float top = ninf;  // of all experts
     if (SCORE == MOE_SCORE_SOFTMAX) {
       uint32_t k = 0;
 #pragma unroll
       for (int j = 0; j < V; ++j) k = max(k, x[j] == x[j] ? order_key(x[j]) : 0u);
-      k = wave_max(k);
+      k = token_max<L>(k);
       top = k ? key_value(k) : ninf;
     }
+    Key most_of[G];
     if constexpr (BIAS) {
       // selection by score + bias: near ties decide which experts run, so in 64 bits
       double s[V], sum = 0.0;
@@ -162,68 +199,91 @@ __global__ __launch_bounds__(kRtThreads) void k_router_topk(
         if (SCORE == MOE_SCORE_SIGMOID) s[j] = 1.0 / (1.0 + exp(-s[j]));
         if (SCORE == MOE_SCORE_SOFTMAX) sum += s[j] = exp(s[j] - (double)top);
       }
-      if (SCORE == MOE_SCORE_SOFTMAX) sum = wave_sum(sum);
+      if (SCORE == MOE_SCORE_SOFTMAX) sum = token_sum<L>(sum);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = expert_of<P>(lane, j);
-        if (SCORE == MOE_SCORE_SOFTMAX) s[j] /= sum;
-        key[j] = e < E ? order_key(s[j] + (double)bias[e]) : 0;
-        rank[j] = -1;
+      for (int g = 0; g < G; ++g) {
+        Keys k;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          double v = s[4 * g + j];
+          if (SCORE == MOE_SCORE_SOFTMAX) v /= sum;
+          k[j] = e0 + 4 * g + j < E ? order_key(v + (double)bias[e0 + 4 * g + j]) : 0;
+        }
+        own[g] = k;
+        most_of[g] = max(max(k[0], k[1]), max(k[2], k[3]));
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) key[j] = expert_of<P>(lane, j) < E ? order_key(x[j]) : 0, rank[j] = -1;
-    }
-    for (int r = 0; r < K; ++r) {
-      Key best = 0;
+      for (int g = 0; g < G; ++g) {
+        Keys k;
 #pragma unroll
-      for (int j = 0; j < V; ++j) best = max(best, key[j]);
-      const Key most = wave_max(best);
-      // the first chunk that has it, its lowest lane, that lane's first place
-      bool open = true;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        bool here = false;
-#pragma unroll
-        for (int j = 0; j < P; ++j) here |= key[c * P + j] == most;
-        const unsigned long long who = __ballot(open && here);
-        if (open && who) {
-          open = false;
-          bool mine = lane == __ffsll(who) - 1;
-#pragma unroll
-          for (int j = 0; j < P; ++j)
-            if (mine && key[c * P + j] == most) key[c * P + j] = 0, rank[c * P + j] = r, mine = false;
-        }
+        for (int j = 0; j < 4; ++j) k[j] = e0 + 4 * g + j < E ? order_key(x[4 * g + j]) : 0;
+        own[g] = k;
+        most_of[g] = max(max(k[0], k[1]), max(k[2], k[3]));
       }
     }
+    float sum = 0.0f;
+    if (SCORE == MOE_SCORE_SOFTMAX) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum += e0 + j < E && x[j] != ninf ? expf(x[j] - top) : 0.0f;
+      sum = token_sum<L>(sum);
+    }
+    for (int r = 0; r < K; ++r) {
+      Key best = most_of[0];
+#pragma unroll
+      for (int g = 1; g < G; ++g) best = max(best, most_of[g]);
+      const Key most = token_max<L>(best);
+      const unsigned long long who = __ballot(best == most) >> (lane - l);
+      if (l == __ffsll(who) - 1) {  // the token's lowest lane that has it
+        int g = 0;
+#pragma unroll
+        for (int i = G - 1; i > 0; --i) g = most_of[i] == most ? i : g;
+        if (G > 1) g = most_of[0] == most ? 0 : g;
+        Keys k = own[g];
+        int p = 3;
+#pragma unroll
+        for (int j = 2; j >= 0; --j) p = k[j] == most ? j : p;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = j == p ? 0 : k[j];
+        own[g] = k;
+        const Key rest = max(max(k[0], k[1]), max(k[2], k[3]));
+#pragma unroll
+        for (int i = 0; i < G; ++i) most_of[i] = i == g ? rest : most_of[i];
+        list[r] = (uint16_t)(e0 + 4 * g + p);
+      }
+    }
+    asm volatile("" ::: "memory");  // the list is read by other lanes of this wave, after its writes
     // weights of the chosen: score / sum, 0 where the sum is 0
-    float m = top, sum = 0.0f, s[V];
+    float m = top;
+    auto logit = [&](int r) { return t < T && r < K ? load_logit<BF16>(logits, t * E + list[r]) : ninf; };
     if (SCORE == MOE_SCORE_SOFTMAX_TOPK) {
       uint32_t k = 0;
-#pragma unroll
-      for (int j = 0; j < V; ++j) k = max(k, rank[j] >= 0 && x[j] == x[j] ? order_key(x[j]) : 0u);
-      k = wave_max(k);
+      for (int r = l; r < K; r += L) {
+        const float c = logit(r);
+        k = max(k, c == c ? order_key(c) : 0u);
+      }
+      k = token_max<L>(k);
       m = k ? key_value(k) : ninf;
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const bool in = SCORE == MOE_SCORE_SOFTMAX ? expert_of<P>(lane, j) < E : rank[j] >= 0;
-      s[j] = SCORE == MOE_SCORE_SIGMOID ? logistic(x[j]) : x[j] == ninf ? 0.0f : expf(x[j] - m);
-      sum += in ? s[j] : 0.0f;
+    auto score = [&](float c) {
+      return SCORE == MOE_SCORE_SIGMOID ? logistic(c) : c == ninf ? 0.0f : expf(c - m);
+    };
+    if (SCORE != MOE_SCORE_SOFTMAX) {
+      for (int r = l; r < K; r += L) sum += score(logit(r));
+      sum = token_sum<L>(sum);
     }
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (rank[j] >= 0) {
-        idx[t * K + rank[j]] = expert_of<P>(lane, j);
-        w[t * K + rank[j]] = sum == 0.0f ? 0.0f : factor * (s[j] / sum);
+    for (int r = l; r < K; r += L)
+      if (t < T) {
+        idx[t * K + r] = list[r];
+        w[t * K + r] = sum == 0.0f ? 0.0f : factor * (score(logit(r)) / sum);
       }
   }
 }
 
-// dlogits of one token per wave.  Each chosen entry's gradient is worked out by one lane, 64
-// entries at a time, and added in entry order into the lanes that hold the experts (the same
-// expert twice adds twice).
+// dlogits of one token per wave.  Expert e sits in chunk c = e / (64 P), lane e / P % 64, place e % P of the
+// lane (P = 4, 16 bytes of fp32 a lane, so that a row moves as contiguous vectors; P = 1 up to 64 experts).
+// Each chosen entry's gradient is worked out by one lane, 64 entries at a time, and added in entry order
+// into the lanes that hold the experts (the same expert twice adds twice).
 template <int C, int P, bool BF16, int SCORE>
 __global__ __launch_bounds__(kRtThreads) void k_router_bwd(
     const void *__restrict__ logits, const int32_t *__restrict__ idx,
@@ -327,29 +387,34 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(
   }
 }
 
-template <int C, int P, bool BF16, int SCORE>
+template <int L, int V, bool BF16, int SCORE>
 static void launch_topk(dim3 grid, hipStream_t stream, const void *logits, const float *bias,
                         int32_t *idx, float *w, int64_t T, int E, int K, float factor, int vec) {
   if (bias)
-    hipLaunchKernelGGL((k_router_topk<C, P, BF16, SCORE, true>), grid, dim3(kRtThreads), 0, stream,
+    hipLaunchKernelGGL((k_router_topk<L, V, BF16, SCORE, true>), grid, dim3(kRtThreads), 0, stream,
                        logits, bias, idx, w, T, E, K, factor, vec);
   else
-    hipLaunchKernelGGL((k_router_topk<C, P, BF16, SCORE, false>), grid, dim3(kRtThreads), 0, stream,
+    hipLaunchKernelGGL((k_router_topk<L, V, BF16, SCORE, false>), grid, dim3(kRtThreads), 0, stream,
                        logits, bias, idx, w, T, E, K, factor, vec);
 }
 
-template <int C, int P, bool BF16>
-struct Router {
-  static void topk(int score, dim3 grid, hipStream_t stream, const void *logits, const float *bias,
-                   int32_t *idx, float *w, int64_t T, int E, int K, float factor, int vec) {
+template <int L_, int V, bool BF16>
+struct TopK {
+  static constexpr int L = L_;
+  static void run(int score, dim3 grid, hipStream_t stream, const void *logits, const float *bias,
+                  int32_t *idx, float *w, int64_t T, int E, int K, float factor, int vec) {
     if (score == MOE_SCORE_SOFTMAX_TOPK)
-      launch_topk<C, P, BF16, MOE_SCORE_SOFTMAX_TOPK>(grid, stream, logits, bias, idx, w, T, E, K, factor, vec);
+      launch_topk<L, V, BF16, MOE_SCORE_SOFTMAX_TOPK>(grid, stream, logits, bias, idx, w, T, E, K, factor, vec);
     else if (score == MOE_SCORE_SOFTMAX)
-      launch_topk<C, P, BF16, MOE_SCORE_SOFTMAX>(grid, stream, logits, bias, idx, w, T, E, K, factor, vec);
+      launch_topk<L, V, BF16, MOE_SCORE_SOFTMAX>(grid, stream, logits, bias, idx, w, T, E, K, factor, vec);
     else
-      launch_topk<C, P, BF16, MOE_SCORE_SIGMOID>(grid, stream, logits, bias, idx, w, T, E, K, factor, vec);
+      launch_topk<L, V, BF16, MOE_SCORE_SIGMOID>(grid, stream, logits, bias, idx, w, T, E, K, factor, vec);
   }
-  static void bwd(int score, dim3 grid, hipStream_t stream, const void *logits, const int32_t *idx,
+};
+
+template <int C, int P, bool BF16>
+struct Backward {
+  static void run(int score, dim3 grid, hipStream_t stream, const void *logits, const int32_t *idx,
                   const float *dw, void *dlogits, int64_t T, int E, int K, float factor, int vec) {
     if (score == MOE_SCORE_SOFTMAX_TOPK)
       hipLaunchKernelGGL((k_router_bwd<C, P, BF16, MOE_SCORE_SOFTMAX_TOPK>), grid, dim3(kRtThreads), 0,
@@ -363,13 +428,29 @@ struct Router {
   }
 };
 
+// Lanes and experts per lane.  Few lanes share the wave's instructions among more tokens; all 64 make a
+// token's own time shortest, which is what counts while there are not two tokens for each SIMD.  Fp32, K = 8,
+// us a launch (16 lanes / 64 lanes): 1 x 256 5.0 / 3.8, 1024 x 256 5.5 / 4.4, 4096 x 256 5.5 / 5.8,
+// 65536 x 256 27 / 44; 65536 x 64, K = 6, 12 / 39.
+template <bool BF16, class F>
+static void with_topk(int E, int64_t T, F f) {
+  const bool few = T <= 8LL * device_cu_count();
+  if (E <= 64) f(TopK<16, 4, BF16>{});
+  else if (E <= 128 && !few) f(TopK<16, 8, BF16>{});
+  else if (E <= 256 && !few) f(TopK<16, 16, BF16>{});
+  else if (E <= 256) f(TopK<64, 4, BF16>{});
+  else if (E <= 512 && !few) f(TopK<32, 16, BF16>{});
+  else if (E <= 512) f(TopK<64, 8, BF16>{});
+  else f(TopK<64, 16, BF16>{});
+}
+
 // The fewest values per lane that hold E experts.
-template <class F>
-static void with_shape(int E, bool bf16, F f) {
-  if (E <= 64) bf16 ? f(Router<1, 1, true>{}) : f(Router<1, 1, false>{});
-  else if (E <= 256) bf16 ? f(Router<1, 4, true>{}) : f(Router<1, 4, false>{});
-  else if (E <= 512) bf16 ? f(Router<2, 4, true>{}) : f(Router<2, 4, false>{});
-  else bf16 ? f(Router<4, 4, true>{}) : f(Router<4, 4, false>{});
+template <bool BF16, class F>
+static void with_backward(int E, F f) {
+  if (E <= 64) f(Backward<1, 1, BF16>{});
+  else if (E <= 256) f(Backward<1, 4, BF16>{});
+  else if (E <= 512) f(Backward<2, 4, BF16>{});
+  else f(Backward<4, 4, BF16>{});
 }
 
 // Whether every row of p can be read and written as vectors of 4 values.
@@ -388,8 +469,9 @@ static bool router_args_ok(moe_dtype dtype, moe_score score, int64_t T, int32_t 
 
 static bool misaligned(const void *p, size_t n) { return (uintptr_t)p % n != 0; }
 
-static dim3 router_grid(int64_t T) {
-  const int64_t b = (T + kRtThreads / kWave - 1) / (kRtThreads / kWave);
+// Workgroups for T tokens of `lanes` lanes.
+static dim3 router_grid(int64_t T, int lanes) {
+  const int64_t per = kRtThreads / lanes, b = (T + per - 1) / per;
   return dim3((unsigned)(b < (1 << 22) ? b : (1 << 22)));
 }
 
@@ -407,10 +489,11 @@ extern "C" moe_status_t moe_router_topk(moe_dtype dtype, moe_score score, int64_
   if (misaligned(logits, dtype == MOE_BF16 ? 2 : 4) || misaligned(bias, 4) || misaligned(topk_idx, 4) ||
       misaligned(topk_w, 4))
     return MOE_EINVAL;
-  with_shape(E, dtype == MOE_BF16, [&](auto r) {
-    r.topk(score, router_grid(T), stream, logits, bias, topk_idx, topk_w, T, E, K, factor,
-           rows_of_4(dtype, E, logits));
-  });
+  auto launch = [&](auto k) {
+    k.run(score, router_grid(T, k.L), stream, logits, bias, topk_idx, topk_w, T, E, K, factor,
+          rows_of_4(dtype, E, logits));
+  };
+  dtype == MOE_BF16 ? with_topk<true>(E, T, launch) : with_topk<false>(E, T, launch);
   return launch_status();
 }
 
@@ -425,9 +508,10 @@ extern "C" moe_status_t moe_router_backward(moe_dtype dtype, moe_score score, in
   if (misaligned(logits, size) || misaligned(dlogits, size) || misaligned(topk_idx, 4) ||
       misaligned(dtopk_w, 4))
     return MOE_EINVAL;
-  with_shape(E, dtype == MOE_BF16, [&](auto r) {
-    r.bwd(score, router_grid(T), stream, logits, topk_idx, dtopk_w, dlogits, T, E, K, factor,
+  auto launch = [&](auto k) {
+    k.run(score, router_grid(T, kWave), stream, logits, topk_idx, dtopk_w, dlogits, T, E, K, factor,
           rows_of_4(dtype, E, logits) && rows_of_4(dtype, E, dlogits));
-  });
+  };
+  dtype == MOE_BF16 ? with_backward<true>(E, launch) : with_backward<false>(E, launch);
   return launch_status();
 }

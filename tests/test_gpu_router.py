@@ -89,6 +89,41 @@ def test_topk_masked(m, score, E):
     assert (np.abs(w - ww) <= weight_tol(finite, E) * ww + 2.0 ** -126).all()
 
 
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("E,K", [(3, 3), (64, 5), (65, 8), (128, 8), (130, 130), (251, 8), (256, 16), (300, 8), (512, 12),
+                                 (513, 70), (1024, 8)])
+def test_topk_many_tokens(m, score, E, K, bias):
+    """More tokens than any device's 8 per compute unit, not a multiple of a wave's: normal rows between
+    masked, equal, tied, NaN and infinite ones, which share waves with them."""
+    r = np.random.default_rng(E + K)
+    x = r.standard_normal((37, E)).astype(np.float32)
+    x[:, ::5] = np.round(x[:, ::5] * 2) / 2
+    x[3] = -np.inf
+    x[8] = 0.25
+    x[11, ::2] = -np.inf
+    x[17, E // 2] = np.nan
+    x[20] = np.finfo(np.float32).min
+    T = 8209
+    rows = np.arange(T) % 37
+    b = r.standard_normal(E).astype(np.float32) if bias else None
+    keep = np.ones(37, bool)
+    if bias and score == "softmax":
+        keep[[3, 17]] = False   # scores of NaN over all experts: no order to compare
+    idx, w = topk(m, torch.from_numpy(x[rows]).cuda(), K, score, b)
+    assert (idx.min(1) >= 0).all() and (idx.max(1) < E).all()
+    k = keep[rows]
+    assert np.array_equal(idx[k], idx[:37][rows][k]) and np.array_equal(w[k], w[:37][rows][k], equal_nan=True)
+    widx, ww = ref.router_topk(x[keep].astype(np.float64), K, score, b)
+    assert np.array_equal(idx[:37][keep], widx)
+    finite = np.where(np.abs(x) < 1e30, x, 0.0).astype(np.float64)
+    finite[np.isnan(x)] = 0.0
+    got = w[:37][keep]
+    assert np.array_equal(np.isnan(got), np.isnan(ww))
+    ok = ~np.isnan(ww)
+    assert (np.abs(got - ww)[ok] <= (weight_tol(finite, E) * ww + 2.0 ** -126)[ok]).all()
+
+
 def test_topk_nan_first(m):
     x = np.zeros((2, 70), np.float32)
     x[0, 65] = np.nan
