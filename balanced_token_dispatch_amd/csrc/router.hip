@@ -1,7 +1,7 @@
 // moe_router_topk, moe_router_backward: the K experts of each token and their weights from the
 // gate's logits, and the logits' gradient from the weights'.
 //
-// Forward, several tokens share a wave (16 lanes each up to 256 experts); backward, one wave has a token.
+// Several tokens share a wave (16 lanes each up to 256 experts) where there are enough of them.
 //
 // Latency-bound at small T (one token of 256 experts, K = 8: 3.8 us, launch included), and by the K rounds of
 // selection at large: 4096 x 256 fp32 logits 5.5 us where reading them takes 0.8, 65536 x 256 27 us where
@@ -15,36 +15,12 @@ namespace moe {
 constexpr int kRtThreads = 256;
 constexpr int kRtMaxE = 1024;
 
-// Wave-wide maximum and sum without LDS: each step combines a lane with one a power of two away (row
-// shifts within 16 lanes, then the last lane of a row into the next rows); lane 63 ends with all.
-template <int CTRL, int ROWS>
-__device__ inline uint32_t dpp_step(uint32_t keep, uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)keep, (int)v, CTRL, ROWS, 0xF, false);
+// The value of the lane N places on, around a row of 16 lanes.
+template <int CTRL>
+__device__ inline uint32_t rotated(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
 }
 constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;
-constexpr int kShr1 = 0x111, kShr2 = 0x112, kShr4 = 0x114, kShr8 = 0x118, kBcast15 = 0x142, kBcast31 = 0x143;
-
-__device__ inline uint32_t wave_max(uint32_t v) {
-  v = max(v, dpp_step<kShr1, 0xF>(0, v));
-  v = max(v, dpp_step<kShr2, 0xF>(0, v));
-  v = max(v, dpp_step<kShr4, 0xF>(0, v));
-  v = max(v, dpp_step<kShr8, 0xF>(0, v));
-  v = max(v, dpp_step<kBcast15, 0xA>(0, v));
-  v = max(v, dpp_step<kBcast31, 0xC>(0, v));
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-
-__device__ inline float wave_sum(float v) {
-  auto at = [](uint32_t x) { return __builtin_bit_cast(float, x); };
-  v += at(dpp_step<kShr1, 0xF>(0, __builtin_bit_cast(uint32_t, v)));
-  v += at(dpp_step<kShr2, 0xF>(0, __builtin_bit_cast(uint32_t, v)));
-  v += at(dpp_step<kShr4, 0xF>(0, __builtin_bit_cast(uint32_t, v)));
-  v += at(dpp_step<kShr8, 0xF>(0, __builtin_bit_cast(uint32_t, v)));
-  v += at(dpp_step<kBcast15, 0xA>(0, __builtin_bit_cast(uint32_t, v)));
-  v += at(dpp_step<kBcast31, 0xC>(0, __builtin_bit_cast(uint32_t, v)));
-  return at((uint32_t)__builtin_amdgcn_readlane((int)__builtin_bit_cast(uint32_t, v), 63));
-}
-
 // Keys whose unsigned order is the values' order: -0 and 0 are equal, a NaN is above all.
 // No key is 0 (0 marks a taken expert).
 __device__ inline uint32_t order_key(float v) {
@@ -71,43 +47,6 @@ __device__ inline float load_logit(const void *p, long long i) {
     return ((const float *)p)[i];
 }
 
-// Where lane `lane` holds place v of its C P values.
-template <int P>
-__device__ inline int expert_of(int lane, int v) {
-  return v / P * (64 * P) + lane * P + v % P;
-}
-
-// This lane's values of the row that starts at element i, -inf past E.  vec: whole rows are aligned to
-// a lane's 4 values and E is a multiple of them.
-template <int C, int P, bool BF16>
-__device__ inline void load_row(const void *p, long long i, int E, bool vec, float (&x)[C * P]) {
-  const int lane = threadIdx.x & 63;
-  const float ninf = -__builtin_inff();
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int e = expert_of<P>(lane, c * P);
-    if (P == 4 && vec) {
-      if (e >= E) {
-#pragma unroll
-        for (int j = 0; j < P; ++j) x[c * P + j] = ninf;
-      } else if constexpr (BF16) {
-        const uint2 t = *(const uint2 *)((const uint16_t *)p + i + e);
-        x[c * P] = bf16_lo(t.x);
-        x[c * P + 1 % P] = bf16_hi(t.x);
-        x[c * P + 2 % P] = bf16_lo(t.y);
-        x[c * P + 3 % P] = bf16_hi(t.y);
-      } else {
-        const f32x4 t = *(const f32x4 *)((const float *)p + i + e);
-#pragma unroll
-        for (int j = 0; j < P; ++j) x[c * P + j] = t[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < P; ++j) x[c * P + j] = e + j < E ? load_logit<BF16>(p, i + e + j) : ninf;
-    }
-  }
-}
-
 // 1 / (1 + exp(-x)); exp's overflow to infinity gives the right zero
 __device__ inline float logistic(float x) { return 1.0f / (1.0f + expf(-x)); }
 
@@ -115,10 +54,10 @@ __device__ inline float logistic(float x) { return 1.0f / (1.0f + expf(-x)); }
 // then rows and halves of the wave swapped.
 template <int L>
 __device__ inline uint32_t token_max(uint32_t v) {
-  v = max(v, dpp_step<kRor8, 0xF>(v, v));
-  v = max(v, dpp_step<kRor4, 0xF>(v, v));
-  v = max(v, dpp_step<kRor2, 0xF>(v, v));
-  v = max(v, dpp_step<kRor1, 0xF>(v, v));
+  v = max(v, rotated<kRor8>(v));
+  v = max(v, rotated<kRor4>(v));
+  v = max(v, rotated<kRor2>(v));
+  v = max(v, rotated<kRor1>(v));
   if (L >= 32) {
     const auto w = __builtin_amdgcn_permlane16_swap(v, v, false, false);
     v = max(w[0], w[1]);
@@ -135,10 +74,49 @@ __device__ inline unsigned long long token_max(unsigned long long v) {
   const uint32_t hi = token_max<L>((uint32_t)(v >> 32));
   return (unsigned long long)hi << 32 | token_max<L>((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
 }
-template <int L, class T>
-__device__ inline T token_sum(T v) {
+template <int L>
+__device__ inline float token_sum(float v) {
+  auto at = [](uint32_t x) { return __builtin_bit_cast(float, x); };
+  v += at(rotated<kRor8>(__builtin_bit_cast(uint32_t, v)));
+  v += at(rotated<kRor4>(__builtin_bit_cast(uint32_t, v)));
+  v += at(rotated<kRor2>(__builtin_bit_cast(uint32_t, v)));
+  v += at(rotated<kRor1>(__builtin_bit_cast(uint32_t, v)));
+  if (L >= 32) {
+    const auto w = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = at(w[0]) + at(w[1]);
+  }
+  if (L >= 64) {
+    const auto w = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = at(w[0]) + at(w[1]);
+  }
+  return v;
+}
+template <int L>
+__device__ inline double token_sum(double v) {
 #pragma unroll
   for (int off = 1; off < L; off <<= 1) v += __shfl_xor(v, off, kWave);
+  return v;
+}
+
+// 4 logits from element i, of which n are in the row (the others: -inf).  vec: the row is aligned to 4 values
+// and n is 4 or at most 0.
+template <bool BF16>
+__device__ inline f32x4 load_4(const void *p, long long i, int n, bool vec) {
+  const float ninf = -__builtin_inff();
+  f32x4 v = {ninf, ninf, ninf, ninf};
+  if (vec) {
+    if (n <= 0) return v;
+    if constexpr (BF16) {
+      const uint2 q = *(const uint2 *)((const uint16_t *)p + i);
+      v = (f32x4){bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+    } else {
+      v = *(const f32x4 *)((const float *)p + i);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) v[j] = load_logit<BF16>(p, i + j);
+  }
   return v;
 }
 
@@ -166,20 +144,9 @@ __global__ __launch_bounds__(kRtThreads) void k_router_topk(
     float x[V];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const int e = e0 + 4 * g;
-      float *v = x + 4 * g;
-      if (vec && t < T && e < E) {
-        if constexpr (BF16) {
-          const uint2 q = *(const uint2 *)((const uint16_t *)logits + t * E + e);
-          v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
-        } else {
-          const f32x4 q = *(const f32x4 *)((const float *)logits + t * E + e);
-          v[0] = q[0], v[1] = q[1], v[2] = q[2], v[3] = q[3];
-        }
-      } else {
+      const f32x4 q = load_4<BF16>(logits, t * E + e0 + 4 * g, t < T ? E - e0 - 4 * g : 0, vec);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = t < T && e + j < E ? load_logit<BF16>(logits, t * E + e + j) : ninf;
-      }
+      for (int j = 0; j < 4; ++j) x[4 * g + j] = q[j];
     }
     float top = ninf;  // of all experts
     if (SCORE == MOE_SCORE_SOFTMAX) {
@@ -280,43 +247,53 @@ __global__ __launch_bounds__(kRtThreads) void k_router_topk(
   }
 }
 
-// dlogits of one token per wave.  Expert e sits in chunk c = e / (64 P), lane e / P % 64, place e % P of the
-// lane (P = 4, 16 bytes of fp32 a lane, so that a row moves as contiguous vectors; P = 1 up to 64 experts).
-// Each chosen entry's gradient is worked out by one lane, 64 entries at a time, and added in entry order
-// into the lanes that hold the experts (the same expert twice adds twice).
-template <int C, int P, bool BF16, int SCORE>
+// dlogits, L lanes per token and V = 4 G experts each: group i of lane l starts at expert 4 (l + L i), so
+// that a row moves as contiguous vectors.  The row is put together in LDS: first what every expert gets,
+// then each chosen entry's gradient, worked out by one lane, L entries at a time.  Entries of the same
+// expert are added by the first of them, in their order.  (One token per wave, every lane looking for its
+// experts among the entries, took 27 us at 65536 x 64 and 35 at 65536 x 256.)
+template <int L, int V, bool BF16, int SCORE>
 __global__ __launch_bounds__(kRtThreads) void k_router_bwd(
     const void *__restrict__ logits, const int32_t *__restrict__ idx,
     const float *__restrict__ dw, void *__restrict__ dlogits, long long T, int E, int K,
     float factor, int vec) {
-  constexpr int V = C * P;
-  const int lane = threadIdx.x & 63;
-  const long long waves = (long long)gridDim.x * (kRtThreads / kWave);
+  constexpr int G = V / 4;
+  __shared__ f32x4 rows[kRtThreads * G];
+  const int lane = threadIdx.x & 63, l = lane % L;
+  f32x4 *row = rows + (threadIdx.x - l) * G;
+  float *at = (float *)row;
   const float ninf = -__builtin_inff();
   auto largest = [&](float a, float b) { return b > a ? b : a; };  // of numbers; a NaN passes by
-  for (long long t = (long long)blockIdx.x * (kRtThreads / kWave) + (threadIdx.x >> 6); t < T;
-       t += waves) {
-    float x[V];
+  for (long long t0 = ((long long)blockIdx.x * kRtThreads + (threadIdx.x & ~63)) / L; t0 < T;
+       t0 += (long long)gridDim.x * (kRtThreads / L)) {
+    const long long t = t0 + lane / L;
     float m = ninf, sum = 0.0f, inner = 0.0f;
     auto all_lanes = [&]() {
-      const uint32_t k = wave_max(m == ninf ? 0u : order_key(m));
+      const uint32_t k = token_max<L>(m == ninf ? 0u : order_key(m));
       m = k ? key_value(k) : ninf;
     };
+    f32x4 x[G];
     if (SCORE == MOE_SCORE_SOFTMAX) {
-      load_row<C, P, BF16>(logits, t * E, E, vec, x);
 #pragma unroll
-      for (int j = 0; j < V; ++j) m = largest(m, x[j]);
+      for (int i = 0; i < G; ++i) {
+        const int e = 4 * (l + L * i);
+        x[i] = load_4<BF16>(logits, t * E + e, t < T ? E - e : 0, vec);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = largest(m, x[i][j]);
+      }
       all_lanes();
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        x[j] = x[j] == ninf ? 0.0f : expf(x[j] - m);
-        sum += x[j];
-      }
+      for (int i = 0; i < G; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[i][j] = x[i][j] == ninf ? 0.0f : expf(x[i][j] - m);
+          sum += x[i][j];
+        }
     }
     // entry r of this token: its expert (-1: none), logit and weight's gradient
     auto entry = [&](int r, int &e, float &c, float &d) {
       e = -1, c = ninf, d = 0.0f;
-      if (r < K) {
+      if (t < T && r < K) {
         e = idx[t * K + r];
         if (e < 0 || e >= E) e = -1;
         if (e >= 0) c = load_logit<BF16>(logits, t * E + e), d = factor * dw[t * K + r];
@@ -325,26 +302,31 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(
     int e;
     float c, d;
     if (SCORE == MOE_SCORE_SOFTMAX_TOPK) {
-      for (int r = lane; r < K; r += kWave) entry(r, e, c, d), m = largest(m, c);
+      for (int r = l; r < K; r += L) entry(r, e, c, d), m = largest(m, c);
       all_lanes();
     }
     auto score = [&](float v) {
       return SCORE == MOE_SCORE_SIGMOID ? logistic(v) : v == ninf ? 0.0f : expf(v - m);
     };
-    for (int r = lane; r < K; r += kWave) {
+    for (int r = l; r < K; r += L) {
       entry(r, e, c, d);
       const float s = score(c);
       if (SCORE != MOE_SCORE_SOFTMAX) sum += e >= 0 ? s : 0.0f;
       inner += d * s;
     }
-    sum = wave_sum(sum);
+    sum = token_sum<L>(sum);
     const float rs = sum == 0.0f ? 0.0f : 1.0f / sum;
-    inner = wave_sum(inner) * rs;
-    float out[V];
+    inner = token_sum<L>(inner) * rs;
 #pragma unroll
-    for (int j = 0; j < V; ++j) out[j] = SCORE == MOE_SCORE_SOFTMAX ? -inner * (x[j] * rs) : 0.0f;
-    for (int r0 = 0; r0 < K; r0 += kWave) {
-      entry(r0 + lane, e, c, d);
+    for (int i = 0; i < G; ++i) {
+      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (SCORE == MOE_SCORE_SOFTMAX)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = -inner * (x[i][j] * rs);
+      row[l + L * i] = v;
+    }
+    for (int r0 = 0; r0 < K; r0 += L) {
+      entry(r0 + l, e, c, d);
       const float wgt = score(c) * rs;
       float gr = 0.0f;
       if (e >= 0) {
@@ -352,36 +334,41 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(
         if (SCORE == MOE_SCORE_SOFTMAX_TOPK) gr = wgt * (d - inner);
         if (SCORE == MOE_SCORE_SIGMOID) gr = wgt * (d - inner) / (1.0f + expf(c));
       }
-      for (int r = 0; r < min(K - r0, kWave); ++r) {
-        const int er = __builtin_amdgcn_readlane(e, r);
-        const float g = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, gr), r));
-#pragma unroll
-        for (int j = 0; j < V; ++j) out[j] += er == expert_of<P>(lane, j) ? g : 0.0f;
+      float total = 0.0f;
+      bool first = e >= 0;
+      for (int r = 0; r < min(K - r0, L); ++r) {
+        const int er = __shfl(e, lane - l + r, kWave);
+        const float g = __shfl(gr, lane - l + r, kWave);
+        total += er == e ? g : 0.0f;
+        first = first && (er != e || r >= l);
       }
+      asm volatile("" ::: "memory");  // the row's entries were written by other lanes of this wave
+      if (first) at[e] += total;
     }
+    asm volatile("" ::: "memory");
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int n = expert_of<P>(lane, c * P);
-      if (P == 4 && vec) {
-        if (n >= E) continue;
+    for (int i = 0; i < G; ++i) {
+      const int n = 4 * (l + L * i);
+      if (t >= T || n >= E) continue;
+      const f32x4 v = row[l + L * i];
+      if (vec) {
         if constexpr (BF16) {
           uint2 o;
-          o.x = pack_bf16x2(out[c * P], out[c * P + 1 % P]);
-          o.y = pack_bf16x2(out[c * P + 2 % P], out[c * P + 3 % P]);
+          o.x = pack_bf16x2(v[0], v[1]);
+          o.y = pack_bf16x2(v[2], v[3]);
           *(uint2 *)((uint16_t *)dlogits + t * E + n) = o;
         } else {
-          *(f32x4 *)((float *)dlogits + t * E + n) =
-              (f32x4){out[c * P], out[c * P + 1 % P], out[c * P + 2 % P], out[c * P + 3 % P]};
+          *(f32x4 *)((float *)dlogits + t * E + n) = v;
         }
         continue;
       }
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
+      for (int j = 0; j < 4; ++j) {
         if (n + j >= E) continue;
         if constexpr (BF16)
-          ((uint16_t *)dlogits)[t * E + n + j] = (uint16_t)pack_bf16x2(out[c * P + j], 0.0f);
+          ((uint16_t *)dlogits)[t * E + n + j] = (uint16_t)pack_bf16x2(v[j], 0.0f);
         else
-          ((float *)dlogits)[t * E + n + j] = out[c * P + j];
+          ((float *)dlogits)[t * E + n + j] = v[j];
       }
     }
   }
@@ -399,10 +386,10 @@ static void launch_topk(dim3 grid, hipStream_t stream, const void *logits, const
 }
 
 template <int L_, int V, bool BF16>
-struct TopK {
+struct Router {
   static constexpr int L = L_;
-  static void run(int score, dim3 grid, hipStream_t stream, const void *logits, const float *bias,
-                  int32_t *idx, float *w, int64_t T, int E, int K, float factor, int vec) {
+  static void topk(int score, dim3 grid, hipStream_t stream, const void *logits, const float *bias,
+                   int32_t *idx, float *w, int64_t T, int E, int K, float factor, int vec) {
     if (score == MOE_SCORE_SOFTMAX_TOPK)
       launch_topk<L, V, BF16, MOE_SCORE_SOFTMAX_TOPK>(grid, stream, logits, bias, idx, w, T, E, K, factor, vec);
     else if (score == MOE_SCORE_SOFTMAX)
@@ -410,47 +397,34 @@ struct TopK {
     else
       launch_topk<L, V, BF16, MOE_SCORE_SIGMOID>(grid, stream, logits, bias, idx, w, T, E, K, factor, vec);
   }
-};
-
-template <int C, int P, bool BF16>
-struct Backward {
-  static void run(int score, dim3 grid, hipStream_t stream, const void *logits, const int32_t *idx,
-                  const float *dw, void *dlogits, int64_t T, int E, int K, float factor, int vec) {
+  static void backward(int score, dim3 grid, hipStream_t stream, const void *logits, const int32_t *idx,
+                       const float *dw, void *dlogits, int64_t T, int E, int K, float factor, int vec) {
     if (score == MOE_SCORE_SOFTMAX_TOPK)
-      hipLaunchKernelGGL((k_router_bwd<C, P, BF16, MOE_SCORE_SOFTMAX_TOPK>), grid, dim3(kRtThreads), 0,
+      hipLaunchKernelGGL((k_router_bwd<L, V, BF16, MOE_SCORE_SOFTMAX_TOPK>), grid, dim3(kRtThreads), 0,
                          stream, logits, idx, dw, dlogits, T, E, K, factor, vec);
     else if (score == MOE_SCORE_SOFTMAX)
-      hipLaunchKernelGGL((k_router_bwd<C, P, BF16, MOE_SCORE_SOFTMAX>), grid, dim3(kRtThreads), 0,
+      hipLaunchKernelGGL((k_router_bwd<L, V, BF16, MOE_SCORE_SOFTMAX>), grid, dim3(kRtThreads), 0,
                          stream, logits, idx, dw, dlogits, T, E, K, factor, vec);
     else
-      hipLaunchKernelGGL((k_router_bwd<C, P, BF16, MOE_SCORE_SIGMOID>), grid, dim3(kRtThreads), 0,
+      hipLaunchKernelGGL((k_router_bwd<L, V, BF16, MOE_SCORE_SIGMOID>), grid, dim3(kRtThreads), 0,
                          stream, logits, idx, dw, dlogits, T, E, K, factor, vec);
   }
 };
 
 // Lanes and experts per lane.  Few lanes share the wave's instructions among more tokens; all 64 make a
-// token's own time shortest, which is what counts while there are not two tokens for each SIMD.  Fp32, K = 8,
-// us a launch (16 lanes / 64 lanes): 1 x 256 5.0 / 3.8, 1024 x 256 5.5 / 4.4, 4096 x 256 5.5 / 5.8,
-// 65536 x 256 27 / 44; 65536 x 64, K = 6, 12 / 39.
+// token's own time shortest, which is what counts while there are not two tokens for each SIMD.
+// moe_router_topk of fp32 logits, K = 8, us a launch (16 lanes / 64 lanes): 1 x 256 5.0 / 3.8, 1024 x 256
+// 5.5 / 4.4, 4096 x 256 5.5 / 5.8, 65536 x 256 27 / 44; 65536 x 64, K = 6, 12 / 39.
 template <bool BF16, class F>
-static void with_topk(int E, int64_t T, F f) {
+static void with_shape(int E, int64_t T, F f) {
   const bool few = T <= 8LL * device_cu_count();
-  if (E <= 64) f(TopK<16, 4, BF16>{});
-  else if (E <= 128 && !few) f(TopK<16, 8, BF16>{});
-  else if (E <= 256 && !few) f(TopK<16, 16, BF16>{});
-  else if (E <= 256) f(TopK<64, 4, BF16>{});
-  else if (E <= 512 && !few) f(TopK<32, 16, BF16>{});
-  else if (E <= 512) f(TopK<64, 8, BF16>{});
-  else f(TopK<64, 16, BF16>{});
-}
-
-// The fewest values per lane that hold E experts.
-template <bool BF16, class F>
-static void with_backward(int E, F f) {
-  if (E <= 64) f(Backward<1, 1, BF16>{});
-  else if (E <= 256) f(Backward<1, 4, BF16>{});
-  else if (E <= 512) f(Backward<2, 4, BF16>{});
-  else f(Backward<4, 4, BF16>{});
+  if (E <= 64) f(Router<16, 4, BF16>{});
+  else if (E <= 128 && !few) f(Router<16, 8, BF16>{});
+  else if (E <= 256 && !few) f(Router<16, 16, BF16>{});
+  else if (E <= 256) f(Router<64, 4, BF16>{});
+  else if (E <= 512 && !few) f(Router<32, 16, BF16>{});
+  else if (E <= 512) f(Router<64, 8, BF16>{});
+  else f(Router<64, 16, BF16>{});
 }
 
 // Whether every row of p can be read and written as vectors of 4 values.
@@ -489,11 +463,11 @@ extern "C" moe_status_t moe_router_topk(moe_dtype dtype, moe_score score, int64_
   if (misaligned(logits, dtype == MOE_BF16 ? 2 : 4) || misaligned(bias, 4) || misaligned(topk_idx, 4) ||
       misaligned(topk_w, 4))
     return MOE_EINVAL;
-  auto launch = [&](auto k) {
-    k.run(score, router_grid(T, k.L), stream, logits, bias, topk_idx, topk_w, T, E, K, factor,
+  auto launch = [&](auto r) {
+    r.topk(score, router_grid(T, r.L), stream, logits, bias, topk_idx, topk_w, T, E, K, factor,
           rows_of_4(dtype, E, logits));
   };
-  dtype == MOE_BF16 ? with_topk<true>(E, T, launch) : with_topk<false>(E, T, launch);
+  dtype == MOE_BF16 ? with_shape<true>(E, T, launch) : with_shape<false>(E, T, launch);
   return launch_status();
 }
 
@@ -508,10 +482,10 @@ extern "C" moe_status_t moe_router_backward(moe_dtype dtype, moe_score score, in
   if (misaligned(logits, size) || misaligned(dlogits, size) || misaligned(topk_idx, 4) ||
       misaligned(dtopk_w, 4))
     return MOE_EINVAL;
-  auto launch = [&](auto k) {
-    k.run(score, router_grid(T, kWave), stream, logits, topk_idx, dtopk_w, dlogits, T, E, K, factor,
+  auto launch = [&](auto r) {
+    r.backward(score, router_grid(T, r.L), stream, logits, topk_idx, dtopk_w, dlogits, T, E, K, factor,
           rows_of_4(dtype, E, logits) && rows_of_4(dtype, E, dlogits));
   };
-  dtype == MOE_BF16 ? with_backward<true>(E, launch) : with_backward<false>(E, launch);
+  dtype == MOE_BF16 ? with_shape<true>(E, T, launch) : with_shape<false>(E, T, launch);
   return launch_status();
 }

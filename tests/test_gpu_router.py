@@ -162,6 +162,33 @@ def test_backward(m, score, T, E, K, dtype):
     assert grad_close(run_backward(m, x, idx, dw, score, 1.5), want, xd, dw, 1.5, dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("E,K", [(3, 3), (64, 5), (65, 8), (128, 20), (130, 130), (251, 8), (256, 16), (300, 40), (512, 12),
+                                 (513, 70), (1024, 8)])
+def test_backward_many_tokens(m, score, E, K, dtype):
+    """More tokens than any device's 8 per compute unit: masked rows, ids twice and more and outside the
+    experts, among rows that share their waves."""
+    r = np.random.default_rng(E * K)
+    x = torch.from_numpy(r.standard_normal((37, E)).astype(np.float32)).to(dtype)
+    x[3] = -float("inf")
+    x[11, ::2] = -float("inf")
+    xd = x.double().numpy()
+    idx, _ = ref.router_topk(xd, K, score)
+    idx[5, :] = idx[5, 0]
+    idx[6, ::2] = idx[6, 0]
+    idx[7, 1:] = E
+    idx[8] = -1
+    idx[9, K - 1] = idx[9, 0]
+    dw = r.standard_normal((37, K)).astype(np.float32)
+    rows = np.arange(8209) % 37
+    d = run_backward(m, x[torch.from_numpy(rows)].cuda(), idx[rows], dw[rows], score, 1.5)
+    first = d[:37]
+    assert torch.equal(d, first[torch.from_numpy(rows).cuda()])   # finite, and the same in every wave
+    want = ref.router_backward(xd, idx, dw, score, 1.5)
+    assert grad_close(first, want, np.where(np.isfinite(xd), xd, 0.0), dw, 1.5, dtype)
+
+
 @pytest.mark.parametrize("score", SCORES)
 def test_backward_odd_ids(m, score):
     """Ids outside the experts, the same id twice, rows with no valid id, masked logits."""
