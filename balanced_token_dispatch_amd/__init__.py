@@ -269,11 +269,15 @@ def _take(dev, name, t, dtypes, numel):
     raise MoeError(f"{name}: shape {tuple(t.shape)}, expected {numel} elements")
 
 
-def _int32(**sizes):
+def _int32(*sizes):
     """Refuses sizes that the C interface's 32-bit arguments would wrap around."""
-    for name, v in sizes.items():
-        if not 0 <= v < 1 << 31:
-            raise MoeError(f"{name}: {v}, expected a number of 0 to 2^31 - 1")
+    if min(sizes) < 0 or max(sizes) >= 1 << 31:
+        raise MoeError(f"sizes {sizes}, expected numbers of 0 to 2^31 - 1")
+
+
+def _on(dev, stream):
+    """The handle of a stream, or of device dev's current one."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def scale_row_bytes(columns):
@@ -299,9 +303,9 @@ def moe_quant_rows(x, q, scale, gather=None, gather_div=1, row_scale=None, copy=
         if row_scale.numel() < (rows if gather is None else src_rows * gather_div):
             raise MoeError("row_scale: fewer entries than rows (or gather entries) to weight")
     cp = None if copy is None else _take(dev, "copy", copy, (x.dtype,), rows * width)
-    _int32(gather_div=gather_div)
+    _int32(gather_div, rows)
     _check(_lib.moe_quant_rows(_FLOATS[x.dtype], _FP8[q.dtype], rows, width, xp, src_rows, gp,
-                               gather_div, wp, qp, sp, cp, _stream(stream)), "moe_quant_rows")
+                               gather_div, wp, qp, sp, cp, _on(dev, stream)), "moe_quant_rows")
 
 
 def moe_quant_weight(w, q=None, q_scale=None, qt=None, qt_scale=None, stream=None):
@@ -311,13 +315,13 @@ def moe_quant_weight(w, q=None, q_scale=None, qt=None, qt_scale=None, stream=Non
         raise MoeError(f"moe_quant_weight: w has {w.dim()} dimensions, expected 3")
     dev = _current("w", w)
     G, Kd, N = w.shape
-    _int32(G=G, Kd=Kd, N=N)
+    _int32(G, Kd, N)
     e4 = (torch.float8_e4m3fn,)
     p = [None if t is None else _take(dev, n, t, d, c) for n, t, d, c in (
         ("q", q, e4, G * Kd * N), ("q_scale", q_scale, _SCALE, G * -(-Kd // 128) * scale_row_bytes(N)),
         ("qt", qt, e4, G * Kd * N), ("qt_scale", qt_scale, _SCALE, G * -(-N // 128) * scale_row_bytes(Kd)))]
     _check(_lib.moe_quant_weight(_dtype(w), G, Kd, N, _take(dev, "w", w, _FLOATS, None), *p,
-                                 _stream(stream)), "moe_quant_weight")
+                                 _on(dev, stream)), "moe_quant_weight")
 
 
 def moe_group_gemm_scaled(op, a, a_scale, b, b_scale, cu_seqlens, out, Kd, N, stream=None):
@@ -326,7 +330,7 @@ def moe_group_gemm_scaled(op, a, a_scale, b, b_scale, cu_seqlens, out, Kd, N, st
     dev = _current("a", a)
     G, M = cu_seqlens.numel() - 1, a.shape[0]
     K, C = (Kd, N) if op == GEMM_FWD else (N, Kd)
-    _int32(rows=M, Kd=Kd, N=N)
+    _int32(M, Kd, N)
     ap = _take(dev, "a", a, _FP8, M * K)
     asp = _take(dev, "a_scale", a_scale, _SCALE, M * scale_row_bytes(K))
     bp = _take(dev, "b", b, (torch.float8_e4m3fn,), G * K * C)
@@ -334,7 +338,7 @@ def moe_group_gemm_scaled(op, a, a_scale, b, b_scale, cu_seqlens, out, Kd, N, st
     cp = _take(dev, "cu_seqlens", cu_seqlens, (torch.int32,), None)
     op_ = _take(dev, "out", out, (torch.bfloat16,), M * C)
     _check(_lib.moe_group_gemm_scaled(op, _FP8[a.dtype], G, M, Kd, N, ap, asp, bp, bsp, cp,
-                                      op_, _stream(stream)),
+                                      op_, _on(dev, stream)),
            "moe_group_gemm_scaled")
 
 
@@ -352,13 +356,13 @@ def moe_router_topk(logits, topk_idx, topk_w, score="softmax_topk", bias=None, f
     dev = _current("logits", logits)
     T, E = logits.shape
     K = topk_idx.shape[-1]
-    _int32(experts=E, K=K)
+    _int32(E, K)
     bp = None if bias is None else _take(dev, "bias", bias, (torch.float32,), E)
     _check(_lib.moe_router_topk(_dtype(logits), _score(score), T, E, K,
                                 _take(dev, "logits", logits, _FLOATS, None), bp, factor,
                                 _take(dev, "topk_idx", topk_idx, (torch.int32,), T * K),
                                 _take(dev, "topk_w", topk_w, (torch.float32,), T * K),
-                                _stream(stream)), "moe_router_topk")
+                                _on(dev, stream)), "moe_router_topk")
 
 
 def moe_router_backward(logits, topk_idx, dtopk_w, dlogits, score="softmax_topk", factor=1.0,
@@ -369,13 +373,13 @@ def moe_router_backward(logits, topk_idx, dtopk_w, dlogits, score="softmax_topk"
     dev = _current("logits", logits)
     T, E = logits.shape
     K = topk_idx.shape[-1]
-    _int32(experts=E, K=K)
+    _int32(E, K)
     _check(_lib.moe_router_backward(_dtype(logits), _score(score), T, E, K,
                                     _take(dev, "logits", logits, _FLOATS, None),
                                     _take(dev, "topk_idx", topk_idx, (torch.int32,), T * K),
                                     _take(dev, "dtopk_w", dtopk_w, (torch.float32,), T * K), factor,
                                     _take(dev, "dlogits", dlogits, (logits.dtype,), T * E),
-                                    _stream(stream)), "moe_router_backward")
+                                    _on(dev, stream)), "moe_router_backward")
 
 
 def grad_sumsq_workspace_bytes():
@@ -407,7 +411,7 @@ def moe_grad_sumsq(grads, sumsq, ws, stream=None):
     _check(_lib.moe_grad_sumsq(len(grads), _at(ptr), _at(numel), _at(dt),
                                _take(dev, "sumsq", sumsq, (torch.float64,), 1),
                                _take(dev, "ws", ws, (ws.dtype,), None), ws.numel() * ws.element_size(),
-                               _stream(stream)), "moe_grad_sumsq")
+                               _on(dev, stream)), "moe_grad_sumsq")
 
 
 def moe_grad_clip(grads, sumsq, max_norm, norm=None, out=None, stream=None):
@@ -426,4 +430,4 @@ def moe_grad_clip(grads, sumsq, max_norm, norm=None, out=None, stream=None):
     np_ = None if norm is None else _take(dev, "norm", norm, (torch.float32,), 1)
     _check(_lib.moe_grad_clip(len(grads), _at(ptr), _at(numel), _at(dt),
                               _take(dev, "sumsq", sumsq, (torch.float64,), 1), max_norm, np_, _at(optr),
-                              _stream(stream)), "moe_grad_clip")
+                              _on(dev, stream)), "moe_grad_clip")
