@@ -25,6 +25,9 @@ are listed per function in the tests:
   scipy's logistic function, closed forms (silu(x) - silu(-x) = x), central
   differences of the forward, and a dense gated MoE written copy by copy.
 * ``bf16``: torch's CPU cast on sampled bit patterns.
+* ``scaled_ref`` (a module of its own: 8-bit blocks, the product on them, the router, the clipping): the 8-bit
+  formats against torch's casts over all bytes and on random values; the router and the clipping
+  against torch in float64; the router's gradient against central differences.
 
 Parity unpinned: any specific plan versus the original library's planner
 (the pages print none).
