@@ -16,6 +16,8 @@
 // own rounding to 8 bits (2^-4 of each value) that is nothing: 4e-5 of the result's norm on
 // operands of random bytes, where rounding the result to bf16 costs 1.7e-3.  It is why there is no
 // fp32 output here.
+#include <type_traits>
+
 #include "fp8.hpp"
 
 namespace moe {
@@ -500,15 +502,12 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
   Fragments<T> f[2], g[2];  // of sub-steps 0 and 1
 #pragma unroll
   for (int i = 0; i < (T::whole ? 2 : 1) * NF; ++i) f[i / NF].read(i % NF, ring, wi, wj, lane, i / NF);
-  // scale bytes of this lane's rows and of the wave's column block: stage q of the piece in buffer buf;
-  // mask 0 for a stage past the contraction, whose bytes may be anything (2^-127 times zeros)
-  auto scale_at = [&](int buf, int q, int row, int mask) {
-    return scales[buf * T::scale_bytes + row * 16 + q] & mask;
-  };
+  // scale bytes of this lane's rows and of the wave's column block: stage q of the piece in buffer buf
+  auto scale_at = [&](int buf, int q, int row) -> int { return scales[buf * T::scale_bytes + row * 16 + q]; };
   int sa[TM], sb, buf = 0;
 #pragma unroll
-  for (int i = 0; i < TM; ++i) sa[i] = scale_at(0, 0, wi + 32 * i + (lane & 31), 255);
-  sb = scale_at(0, 0, T::rows + (wj >> 7), 255);
+  for (int i = 0; i < TM; ++i) sa[i] = scale_at(0, 0, wi + 32 * i + (lane & 31));
+  sb = scale_at(0, 0, T::rows + (wj >> 7));
   int cur = 0;         // ring slot of stage s
   int settled = 1;     // 0: the stores of the tile before may be in flight
   for (;;) {
@@ -516,17 +515,18 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
 #pragma unroll
     for (int i = 0; i < NM; ++i) acc[i / TN][i % TN] = (f32x16){};
     if constexpr (T::whole) {
-      auto stage = [&](int s, Fragments<T> (&f)[2], Fragments<T> (&g)[2]) {
+      auto stage = [&](int s, Fragments<T> (&f)[2], Fragments<T> (&g)[2], auto inner) __attribute__((always_inline)) {
+        constexpr bool kInner = decltype(inner)::value;
         const int nxt = cur + 1 == R ? 0 : cur + 1;
         const uint8_t *ns = ring + nxt * T::stage;
         const int q = s % kScaleStages;
-        const bool turn = q == kScaleStages - 1 || s == nk - 1;
+        const bool turn = q == kScaleStages - 1 || (!kInner && s == nk - 1);
         const int nbuf = !turn ? buf : buf + 1 == kScaleBufs ? 0 : buf + 1, nq = turn ? 0 : q + 1;
-        const int mask = s == nk - 1 || s + 1 < kblocks ? 255 : 0;
-        const int ls = s + R < nk ? s + R : s + R - nk;
-        const Place &lp = s + R < nk ? at : next;
-        const __amdgpu_buffer_rsrc_t ra = buffer_of(lp.a, ls < kblocks ? lp.rows * K : 0);
-        const __amdgpu_buffer_rsrc_t rb = buffer_of(lp.b, ls < kblocks ? lp.cols * K : 0);
+        const int mask = kInner || s == nk - 1 || s + 1 < kblocks ? 255 : 0;  // as below
+        const int ls = kInner ? s + R : s + R - nk;
+        const Place &lp = kInner ? at : next;
+        const __amdgpu_buffer_rsrc_t ra = buffer_of(lp.a, kInner || ls < kblocks ? lp.rows * K : 0);
+        const __amdgpu_buffer_rsrc_t rb = buffer_of(lp.b, kInner || ls < kblocks ? lp.cols * K : 0);
         wait_loads_or<kAhead, T::stores>(s | settled);
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -534,8 +534,8 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
 #pragma unroll
         for (int j = 0; j < 2 * NF; ++j) g[j / NF].read(j % NF, ns, wi, wj, lane, j / NF);
 #pragma unroll
-        for (int j = 0; j < TM; ++j) na[j] = scale_at(nbuf, nq, wi + 32 * j + (lane & 31), mask);
-        const int nb = scale_at(nbuf, nq, T::rows + (wj >> 7), mask);
+        for (int j = 0; j < TM; ++j) na[j] = scale_at(nbuf, nq, wi + 32 * j + (lane & 31));
+        const int nb = scale_at(nbuf, nq, T::rows + (wj >> 7));
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 2 * NM; ++i) {
@@ -556,41 +556,54 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sa[i] = na[i];
-        sb = nb;
+        for (int i = 0; i < TM; ++i) sa[i] = na[i] & mask;
+        sb = nb & mask;
         buf = nbuf;
         cur = nxt;
       };
       int s = 0;
 #pragma clang loop unroll(disable)
+      for (; s + 1 + R < nk; s += 2) {
+        stage(s, f, g, std::true_type{});
+        stage(s + 1, g, f, std::true_type{});
+      }
+      if (s + R < nk) {
+        stage(s++, f, g, std::true_type{});
+#pragma unroll
+        for (int h = 0; h < 2; ++h) f[h] = g[h];
+      }
+#pragma clang loop unroll(disable)
       for (; s + 2 <= nk; s += 2) {
-        stage(s, f, g);
-        stage(s + 1, g, f);
+        stage(s, f, g, std::false_type{});
+        stage(s + 1, g, f, std::false_type{});
       }
       if (s < nk) {
-        stage(s, f, g);
+        stage(s, f, g, std::false_type{});
 #pragma unroll
         for (int h = 0; h < 2; ++h) f[h] = g[h];
       }
     } else {
-#pragma clang loop unroll(disable)
-    for (int s = 0; s < nk; ++s) {
+    // inner: the stages whose loads that run ahead are this tile's
+    auto stage = [&](int s, auto inner) __attribute__((always_inline)) {
+      constexpr bool kInner = decltype(inner)::value;
       const int nxt = cur + 1 == R ? 0 : cur + 1, prv = cur == 0 ? R - 1 : cur - 1;
       const uint8_t *cs = ring + cur * T::stage, *ns = ring + nxt * T::stage;
       int na[TM], nb = 0;
       const int q = s % kScaleStages;
       // the next piece: this tile's next 16 stages, or the next tile's first
-      const bool turn = q == kScaleStages - 1 || s == nk - 1;
+      const bool turn = q == kScaleStages - 1 || (!kInner && s == nk - 1);
       const int nbuf = !turn ? buf : buf + 1 == kScaleBufs ? 0 : buf + 1, nq = turn ? 0 : q + 1;
-      const int mask = s == nk - 1 || s + 1 < kblocks ? 255 : 0;
+      // 0 for a stage past the contraction, whose scale bytes may be anything (2^-127 times zeros).  Applied at
+      // the stage's end: next to the read it would wait for it, five times a stage
+      const int mask = kInner || s == nk - 1 || s + 1 < kblocks ? 255 : 0;
       // loads of stage s + R (b's of s + R - 1 where they are split): this tile's or, past its end,
-      // the next one's
-      const int as = s + R < nk ? s + R : s + R - nk;
-      const Place &ap = s + R < nk ? at : next;
-      const __amdgpu_buffer_rsrc_t ra = buffer_of(ap.a, as < kblocks ? ap.rows * K : 0);
-      const int bn = s + R - (kSplit ? 1 : 0), bs = bn < nk ? bn : bn - nk;
-      const Place &bp = bn < nk ? at : next;
-      const __amdgpu_buffer_rsrc_t rb = buffer_of(bp.b, bs < kblocks ? bp.cols * K : 0);
+      // the next one's.  (nk is more than the contraction's blocks only where it is R: no inner stages then.)
+      const int as = kInner ? s + R : s + R - nk;
+      const Place &ap = kInner ? at : next;
+      const __amdgpu_buffer_rsrc_t ra = buffer_of(ap.a, kInner || as < kblocks ? ap.rows * K : 0);
+      const int bn = s + R - (kSplit ? 1 : 0), bs = kInner || bn < nk ? bn : bn - nk;
+      const Place &bp = kInner || bn < nk ? at : next;
+      const __amdgpu_buffer_rsrc_t rb = buffer_of(bp.b, kInner || bs < kblocks ? bp.cols * K : 0);
       const uint32_t to_a = ring_lds + cur * T::stage, to_b = ring_lds + (kSplit ? prv : cur) * T::stage + T::a_bytes;
       __builtin_amdgcn_sched_barrier(0);
       Fetch fe;
@@ -603,8 +616,8 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
           if (j * H / NF == i % NM) f[1 - h].read(j, h ? ns : cs, wi, wj, lane, 1 - h);
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-          if (H + j * (NM - H) / TM == i) na[j] = scale_at(nbuf, nq, wi + 32 * j + (lane & 31), mask);
-        if (i == NM - 1) nb = scale_at(nbuf, nq, T::rows + (wj >> 7), mask);
+          if (H + j * (NM - H) / TM == i) na[j] = scale_at(nbuf, nq, wi + 32 * j + (lane & 31));
+        if (i == NM - 1) nb = scale_at(nbuf, nq, T::rows + (wj >> 7));
 #pragma unroll
         for (int u = 0; u < T::a_loads; ++u)
           if ((kSplit ? NM + u * NM / T::a_loads : kFree + u * kSpan / kAll) == i)
@@ -631,11 +644,16 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
 #pragma unroll
       for (int i = NM; i < 2 * NM; ++i) slot(i);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) sa[i] = na[i];
-      sb = nb;
+      for (int i = 0; i < TM; ++i) sa[i] = na[i] & mask;
+      sb = nb & mask;
       buf = nbuf;
       cur = nxt;
-    }
+    };
+    int s = 0;
+#pragma clang loop unroll(disable)
+    for (; s + R < nk; ++s) stage(s, std::true_type{});
+#pragma clang loop unroll(disable)
+    for (; s < nk; ++s) stage(s, std::false_type{});
     }
     tile_out<T>(acc, out + (long long)at.m0 * N + at.j0, N, at.rows, at.cols);
     __builtin_amdgcn_sched_barrier(0);
