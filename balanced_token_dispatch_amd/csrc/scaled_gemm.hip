@@ -425,13 +425,20 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
   // past the next tile; stages past the contraction load zeros.)
   //
   // A stage s is two sub-steps of TM TN matrix instructions; behind each the wave issues a few memory
-  // operations for later:
+  // operations for later.  R > 2:
   //   sub-step 0: reads the fragments of sub-step 1 and the scales of stage s + 1; issues b's loads of
-  //     stage s + R - 1 (R > 2); asks for the next piece of scales;
+  //     stage s + R - 1; asks for the next piece of scales;
   //   wait until only the loads of stages s + 2 .. s + R - 1 are in flight (stage s + 1 has landed),
   //   barrier (every wave has read all of stage s);
-  //   sub-step 1: reads the fragments of stage s + 1's sub-step 0; issues a's loads of stage s + R (and
-  //     b's, R = 2: a later issue would be waited for at once) into slot s % R.
+  //   sub-step 1: reads the fragments of stage s + 1's sub-step 0; issues a's loads of stage s + R into slot
+  //     s % R.
+  // R = 2 (kDeep), where a stage's slot has to be free early for its loads to have the time they need:
+  //   barrier (every wave has read all of stage s, both sub-steps, into registers);
+  //   sub-step 0: issues the first two thirds of the loads of stage s + 2 into slot s % 2;
+  //   wait until only those are in flight (stage s + 1 has landed), barrier;
+  //   sub-step 1: issues the other loads; reads all fragments and the scales of stage s + 1, those of its
+  //     sub-step 1 into registers that alternate from stage to stage; asks for the next piece of scales.
+  // (32768 x 1 x 7168 x 2048: 381 us; loads over one sub-step 403, over both 384.)
   // Loads and stores complete in order, so where the stores of the tile before came after the loads
   // waited for (stage 0), they are counted in; the loads of the scales only make a wait stricter.
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
@@ -441,12 +448,11 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
   const int kblocks = (K + kBlock - 1) / kBlock, nk = max(kblocks, R);
   constexpr int kAhead = (R - 2) * (T::a_loads + T::b_loads);
   constexpr int kAll = T::a_loads + T::b_loads;
-  // R > 2: b's loads go out in sub-step 0, one stage later than a's
-  constexpr bool kSplit = R > 2 && !T::whole;
-  // R = 2: the loads of stage s + 2 go out from the matrix instruction on before which another barrier
-  // frees the slot, evenly to the stage's end; kEarly of them before the wait
-  constexpr int kFree = H + 2, kSpan = T::whole ? 1 : 2 * NM - kFree;
-  constexpr int kEarly = T::whole || kSplit ? 0 : ((NM - kFree) * kAll + kSpan - 1) / kSpan;
+  constexpr bool kDeep = R == 2;
+  constexpr int kSpan = 3 * NM / 2;  // matrix instructions over which a stage's loads go out (kDeep)
+  static_assert(!(kDeep && T::whole), "whole stages need a ring of more than 2");
+  // b's loads go out in sub-step 0, one stage later than a's
+  constexpr bool kSplit = !kDeep && !T::whole;
   constexpr int kLoads = T::a_loads > T::b_loads ? T::a_loads : T::b_loads;
   const Offsets<kLoads> lo = offsets<kLoads>(K);
 
@@ -501,7 +507,7 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
   lds_barrier();
   Fragments<T> f[2], g[2];  // of sub-steps 0 and 1
 #pragma unroll
-  for (int i = 0; i < (T::whole ? 2 : 1) * NF; ++i) f[i / NF].read(i % NF, ring, wi, wj, lane, i / NF);
+  for (int i = 0; i < (kSplit ? 1 : 2) * NF; ++i) f[i / NF].read(i % NF, ring, wi, wj, lane, i / NF);
   // scale bytes of this lane's rows and of the wave's column block: stage q of the piece in buffer buf
   auto scale_at = [&](int buf, int q, int row) -> int { return scales[buf * T::scale_bytes + row * 16 + q]; };
   int sa[TM], sb, buf = 0;
@@ -583,8 +589,9 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
         for (int h = 0; h < 2; ++h) f[h] = g[h];
       }
     } else {
-    // inner: the stages whose loads that run ahead are this tile's
-    auto stage = [&](int s, auto inner) __attribute__((always_inline)) {
+    // inner: the stages whose loads that run ahead are this tile's.  f0, f1: the fragments of the sub-steps;
+    // to1: where the next stage's sub-step 1 goes.
+    auto stage = [&](int s, Fragments<T> &f0, Fragments<T> &f1, Fragments<T> &to1, auto inner) __attribute__((always_inline)) {
       constexpr bool kInner = decltype(inner)::value;
       const int nxt = cur + 1 == R ? 0 : cur + 1, prv = cur == 0 ? R - 1 : cur - 1;
       const uint8_t *cs = ring + cur * T::stage, *ns = ring + nxt * T::stage;
@@ -609,36 +616,40 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
       Fetch fe;
       // matrix instruction i of the stage's 2 NM, and what is issued behind it
       auto slot = [&](int i) __attribute__((always_inline)) {
-        const int tm = i % NM / TN, tn = i % TN, h = i / NM;
-        acc[tm][tn] = mma<FMT>(f[h].b[tn], f[h].a[tm], acc[tm][tn], sb, sa[tm]);
+        const int tm = i % NM / TN, tn = i % TN;
+        acc[tm][tn] = mma<FMT>(i < NM ? f0.b[tn] : f1.b[tn], i < NM ? f0.a[tm] : f1.a[tm], acc[tm][tn], sb, sa[tm]);
+        if constexpr (kDeep) {
 #pragma unroll
-        for (int j = 0; j < NF; ++j)
-          if (j * H / NF == i % NM) f[1 - h].read(j, h ? ns : cs, wi, wj, lane, 1 - h);
+          for (int j = 0; j < 2 * NF; ++j)
+            if (NM + j * NM / (2 * NF) == i) (j < NF ? f0 : to1).read(j % NF, ns, wi, wj, lane, j / NF);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NF; ++j)
+            if (j * H / NF == i % NM) (i < NM ? f1 : f0).read(j, i < NM ? cs : ns, wi, wj, lane, i < NM);
+        }
+        constexpr int kScale = kDeep ? NM : H;
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-          if (H + j * (NM - H) / TM == i) na[j] = scale_at(nbuf, nq, wi + 32 * j + (lane & 31));
-        if (i == NM - 1) nb = scale_at(nbuf, nq, T::rows + (wj >> 7));
+          if (kScale + j * (NM - H) / TM == i) na[j] = scale_at(nbuf, nq, wi + 32 * j + (lane & 31));
+        if (i == kScale + NM - H - 1) nb = scale_at(nbuf, nq, T::rows + (wj >> 7));
 #pragma unroll
         for (int u = 0; u < T::a_loads; ++u)
-          if ((kSplit ? NM + u * NM / T::a_loads : kFree + u * kSpan / kAll) == i)
-            op_load<RAGGED>(lo, ra, as, K, to_a, u);
+          if ((kSplit ? NM + u * NM / T::a_loads : u * kSpan / kAll) == i) op_load<RAGGED>(lo, ra, as, K, to_a, u);
 #pragma unroll
         for (int u = 0; u < T::b_loads; ++u)
-          if ((kSplit ? u * NM / T::b_loads : kFree + (T::a_loads + u) * kSpan / kAll) == i)
+          if ((kSplit ? u * NM / T::b_loads : (T::a_loads + u) * kSpan / kAll) == i)
             op_load<RAGGED>(lo, rb, bs, K, to_b, u);
-        if (i == H / 2) fe = next_scales(s, q, nk, buf);
-        if (i == H) load_scales(fe.skip, fe.own ? at : next, fe.at, fe.to);
+        if (i == (kDeep ? NM : 0) + H / 2) fe = next_scales(s, q, nk, buf);
+        if (i == (kDeep ? NM : 0) + H) load_scales(fe.skip, fe.own ? at : next, fe.at, fe.to);
         __builtin_amdgcn_sched_barrier(0);
       };
-#pragma unroll
-      for (int i = 0; i < kFree; ++i) slot(i);
-      if (!kSplit) {
+      if constexpr (kDeep) {
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int i = kFree; i < NM; ++i) slot(i);
-      wait_loads_or<kAhead + kEarly, T::stores>(s | settled);
+      for (int i = 0; i < NM; ++i) slot(i);
+      wait_loads_or<kDeep ? (NM * kAll + kSpan - 1) / kSpan : kAhead, T::stores>(s | settled);
       lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -650,10 +661,24 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
       cur = nxt;
     };
     int s = 0;
+    if constexpr (kDeep) {
 #pragma clang loop unroll(disable)
-    for (; s + R < nk; ++s) stage(s, std::true_type{});
+      for (; s + 1 + R < nk; s += 2) {
+        stage(s, f[0], f[1], g[1], std::true_type{});
+        stage(s + 1, f[0], g[1], f[1], std::true_type{});
+      }
+      if (s + R < nk) {
+        stage(s++, f[0], f[1], g[1], std::true_type{});
+        f[1] = g[1];
+      }
+      stage(s, f[0], f[1], g[1], std::false_type{});
+      stage(s + 1, f[0], g[1], f[1], std::false_type{});
+    } else {
 #pragma clang loop unroll(disable)
-    for (; s < nk; ++s) stage(s, std::false_type{});
+      for (; s + R < nk; ++s) stage(s, f[0], f[1], f[1], std::true_type{});
+#pragma clang loop unroll(disable)
+      for (; s < nk; ++s) stage(s, f[0], f[1], f[1], std::false_type{});
+    }
     }
     tile_out<T>(acc, out + (long long)at.m0 * N + at.j0, N, at.rows, at.cols);
     __builtin_amdgcn_sched_barrier(0);

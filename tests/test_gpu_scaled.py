@@ -238,6 +238,8 @@ KERNELS = {
     "stream_64x64": ([576], 2176, 2048), "stream_64x128": ([60] * 40, 2064, 2064),
     "stream_64x128_3": ([60] * 40, 2352, 2064), "stream_64x128_6": ([60] * 40, 2800, 2064),
     "stream_128x256": ([300] * 12, 2176, 8208), "stream_128x256_2": ([300] * 12, 2304, 8208),
+    # several tiles a workgroup of one or two blocks of the contraction each
+    "blocks_256x256_1": ([5000], 96, 16400), "blocks_256x256_2": ([9000], 256, 8208),
     "stream_256x256": ([5000], 2064, 8208), "stream_256x256_2": ([5000], 4352, 8208),
 }
 
