@@ -177,10 +177,10 @@ __global__ __launch_bounds__(64 * W) void k_scaled_few(
 // R stages.
 //
 // What bounds it.  32768 rows on 264 experts of 7168 x 2048 (4.24 GB) take 821 us, 5.2 TB/s: memory.
-// With one expert (32768 x 7168 x 2048, 256 x 256 tiles) 395 us, 2.44 PFLOP/s, where torch's library
-// product takes 309 us (3.11 PFLOP/s) and the bare matrix instructions reach 4.7-5.0: the chip holds
-// 1.80 GHz there, the matrix units are busy 62% of the cycles and a wave waits 16%; the same kernel
-// without its loads would take 304 us, with loads that all hit L2 345.  Between them, with 1408 of
+// With one expert (32768 x 7168 x 2048, 256 x 256 tiles) 374 to 390 us, 2.6 to 2.5 PFLOP/s, for normal
+// and for random bytes, where torch's library product takes 310 to 325 and the bare matrix
+// instructions reach 4.7-5.0: the chip's power sets the clock there (1.75 GHz; 303 us on zeros, the
+// library 229), and the matrix units are busy 61% of the cycles.  Between them, with 1408 of
 // contraction (24576 rows, 68 experts, 128 x 256 tiles: 112 us, floor 56), what costs is the tiles' last
 // rows (15% more than the rows there are), the last round of tiles (8 for 7.1) and 11 stages a tile
 // against one start of the ring and one store of the results.
@@ -711,7 +711,7 @@ static void launch_tiles(const uint8_t *a, const uint8_t *as, const uint8_t *b,
 //   6, 68, 2048x1408          8.2 /  9.9 / 11.6 / 17.6 / 24
 //   16, 1, 7168x7168           17 /   22 /   27 /   44 / 68
 //   512, 264, 7168x2048       545 /  544 /  542 /  541 / 658
-//   256, 1, 4096x4096          53 / 15.3 / 17.8 / 30.1 / 45
+//   256, 1, 4096x4096          53 / 15.2 / 17.8 / 30.1 / 45
 //   1000, 16, 1024x1024        18 / 11.5 /  9.2 / 14.3 / 17.3
 //   1024, 68, 2048x1408        53 /   43 /   40 /   43 / 55
 //   4096, 264, 7168x2048      971 /  661 /  666 /  693 / 826
@@ -719,7 +719,7 @@ static void launch_tiles(const uint8_t *a, const uint8_t *as, const uint8_t *b,
 //   24576, 68, 1408x2048        - /  232 /  159 /  114 / 118
 //   32768, 264, 7168x2048       - / 1474 / 1111 /  826 / 942
 //   2000, 1, 7168x7168          - /  252 /  155 /  100 / 92
-//   32768, 1, 7168x2048         - / 1146 /  734 /  446 / 405
+//   32768, 1, 7168x2048         - / 1146 /  734 /  446 / 395
 template <int FMT>
 static void launch_scaled(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
                           const int32_t *cu, uint16_t *out, int G, int M_total, int K, int N,
