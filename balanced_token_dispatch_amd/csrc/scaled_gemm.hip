@@ -24,6 +24,7 @@ namespace moe {
 
 constexpr int kScMaxDim = 1 << 21;  // largest Kd and N (offsets within a tile stay in 32 bits)
 constexpr int kScMaxG = 1088;
+constexpr long long kScMaxTiles = 1LL << 30;
 
 // ---- Few rows -----------------------------------------------------------------------------
 // 16 rows of one segment x 16 CT output columns per workgroup of W waves; wave w takes the blocks
@@ -73,14 +74,15 @@ __device__ inline int sc_build_tiles(const int32_t *cu, int G, int M_total, int 
   return carry;
 }
 
-// last rho with sStart[rho] <= t: the segment owning tile t
+// last rho with sStart[rho] <= t: the segment owning tile t, by the whole wave (t the same in all lanes):
+// every lane looks at one of 64 places, then at one of those between two.  Halving the range took 7 to
+// 10 reads of LDS one after the other.
 __device__ inline int sc_find_seg(const int *sStart, int G, int t) {
-  int lo = 0, hi = G;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (sStart[mid] <= t) lo = mid; else hi = mid;
-  }
-  return lo;
+  const int lane = threadIdx.x & 63, step = (G + kWave - 1) / kWave;  // at most 17
+  const int i = lane * step;
+  const int base = (__popcll(__ballot(i < G && sStart[min(i, G)] <= t)) - 1) * step;
+  const int j = base + lane;
+  return base + __popcll(__ballot(lane < step && j < G && sStart[min(j, G)] <= t)) - 1;
 }
 
 __device__ inline i32x8 join(u32x4 a, u32x4 b) {
@@ -104,13 +106,13 @@ __global__ __launch_bounds__(64 * W) void k_scaled_few(
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n_ct = (N + kFewCols * CT - 1) / (kFewCols * CT), nblk = (K + kBlock - 1) / kBlock;
   const int pitch = (int)scale_pitch(K), nnb = (N + kBlock - 1) / kBlock;
-  const long long total = (long long)n_rt * n_ct;
+  const int total = (int)min((long long)n_rt * n_ct, kScMaxTiles);
   // lane l holds bytes 16 (l / 16) .. + 16 and 64 more on of row l % 16: each load takes whole
   // half lines of 16 rows, and the order of the contraction is the same for both operands
   const int r = lane & 15, kq = 16 * (lane >> 4), off = r * K + kq;
-  for (long long t = blockIdx.x; t < total; t += gridDim.x) {
-    const int rt = (int)(t / n_ct), n0 = (int)(t % n_ct) * kFewCols * CT;
-    const int g = __builtin_amdgcn_readfirstlane(sc_find_seg(sStart, G, rt));
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    const int rt = t / n_ct, n0 = t % n_ct * kFewCols * CT;
+    const int g = sc_find_seg(sStart, G, rt);
     const int m0 = __builtin_amdgcn_readfirstlane(sCu[g] + (rt - sStart[g]) * kFewRows);
     const int rows = __builtin_amdgcn_readfirstlane(min(kFewRows, sCu[g + 1] - m0));
     const int cols = min(kFewCols * CT, N - n0);
@@ -393,18 +395,18 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
       __builtin_amdgcn_readfirstlane(sc_build_tiles<kTileThreads>(cu, G, M_total, T::rows, sCu, sStart));
   const int n_ct = (N + T::cols - 1) / T::cols;
   const int nnb = (N + kBlock - 1) / kBlock, pitch = (int)scale_pitch(K);
-  const long long total = (long long)n_rt * n_ct;
+  const int total = (int)min((long long)n_rt * n_ct, kScMaxTiles);
   // each XCD takes neighbouring tiles, walked in groups of 8 row tiles: shared panels in its L2
   const int grid = gridDim.x;
   const int lb = grid % kXcdCount ? blockIdx.x : blockIdx.x % kXcdCount * (grid / kXcdCount) + blockIdx.x / kXcdCount;
-  auto place = [&](long long t) {
+  auto place = [&](int t) {
     Place p = {a, b, a_scale, b_scale, 0, 0, 0, 0};
     if (t >= total) return p;
-    const int per = kGroupRows * n_ct, grp = (int)(t / per), r = (int)(t - (long long)grp * per);
+    const int per = kGroupRows * n_ct, grp = t / per, r = t - grp * per;
     const int gm = min(kGroupRows, n_rt - grp * kGroupRows);
     const int rt = grp * kGroupRows + r % gm;
     // read from LDS, so uniform only to us: the operands' buffers need them in scalar registers
-    const int g = __builtin_amdgcn_readfirstlane(sc_find_seg(sStart, G, rt));
+    const int g = sc_find_seg(sStart, G, rt);
     p.m0 = __builtin_amdgcn_readfirstlane(sCu[g] + (rt - sStart[g]) * T::rows);
     p.rows = __builtin_amdgcn_readfirstlane(min(T::rows, sCu[g + 1] - p.m0));
     p.j0 = r / gm * T::cols;
@@ -415,7 +417,7 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
     p.sb = b_scale + ((long long)g * nnb + p.j0 / kBlock) * pitch;
     return p;
   };
-  long long t = lb;
+  int t = lb;
   if (t >= total) return;
   Place at = place(t), next = place(t + grid);
 
@@ -755,6 +757,9 @@ extern "C" moe_status_t moe_group_gemm_scaled(moe_gemm_op op, moe_fp8 a_fmt, int
   if (a_fmt != MOE_E4M3 && a_fmt != MOE_E5M2) return MOE_EINVAL;
   if (G < 1 || G > kScMaxG || M_total < 0 || Kd < 16 || N < 16 || Kd % 16 || N % 16) return MOE_EINVAL;
   if (Kd > kScMaxDim || N > kScMaxDim) return MOE_EINVAL;
+  // tiles are counted in 32 bits, with room for the grid beyond the last (the smallest are 16 x 32)
+  if ((M_total / kFewRows + (int64_t)G) * ceil_div(op == MOE_GEMM_FWD ? N : Kd, kFewCols * 2) >= kScMaxTiles)
+    return MOE_EINVAL;
   if (M_total == 0) return MOE_OK;
   if (!a || !a_scale || !b || !b_scale || !cu_seqlens || !out) return MOE_EINVAL;
   if (!aligned16(a) || !aligned16(a_scale) || !aligned16(b) || !aligned16(b_scale) ||

@@ -434,7 +434,8 @@ moe_status_t moe_quant_weight(moe_dtype dtype, int32_t G, int32_t Kd, int32_t N,
  *   DGRAD: a [M_total, N],  b = q  [G, Kd, N]  -> out [M_total, Kd]
  *   a in a_fmt with a_scale [M_total, moe_scale_row_bytes(contraction)], b in
  *   e4m3 with the scales moe_quant_weight wrote beside it; out bf16.
- *   Kd % 16 == 0, N % 16 == 0, both <= 2^21; all 16-byte aligned.  WGRAD is
+ *   Kd % 16 == 0, N % 16 == 0, both <= 2^21, and fewer than 2^30 tiles of 16 x
+ *   32: (M_total / 16 + G) ceil(columns / 32); all 16-byte aligned.  WGRAD is
  *   MOE_EINVAL (its contraction runs over the rows; it takes the 16-bit rows
  *   through moe_group_gemm).
  * ------------------------------------------------------------------------- */

@@ -130,7 +130,7 @@ def test_scaled_gemm_refuses(mod):
     for kw in (dict(a0=mod.GEMM_WGRAD), dict(a0=9), dict(a1=2), dict(a2=0), dict(a2=1089), dict(a3=-1), dict(a4=0),
                dict(a4=24), dict(a4=(1 << 21) + 16), dict(a5=8), dict(a5=(1 << 21) + 16), dict(a6=None), dict(a7=None),
                dict(a8=None), dict(a9=None), dict(a10=None), dict(a11=None), dict(a6=ODD), dict(a7=ODD), dict(a8=ODD),
-               dict(a9=ODD), dict(a11=ODD), dict(a10=ctypes.c_void_p(18))):
+               dict(a9=ODD), dict(a11=ODD), dict(a10=ctypes.c_void_p(18)), dict(a3=(1 << 31) - 1, a5=1 << 14)):
         assert refused(fn, ok, **kw) == bad, kw
     assert refused(fn, ok, a3=0) == mod.MOE_OK
 
