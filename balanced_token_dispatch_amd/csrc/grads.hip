@@ -15,6 +15,9 @@ constexpr int kGradBatch = 64;
 constexpr int kGradThreads = 256;
 constexpr int kGradChunk = 1 << 14;    // elements per chunk
 constexpr int kGradParts = 2048;       // partial sums (and the sum kernel's largest grid)
+// Chunks that one workgroup sums by itself, in one launch (us, one launch / two: 1 chunk 3.5 / 5.5, 2 5.0 / 5.6,
+// 4 full ones 8.0 / 5.7; each launch is 2.7 more on the host)
+constexpr int kGradAlone = 2;
 
 struct GradBatch {
   const void *g[kGradBatch];
@@ -245,6 +248,10 @@ extern "C" moe_status_t moe_grad_sumsq(int32_t n, const void *const *grads, cons
   for (int at = 0; at < n;) {
     at = fill_batch(&b, at, n, grads, nullptr, numel, dtype);
     if (!b.count) break;
+    if (parts == 0 && at == n && b.first[b.count] <= kGradAlone) {
+      hipLaunchKernelGGL(k_grad_sumsq, dim3(1), dim3(kGradThreads), 0, stream, b, sumsq, 0);
+      return launch_status();
+    }
     const int grid = b.first[b.count] < kGradParts ? b.first[b.count] : kGradParts;
     hipLaunchKernelGGL(k_grad_sumsq, dim3(grid), dim3(kGradThreads), 0, stream, b, (double *)ws, parts);
     parts = grid > parts ? grid : parts;

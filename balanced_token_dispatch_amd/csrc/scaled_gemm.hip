@@ -183,7 +183,7 @@ __global__ __launch_bounds__(64 * W) void k_scaled_few(
 // and for random bytes, where torch's library product takes 310 to 325 and the bare matrix
 // instructions reach 4.7-5.0: the chip's power sets the clock there (1.75 GHz; 303 us on zeros, the
 // library 229), and the matrix units are busy 61% of the cycles.  Between them, with 1408 of
-// contraction (24576 rows, 68 experts, 128 x 256 tiles: 112 us, floor 56), what costs is the tiles' last
+// contraction (24576 rows, 68 experts, 128 x 256 tiles: 111 us, floor 56), what costs is the tiles' last
 // rows (15% more than the rows there are), the last round of tiles (8 for 7.1) and 11 stages a tile
 // against one start of the ring and one store of the results.
 constexpr int kTileThreads = 256, kTileWaves = 4;

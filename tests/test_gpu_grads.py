@@ -49,6 +49,8 @@ LISTS = {
     "empty_among": ([0, 4, 0, 0, 33], [F, B]), "many": (list(range(1, 400, 2)), [B, F]),
     "exact_batch": ([40000] * 64, [F]), "batch_and_one": ([100] * 65, [F]),
     "small_then_large": ([10] * 64 + [5000001], [F]), "large_then_small": ([5000001] + [10] * 70, [B]),
+    "one_chunk": ([16384], [F]), "two_chunks": ([16385], [B]), "two_tensors": ([100, 16384], [F, B]),
+    "two_then_empty": ([9, 0, 12] + [0] * 70, [F, B]), "three_chunks": ([1, 2, 3], [B, F]),
     "over_parts": ([1 << 14] * 40 + [(1 << 26) + 3], [F]),
 }
 
