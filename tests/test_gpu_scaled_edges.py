@@ -1,0 +1,76 @@
+"""The 8-bit path where its other tests do not go: packed bf16 rows with every bit pattern."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import scaled_ref as ref
+from scaled_common import FP8, bf16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import balanced_token_dispatch_amd as m
+    return m
+
+
+def quantise_bf16(m, x, fmt):
+    """(q as float64, scale bytes, copy) of bf16 rows without weights: the path that keeps them packed."""
+    t = torch.from_numpy(np.ascontiguousarray(x, np.float32)).bfloat16().cuda()
+    q = torch.full(t.shape, 3, dtype=torch.uint8, device="cuda").view(FP8[fmt])
+    s = torch.full((t.shape[0], m.scale_row_bytes(t.shape[1])), 9, dtype=torch.uint8, device="cuda")
+    copy = torch.full_like(t, 7.0)
+    m.moe_quant_rows(t, q, s, copy=copy)
+    assert torch.equal(copy.view(torch.int16), t.view(torch.int16))
+    return q.float().cpu().numpy().astype(np.float64), s.cpu().numpy()
+
+
+def exactly(m, x, fmt):
+    q, s = quantise_bf16(m, x, fmt)
+    wq, ws, _ = ref.quant_rows(x, fmt)
+    assert np.array_equal(s, ws)
+    assert np.array_equal(q, wq, equal_nan=True)
+    return ws
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_bf16_rows_of_every_value(m, fmt):
+    """Each bf16 bit pattern beside its neighbours, and all of them shuffled, so that every block holds
+    ordinary values, infinities or NaN and tiny ones together."""
+    bits = np.arange(65536, dtype=np.uint32) << 16
+    x = bits.view(np.float32).reshape(512, 128)
+    ws = exactly(m, x, fmt)
+    assert (ws[:, 0] == 0).any()        # blocks held at the smallest scale
+    exactly(m, np.random.default_rng(0).permutation(bits).view(np.float32).reshape(64, 1024), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_bf16_rows_with_one_not_finite(m, fmt):
+    """One infinity or NaN, in each place of a block, beside ordinary values: it does not count for the
+    block's scale, and the others round as without it."""
+    rng = np.random.default_rng(1)
+    base = bf16(rng.standard_normal((128, 272)) * 2.0 ** rng.integers(-3, 4, (128, 272)))
+    for v in (np.inf, -np.inf, np.nan):
+        x = base.copy()
+        x[np.arange(128), np.arange(128)] = v
+        x[:, 256 + 5] = v
+        exactly(m, x, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_bf16_rows_borders(m, fmt):
+    """Block maxima at and next to the format's largest value times a power of two, signed zeros, blocks of
+    zeros, of subnormals, of bf16's largest and smallest values, ties of every kind."""
+    top = ref.FORMATS[fmt][2]
+    rows = []
+    for e in (-126, -60, 0, 60, 100):
+        for f in (1.0 - 2.0 ** -8, 1.0, 1.0 + 2.0 ** -6 / 1.75):   # 0.875 2^n less half a step, itself, the value above
+            r = np.linspace(-1, 1, 128) * top * 0.99
+            r[17] = -top * f
+            rows.append(np.ldexp(r, e - 20 if e == 100 else e))
+    rows += [np.arange(128) / 16 * (top / 8), np.zeros(128), -np.zeros(128), np.full(128, 2.0 ** -133),
+             np.full(128, 3e-39), np.arange(128) * 2.0 ** -133, np.full(128, 2.0 ** -126),
+             np.full(128, float(torch.finfo(torch.bfloat16).max)),
+             np.where(np.arange(128) % 2, 2.0 ** -133, 1.0)]
+    exactly(m, bf16(np.array(rows)), fmt)
