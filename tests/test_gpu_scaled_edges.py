@@ -1,4 +1,5 @@
-"""The 8-bit path where its other tests do not go: packed bf16 rows with every bit pattern."""
+"""The 8-bit path where its other tests do not go: packed bf16 rows with every bit pattern, the kernel
+for few rows over several passes of its grid."""
 import numpy as np
 import pytest
 import torch
@@ -74,3 +75,50 @@ def test_bf16_rows_borders(m, fmt):
              np.full(128, float(torch.finfo(torch.bfloat16).max)),
              np.where(np.arange(128) % 2, 2.0 ** -133, 1.0)]
     exactly(m, bf16(np.array(rows)), fmt)
+
+
+# Sizes that the rule for few rows takes (M_total <= 16, or <= 8 a segment): segments, contraction, columns
+FEW = {
+    "at_most_16": ([7], 7184, 1040), "8_a_segment": ([16, 0, 0], 7184, 1040), "16_in_one": ([0, 24, 0, 0], 2064, 528),
+    # more tiles than one pass of the grid (8 workgroups a compute unit): a workgroup's second tile and on
+    "second_pass": ([i % 5 for i in range(264)], 400, 1024), "third_pass": ([8] * 300 + [0], 144, 1040),
+    "long_segments": ([1000] + [0] * 300 + [900, 3], 272, 1552),
+}
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("name", list(FEW))
+def test_few_rows(m, name, fmt, grad):
+    """The kernel for few rows on integers times powers of two (scales within 2^6, so that sums over the whole
+    contraction stay exact in fp32): equal to the float64 product rounded once."""
+    lens, K, C = FEW[name]
+    M, G = sum(lens) + 3, len(lens)      # 3 rows outside every segment
+    assert M <= 16 or M <= 8 * G
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles = sum(-(-n // 16) for n in lens) * -(-C // 32)
+    assert "pass" not in name or tiles > 8 * cus * (2 if name == "third_pass" else 1)
+    gen = torch.Generator(device="cuda").manual_seed(K + C)
+    ints = lambda *s: torch.randint(-1, 2, s, device="cuda", generator=gen).float()  # noqa: E731
+    a, b = ints(M, K).to(FP8[fmt]), ints(G, C, K).to(FP8["e4m3"])
+
+    def scales(*rows):
+        s = torch.full(rows + (m.scale_row_bytes(K),), 255, dtype=torch.uint8, device="cuda")
+        s[..., :-(-K // 128)] = torch.randint(126, 129, rows + (-(-K // 128),), device="cuda", generator=gen).byte()
+        return s
+
+    sa, sb = scales(M), scales(G, -(-C // 128))
+    cu = torch.tensor(np.concatenate([[2], 2 + np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    out = torch.full((M, C), -7.0, dtype=torch.bfloat16, device="cuda")
+    op, kd, n = (m.GEMM_DGRAD, C, K) if grad else (m.GEMM_FWD, K, C)
+    m.moe_group_gemm_scaled(op, a, sa, b, sb, cu, out, kd, n)
+    want = torch.full_like(out, -7.0)
+    kb = torch.arange(K, device="cuda") // 128
+    two = lambda s: torch.exp2((s.double() - 127))[..., kb]  # noqa: E731
+    at = 2
+    for g, n_rows in enumerate(lens):
+        rows = slice(at, at + n_rows)
+        w = b[g].double() * two(sb[g]).repeat_interleave(128, 0)[:C]
+        want[rows] = (a[rows].double() * two(sa[rows])).mm(w.t().contiguous()).bfloat16()
+        at += n_rows
+    assert torch.equal(out, want)
