@@ -48,8 +48,16 @@ __device__ inline float load_logit(const void *p, long long i) {
     return ((const float *)p)[i];
 }
 
-// 1 / (1 + exp(-x)); exp's overflow to infinity gives the right zero
-__device__ inline float logistic(float x) { return 1.0f / (1.0f + expf(-x)); }
+// The logistic of x over exp(m), m at most 0: exp(x) / (1 + exp(x)) below 0 and 1 / (1 + exp(-x)) above it share
+// the denominator 1 + exp(-|x|), which never overflows.  With m the token's largest chosen logit (0 where that is
+// positive) the scores that are added reach 1/2, however low all of them are, and exp(m) leaves their ratios.
+__device__ inline float logistic_over(float x, float m) {
+  if (x == -__builtin_inff()) return 0.0f;
+  const float e = expf(-fabsf(x));
+  float n = x >= 0.0f ? 1.0f : e;
+  if (m < 0.0f) n = expf(x - m);  // x is at most m then
+  return n / (1.0f + e);
+}
 
 // Maximum and sum over the L lanes of a token, the same in all of them: rotations within 16 lanes,
 // then rows and halves of the wave swapped.
@@ -196,11 +204,13 @@ __global__ __launch_bounds__(kRtThreads) void k_router_topk(
       for (int j = 0; j < V; ++j) sum += e0 + j < E && x[j] != ninf ? expf(x[j] - top) : 0.0f;
       sum = token_sum<L>(sum);
     }
+    Key first = 0;  // the largest key
     for (int r = 0; r < K; ++r) {
       Key best = most_of[0];
 #pragma unroll
       for (int g = 1; g < G; ++g) best = max(best, most_of[g]);
       const Key most = token_max<L>(best);
+      first = max(first, most);
       const unsigned long long who = __ballot(best == most) >> (lane - l);
       if (l == __ffsll(who) - 1) {  // the token's lowest lane that has it
         int g = 0;
@@ -224,7 +234,7 @@ __global__ __launch_bounds__(kRtThreads) void k_router_topk(
     // weights of the chosen: score / sum, 0 where the sum is 0
     float m = top;
     auto logit = [&](int r) { return t < T && r < K ? load_logit<BF16>(logits, t * E + list[r]) : ninf; };
-    if (SCORE == MOE_SCORE_SOFTMAX_TOPK) {
+    if (SCORE == MOE_SCORE_SOFTMAX_TOPK || (SCORE == MOE_SCORE_SIGMOID && BIAS)) {
       uint32_t k = 0;
       for (int r = l; r < K; r += L) {
         const float c = logit(r);
@@ -233,17 +243,21 @@ __global__ __launch_bounds__(kRtThreads) void k_router_topk(
       k = token_max<L>(k);
       m = k ? key_value(k) : ninf;
     }
+    // without a bias the first chosen is the largest (where it is NaN, so are the weights)
+    if (SCORE == MOE_SCORE_SIGMOID) m = fminf(BIAS ? m : key_value((uint32_t)first), 0.0f);
     auto score = [&](float c) {
-      return SCORE == MOE_SCORE_SIGMOID ? logistic(c) : c == ninf ? 0.0f : expf(c - m);
+      return SCORE == MOE_SCORE_SIGMOID ? logistic_over(c, m) : c == ninf ? 0.0f : expf(c - m);
     };
+    const float mine = score(logit(l));  // of the lane's first entry: the only one up to L
     if (SCORE != MOE_SCORE_SOFTMAX) {
-      for (int r = l; r < K; r += L) sum += score(logit(r));
+      sum = l < K ? mine : 0.0f;
+      for (int r = l + L; r < K; r += L) sum += score(logit(r));
       sum = token_sum<L>(sum);
     }
     for (int r = l; r < K; r += L)
       if (t < T) {
         idx[t * K + r] = list[r];
-        w[t * K + r] = sum == 0.0f ? 0.0f : factor * (score(logit(r)) / sum);
+        w[t * K + r] = sum == 0.0f ? 0.0f : factor * ((r == l ? mine : score(logit(r))) / sum);
       }
   }
 }
@@ -291,8 +305,9 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(
           sum += x[i][j];
         }
     }
-    // entry r of this token: its expert (-1: none), logit and weight's gradient
-    auto entry = [&](int r, int &e, float &c, float &d) {
+    // entry r of this token: its expert (-1: none), logit and weight's gradient; the lane's first one (the only
+    // one up to L) is loaded once
+    auto load_entry = [&](int r, int &e, float &c, float &d) {
       e = -1, c = ninf, d = 0.0f;
       if (t < T && r < K) {
         e = idx[t * K + r];
@@ -300,16 +315,29 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(
         if (e >= 0) c = load_logit<BF16>(logits, t * E + e), d = factor * dw[t * K + r];
       }
     };
-    int e;
-    float c, d;
-    if (SCORE == MOE_SCORE_SOFTMAX_TOPK) {
+    int e, e1;
+    float c, d, c1, d1;
+    load_entry(l, e1, c1, d1);
+    auto entry = [&](int r, int &e, float &c, float &d) {
+      if (r == l)
+        e = e1, c = c1, d = d1;
+      else
+        load_entry(r, e, c, d);
+    };
+    if (SCORE != MOE_SCORE_SOFTMAX) {
       for (int r = l; r < K; r += L) entry(r, e, c, d), m = largest(m, c);
       all_lanes();
     }
+    if (SCORE == MOE_SCORE_SIGMOID) m = fminf(m, 0.0f);
     auto score = [&](float v) {
-      return SCORE == MOE_SCORE_SIGMOID ? logistic(v) : v == ninf ? 0.0f : expf(v - m);
+      return SCORE == MOE_SCORE_SIGMOID ? logistic_over(v, m) : v == ninf ? 0.0f : expf(v - m);
     };
-    for (int r = l; r < K; r += L) {
+    const float s1 = score(c1);
+    if (l < K) {
+      if (SCORE != MOE_SCORE_SOFTMAX) sum += e1 >= 0 ? s1 : 0.0f;
+      inner += d1 * s1;
+    }
+    for (int r = l + L; r < K; r += L) {
       entry(r, e, c, d);
       const float s = score(c);
       if (SCORE != MOE_SCORE_SOFTMAX) sum += e >= 0 ? s : 0.0f;
@@ -328,7 +356,7 @@ __global__ __launch_bounds__(kRtThreads) void k_router_bwd(
     }
     for (int r0 = 0; r0 < K; r0 += L) {
       entry(r0 + l, e, c, d);
-      const float wgt = score(c) * rs;
+      const float wgt = (r0 == 0 ? s1 : score(c)) * rs;
       float gr = 0.0f;
       if (e >= 0) {
         if (SCORE == MOE_SCORE_SOFTMAX) gr = wgt * d;

@@ -452,8 +452,10 @@ moe_status_t moe_group_gemm_scaled(moe_gemm_op op, moe_fp8 a_fmt, int32_t G, int
  * (SOFTMAX_TOPK), its softmax over all experts (SOFTMAX) or its logistic
  * (SIGMOID); listed by that value descending, ties to the lower id; a NaN
  * counts as larger than any number.  The bias moves the choice only.  Weights
- * (fp32) are factor times the score of the chosen logits: see moe_score.  An
- * expert whose logit is -inf weighs 0, also where every chosen one is -inf.
+ * (fp32) are factor times the score of the chosen logits: see moe_score; the
+ * logistic over its sum is worked out relative to the largest chosen, so that it
+ * holds for any finite logits.  An expert whose logit is -inf weighs 0, also where
+ * every chosen one is -inf.
  *   logits [T, E] of dtype (bf16 or fp32), 1 <= E <= 1024, 1 <= K <= E,
  *   topk_idx [T, K] int32, topk_w [T, K] fp32; factor finite.
  * ------------------------------------------------------------------------- */

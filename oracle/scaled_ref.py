@@ -148,7 +148,10 @@ def router_weights(x, order, score):
     c = x[list(order)]
     with np.errstate(invalid="ignore", over="ignore"):
         if score == "sigmoid":
-            s = _logistic(c)
+            # over exp(the largest, at most 0), which leaves the ratios: the logistic itself is 0 in
+            # float64 below -745
+            m = min(np.fmax.reduce(c, initial=-np.inf), 0.0)
+            s = np.where(c == -np.inf, 0.0, np.exp(np.minimum(c, 0.0) - m) / (1.0 + np.exp(-np.abs(c))))
             total = s.sum()
         else:
             whole = c if score == "softmax_topk" else x
