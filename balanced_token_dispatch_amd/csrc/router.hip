@@ -169,13 +169,15 @@ __global__ __launch_bounds__(kRtThreads) void k_router_topk(
     if constexpr (BIAS) {
       // selection by score + bias: near ties decide which experts run, so in 64 bits
       double s[V], sum = 0.0;
+      const double base = top == ninf ? 0.0 : (double)top;  // with every logit -inf, scores of 0, not NaN
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         s[j] = x[j];
         if (SCORE == MOE_SCORE_SIGMOID) s[j] = 1.0 / (1.0 + exp(-s[j]));
-        if (SCORE == MOE_SCORE_SOFTMAX) sum += s[j] = exp(s[j] - (double)top);
+        if (SCORE == MOE_SCORE_SOFTMAX) sum += s[j] = exp(s[j] - base);
       }
       if (SCORE == MOE_SCORE_SOFTMAX) sum = token_sum<L>(sum);
+      if (sum == 0.0) sum = 1.0;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         Keys k;

@@ -451,7 +451,8 @@ moe_status_t moe_group_gemm_scaled(moe_gemm_op op, moe_fp8 a_fmt, int32_t G, int
  * largest of score + bias, worked out in 64 bits, where the score is the logit
  * (SOFTMAX_TOPK), its softmax over all experts (SOFTMAX) or its logistic
  * (SIGMOID); listed by that value descending, ties to the lower id; a NaN
- * counts as larger than any number.  The bias moves the choice only.  Weights
+ * counts as larger than any number.  Where every logit is -inf the scores are 0
+ * (SOFTMAX, SIGMOID) and the bias alone orders.  The bias moves the choice only.  Weights
  * (fp32) are factor times the score of the chosen logits: see moe_score; the
  * logistic over its sum is worked out relative to the largest chosen, so that it
  * holds for any finite logits.  An expert whose logit is -inf weighs 0, also where

@@ -134,7 +134,7 @@ def router_topk(logits, K, score, bias=None, factor=1.0):
             if score == "sigmoid":
                 rank = _logistic(x)
             elif score == "softmax":
-                rank = np.exp(x - x.max()) / np.exp(x - x.max()).sum()
+                rank = router_weights(x, range(len(x)), "softmax")
             rank = rank + np.asarray(bias, np.float64)
         order = sorted(range(len(x)), key=lambda e: (-(np.inf if np.isnan(rank[e]) else rank[e]),
                                                      not np.isnan(rank[e]), e))[:K]

@@ -97,3 +97,24 @@ def test_logistic_of_far_logits_against_differences(m):
         down[:, e] -= h
         assert (np.abs((value(up) - value(down)) / (2 * h) - d[:, e]) <= tol).all()
     assert (d[:, K:] == 0).all() and (np.abs(d[:, :K]).max(1) > 1e-2).all()
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("score", ["softmax_topk", "softmax", "sigmoid"])
+@pytest.mark.parametrize("E,K", [(3, 2), (64, 5), (130, 130), (256, 8), (300, 40), (1024, 8)])
+def test_bias_orders_masked_rows(m, E, K, score, many):
+    """Rows without a logit above -inf, with one, with half: the bias alone orders experts whose score is 0."""
+    r = np.random.default_rng(E)
+    x = r.standard_normal((7, E)).astype(np.float32)
+    x[1] = -np.inf
+    x[2, np.arange(E) != E // 2] = -np.inf
+    x[4] = -np.inf
+    x[5, ::2] = -np.inf
+    bias = r.permutation(np.linspace(-1.0, 1.0, E)).astype(np.float32)
+    rows = np.arange(8209) % 7 if many else np.arange(7)
+    idx, w = topk(m, torch.from_numpy(x[rows]).cuda(), K, score, bias)
+    widx, ww = ref.router_topk(x.astype(np.float64), K, score, bias)
+    assert np.array_equal(idx, widx[rows])
+    finite = np.where(np.isfinite(x), x, 0.0).astype(np.float64)
+    assert (np.abs(w - ww[rows]) <= weight_tol(finite, E) * ww[rows]).all()
+    assert (w[rows == 1] == 0).all() and (w[rows == 4] == 0).all()

@@ -41,3 +41,13 @@ def test_logistic_weights_of_masked_logits():
     assert w(low, low, low, low) == [0.25] * 4
     assert w(low, 1.0) == [0.0, 1.0]
     assert np.isnan(w(np.nan, 1.0)).all()
+
+
+@pytest.mark.parametrize("score", ["softmax_topk", "softmax", "sigmoid"])
+def test_bias_orders_a_fully_masked_row(score):
+    """Where every logit is -inf every score is 0 (the logit itself for softmax_topk: no order but the ids), so the
+    bias alone chooses; all weights are 0."""
+    bias = np.array([0.5, -1.0, 2.0, 0.25, 2.0])
+    ids, w = ref.router_topk(np.full((1, 5), -np.inf), 3, score, bias)
+    assert list(ids[0]) == ([0, 1, 2] if score == "softmax_topk" else [2, 4, 0])
+    assert (w == 0).all()
