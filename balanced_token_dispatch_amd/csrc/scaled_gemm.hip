@@ -50,7 +50,8 @@ __device__ inline int sc_build_tiles(const int32_t *cu, int G, int M_total, int 
   for (int base = 0; base < G; base += THREADS) {
     const int rho = base + tid;
     int v = 0;
-    if (rho < G) v = max(sCu[rho + 1] - sCu[rho] + tile - 1, 0) / tile;
+    if (rho < G && sCu[rho + 1] > sCu[rho])
+      v = (sCu[rho + 1] - sCu[rho] - 1) / tile + 1;  // (adding tile - 1 first would pass 2^31)
     int x = v;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {

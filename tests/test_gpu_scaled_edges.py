@@ -122,3 +122,27 @@ def test_few_rows(m, name, fmt, grad):
         want[rows] = (a[rows].double() * two(sa[rows])).mm(w.t().contiguous()).bfloat16()
         at += n_rows
     assert torch.equal(out, want)
+
+
+def test_a_segment_of_nearly_2_31_rows(m):
+    """More rows in one segment than 2^31 less a tile: they are all written."""
+    torch.cuda.empty_cache()
+    M, K = (1 << 31) - 64, 16
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GB of memory")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    ends = torch.randint(-2, 3, (600, K), device="cuda", generator=gen).float().to(FP8["e4m3"])
+    b = torch.randint(-2, 3, (1, K, K), device="cuda", generator=gen).float().to(FP8["e4m3"])
+    want = (ends.double() @ b[0].double().t().contiguous()).bfloat16()
+    a = torch.zeros((M, K), dtype=torch.uint8, device="cuda")
+    a[:300], a[M - 300:] = ends[:300].view(torch.uint8), ends[300:].view(torch.uint8)
+    sa = torch.full((M, 16), 127, dtype=torch.uint8, device="cuda")
+    sb = torch.full((1, 1, 16), 127, dtype=torch.uint8, device="cuda")
+    out = torch.full((M, K), -7.0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    m.moe_group_gemm_scaled(m.GEMM_FWD, a.view(FP8["e4m3"]), sa, b, sb, cu, out, K, K)
+    assert torch.equal(out[:300], want[:300]) and torch.equal(out[M - 300:], want[300:])
+    for lo in range(300, M - 300, 1 << 27):
+        assert not out[lo:min(lo + (1 << 27), M - 300)].any()
+    del a, sa, out
+    torch.cuda.empty_cache()
