@@ -49,7 +49,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (GEMM_DGRAD, GEMM_FWD, GEMM_WGRAD, dims as _mk_dims, dispatch_layout_workspace_bytes,
+from . import (GEMM_DGRAD, GEMM_FWD, GEMM_WGRAD, MoeError, dims as _mk_dims, dispatch_layout_workspace_bytes,
                grad_sumsq_workspace_bytes, group_gemm_workspace_bytes, moe_combine, moe_combine_weight_grad,
                moe_dispatch_layout, moe_grad_clip, moe_grad_sumsq, moe_group_gemm,
                moe_group_gemm_gather, moe_group_gemm_scaled, moe_group_gemm_swiglu,
@@ -218,13 +218,19 @@ class LayerStep:
             moe_quant_weight(w[:E], *(t[:E] for t in qw.tensors()))
         self.weights_quantised = True
 
+    def _check_logits(self, logits):
+        if tuple(logits.shape) != (self.s.S, self.s.E):
+            raise MoeError(f"logits of shape {tuple(logits.shape)}, expected (S, E) = ({self.s.S}, {self.s.E})")
+
     def route(self, logits, score="softmax_topk", bias=None, factor=1.0):
         """This rank's expert ids and router weights (its rows of topk_idx and topk_w) from its gate's
         logits [S, E]."""
+        self._check_logits(logits)
         moe_router_topk(logits, self.topk_idx[self.rank], self.topk_w[self.rank], score, bias, factor)
 
     def route_backward(self, logits, dlogits, score="softmax_topk", factor=1.0):
         """dlogits [S, E] from the router-weight gradient of the last backward."""
+        self._check_logits(logits)
         moe_router_backward(logits, self.topk_idx[self.rank],
                             self.dtopk_w.view(self.s.S, self.s.K), dlogits, score, factor)
 
