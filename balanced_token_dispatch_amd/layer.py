@@ -234,16 +234,16 @@ class LayerStep:
         moe_router_backward(logits, self.topk_idx[self.rank],
                             self.dtopk_w.view(self.s.S, self.s.K), dlogits, score, factor)
 
-    def clip_gradients(self, max_norm, others=(), group=None):
-        """Scales the home experts' weight gradients, and the gradients in `others`, in place to a
-        global norm of at most max_norm; returns the norm before (a one-element tensor).  With a
-        process group the norm is over the gradients of all its ranks.  After backward(), whose fold
-        leaves the slots' rows zero."""
+    def clip_gradients(self, max_norm, others=()):
+        """Scales the experts' weight gradients of this rank, and the gradients in `others`, in place to a
+        norm over all of them of at most max_norm; returns the norm before (a one-element tensor).
+        After backward(), whose fold leaves the slots' rows zero.  The norm is this rank's: an expert
+        with replicas has a part of its gradient on every rank that held one.  Once those are added up,
+        each gradient whole on one rank, moe_grad_sumsq, an all-reduce of its sum and moe_grad_clip give
+        the norm over ranks."""
         E = self.s.E
         grads = [self.dw_up[:E], self.dw_down[:E], *others]
         moe_grad_sumsq(grads, self.sumsq, self.clip_ws)
-        if group is not None:
-            torch.distributed.all_reduce(self.sumsq, group=group)
         moe_grad_clip(grads, self.sumsq, max_norm, self.grad_norm)
         return self.grad_norm
 

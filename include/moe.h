@@ -479,8 +479,9 @@ moe_status_t moe_router_backward(moe_dtype dtype, moe_score score, int64_t T, in
 
 /* ---------------------------------------------------------------------------
  * moe_grad_sumsq -- *sumsq = the sum of the squares of all values of n tensors,
- * in 64 bits and a fixed order.  Ranks that hold different gradients add their
- * sums (an all-reduce of one double) before moe_grad_clip.
+ * in 64 bits and a fixed order.  Ranks that hold different gradients, each whole on
+ * one rank (not the parts of an expert with replicas), add their sums (an
+ * all-reduce of one double) before moe_grad_clip.
  *   grads, numel, dtype: HOST arrays of n entries: device address (aligned to
  *   the element), number of elements (0 allowed) and type (bf16 or fp32); read
  *   before the call returns.

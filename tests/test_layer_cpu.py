@@ -42,3 +42,30 @@ def test_route_takes_logits_of_this_layers_experts(layer, monkeypatch):
     L.route(x)
     L.route_backward(x, torch.zeros_like(x))
     assert len(seen) == 2
+
+
+def clipping_step(layer, monkeypatch):
+    """A LayerStep whose clipping is computed by torch."""
+    def sumsq(grads, out, ws):
+        out.fill_(sum(float(g.double().square().sum()) for g in grads))
+
+    def clip(grads, total, max_norm, norm):
+        norm.copy_(total.sqrt())
+        for g in grads:
+            g.mul_(float(min(1.0, max_norm / (total.sqrt() + 1e-6))))
+
+    monkeypatch.setattr(layer, "moe_grad_sumsq", sumsq)
+    monkeypatch.setattr(layer, "moe_grad_clip", clip)
+    return step_of(layer, dw_up=torch.ones(7, 32, 16), dw_down=torch.ones(7, 16, 32), clip_ws=None,
+                   sumsq=torch.zeros(1, dtype=torch.float64), grad_norm=torch.zeros(1))
+
+
+def test_clipping_has_no_norm_over_ranks(layer, monkeypatch):
+    """An expert with replicas has a part of its gradient on each rank that holds one, and nothing in the step
+    brings them together: the squares of the parts do not add up to the square of their sum."""
+    L = clipping_step(layer, monkeypatch)
+    with pytest.raises(TypeError):
+        L.clip_gradients(1.0, group=object())
+    assert (L.dw_up == 1.0).all()
+    L.clip_gradients(1.0)
+    assert float(L.dw_up[:6].double().square().sum() + L.dw_down[:6].double().square().sum()) == pytest.approx(1.0, rel=1e-6)
