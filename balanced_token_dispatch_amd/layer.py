@@ -245,7 +245,7 @@ class LayerStep:
         grads = [self.dw_up[:E], self.dw_down[:E], *others]
         moe_grad_sumsq(grads, self.sumsq, self.clip_ws)
         moe_grad_clip(grads, self.sumsq, max_norm, self.grad_norm)
-        return self.grad_norm
+        return self.grad_norm.clone()  # the buffer itself is the next call's too
 
     @staticmethod
     def _call(timer, name, fn, *args):

@@ -1,4 +1,4 @@
-"""The 8-bit path where its other tests do not go: packed bf16 rows with every bit pattern, the kernel
+"""The 8-bit path and the clipping where their other tests do not go: packed bf16 rows with every bit pattern, the kernel
 for few rows over several passes of its grid."""
 import numpy as np
 import pytest
@@ -146,3 +146,46 @@ def test_a_segment_of_nearly_2_31_rows(m):
         assert not out[lo:min(lo + (1 << 27), M - 300)].any()
     del a, sa, out
     torch.cuda.empty_cache()
+
+
+def layer_step(**kw):
+    """A small layer with filled inputs."""
+    import synth
+    from balanced_token_dispatch_amd.layer import LayerStep, Shape
+    s = Shape(R=4, S=96, K=2, E=16, B=2, H=272, Hp=144)
+    L = LayerStep(s, rank=1, **kw)
+    idx, w = synth.routing(synth.Dims(R=s.R, S=s.S, K=s.K, E=s.E, B=s.B, H=s.H, Hp=s.Hp), 1.0, 31)
+    synth.fill_normal_(L.x_all, 1.0, 311)
+    synth.fill_normal_(L.w_up, 0.1, 312)
+    synth.fill_normal_(L.w_down, 0.1, 313)
+    L.topk_idx.copy_(torch.from_numpy(idx))
+    L.topk_w.copy_(torch.from_numpy(w))
+    return L
+
+
+def test_a_kept_norm_stays(m):
+    """The norm that clip_gradients returned, after further calls and replays of a captured one."""
+    L = layer_step()
+    kept = []
+    for n in (1.0, 2.0):
+        L.dw_up.fill_(n)
+        kept.append(L.clip_gradients(1e9))
+    L.dw_up.fill_(1.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        L.clip_gradients(1e9)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = L.clip_gradients(1e9)
+    one = (16 * 272 * 144) ** 0.5
+    for n in (3.0, 4.0, 5.0):
+        L.dw_up.fill_(n)
+        g.replay()
+        assert captured.item() == pytest.approx(n * one, rel=1e-6) and L.grad_norm.item() == captured.item()
+        L.dw_up.fill_(2 * n)
+        kept.append(L.clip_gradients(1e9))
+        assert captured.item() == pytest.approx(n * one, rel=1e-6)
+    assert [k.item() for k in kept] == pytest.approx([n * one for n in (1.0, 2.0, 6.0, 8.0, 10.0)], rel=1e-6)

@@ -69,3 +69,13 @@ def test_clipping_has_no_norm_over_ranks(layer, monkeypatch):
     assert (L.dw_up == 1.0).all()
     L.clip_gradients(1.0)
     assert float(L.dw_up[:6].double().square().sum() + L.dw_down[:6].double().square().sum()) == pytest.approx(1.0, rel=1e-6)
+
+
+def test_a_kept_norm_stays(layer, monkeypatch):
+    L = clipping_step(layer, monkeypatch)
+    first = L.clip_gradients(1.0)
+    value = first.item()
+    assert value == pytest.approx((2 * 6 * 32 * 16) ** 0.5)
+    second = L.clip_gradients(0.5)
+    assert first.item() == value and second.item() == pytest.approx(1.0, rel=1e-6)
+    assert L.grad_norm.item() == second.item()
