@@ -163,7 +163,7 @@ class LayerStep:
         self.out = torch.zeros((s.S, s.H), **act)
         if self.scaled:
             self.q_up, self.q_down = QuantWeights(self.w_up), QuantWeights(self.w_down)
-            self.weights_quantised = False
+            self.quantised_from = None   # what quantise_weights() read (_weights)
             e4 = torch.float8_e4m3fn
             self.xq, self.zq = QuantRows(s.SK, s.H, e4, device), QuantRows(s.SK, s.Hp, e4, device)
         self.backward_enabled = backward
@@ -208,6 +208,17 @@ class LayerStep:
         r, SK = self.rank, self.s.SK
         return self.y_all[r * SK:(r + 1) * SK]
 
+    def _weights(self):
+        """The weights and how often torch has changed them in place."""
+        return [(w, None if w.is_inference() else w._version) for w in (self.w_up, self.w_down)]
+
+    @property
+    def weights_quantised(self):
+        """Whether the 8-bit weights are the present ones', as far as torch counts the changes: not those by
+        kernels of other libraries, fused optimizers or .data."""
+        was = self.quantised_from
+        return was is not None and all(w is v and n == k for (w, n), (v, k) in zip(self._weights(), was))
+
     def quantise_weights(self):
         """The home experts' weights into 8 bits (gemm="scaled"): after every change of w_up or w_down.
         The slots' rows follow by the step's prefetch."""
@@ -216,7 +227,7 @@ class LayerStep:
         E = self.s.E
         for w, qw in ((self.w_up, self.q_up), (self.w_down, self.q_down)):
             moe_quant_weight(w[:E], *(t[:E] for t in qw.tensors()))
-        self.weights_quantised = True
+        self.quantised_from = self._weights()
 
     def _check_logits(self, logits):
         if tuple(logits.shape) != (self.s.S, self.s.E):
@@ -257,7 +268,7 @@ class LayerStep:
     def forward(self, timer=None):
         s, r, c = self.s, self.rank, self._call
         if self.scaled and not self.weights_quantised:
-            raise ValueError("forward: quantise_weights() has not put the weights into 8 bits yet")
+            raise ValueError("forward: quantise_weights() has not put these weights into 8 bits, or not since they changed")
         if self.plan_noalloc:
             c(timer, "plan", moe_plan_noalloc, self.d, self.topk_idx, self.counts, self.plan,
               self.status)

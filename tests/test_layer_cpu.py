@@ -79,3 +79,63 @@ def test_a_kept_norm_stays(layer, monkeypatch):
     second = L.clip_gradients(0.5)
     assert first.item() == value and second.item() == pytest.approx(1.0, rel=1e-6)
     assert L.grad_norm.item() == second.item()
+
+
+class Reached(Exception):
+    """The step went on to its first call."""
+
+
+def scaled_step(layer, monkeypatch, **attrs):
+    """An 8-bit LayerStep with weights whose quantising is recorded and whose forward stops at the plan."""
+    calls = []
+    monkeypatch.setattr(layer, "moe_quant_weight", lambda *a: calls.append(a))
+
+    def plan(*a):
+        raise Reached
+    monkeypatch.setattr(layer, "moe_plan", plan)
+    w = dict(w_up=torch.ones(7, 32, 16), w_down=torch.ones(7, 16, 32))
+    L = step_of(layer, scaled=True, plan_noalloc=False, counts=None, plan=None, status=None, ws=None, d=None,
+                quantised_from=None, **w, **attrs)
+    L.q_up, L.q_down = layer.QuantWeights(L.w_up), layer.QuantWeights(L.w_down)
+    return L, calls
+
+
+def test_forward_refuses_weights_changed_since_they_were_quantised(layer, monkeypatch):
+    """An update in place (a whole tensor, a view of it, an optimizer's step on a parameter over it) or another tensor in
+    the weights' place: forward() would run on the old 8-bit ones."""
+    L, _ = scaled_step(layer, monkeypatch)
+
+    def adam():
+        p = torch.nn.Parameter(L.w_down)
+        p.grad = torch.ones_like(p)
+        torch.optim.AdamW([p]).step()
+
+    def replaced():
+        L.w_up = L.w_up.clone()
+
+    def in_inference():
+        with torch.inference_mode():
+            L.w_down.mul_(2.0)
+
+    for change in (lambda: L.w_up.add_(1.0), lambda: L.w_down[2].copy_(torch.zeros(16, 32)), adam, replaced, in_inference):
+        L.quantise_weights()
+        for _ in range(2):
+            with pytest.raises(Reached):
+                L.forward()
+        change()
+        with pytest.raises(ValueError, match="quantise_weights"):
+            L.forward()
+    L.quantise_weights()
+    with pytest.raises(Reached):
+        L.forward()
+
+
+def test_weights_made_in_inference_mode(layer, monkeypatch):
+    """They do not count their changes: the first quantising is asked for, later ones are the caller's."""
+    with torch.inference_mode():
+        L, _ = scaled_step(layer, monkeypatch)
+        with pytest.raises(ValueError, match="quantise_weights"):
+            L.forward()
+        L.quantise_weights()
+        with pytest.raises(Reached):
+            L.forward()
