@@ -65,15 +65,17 @@ kOverlapMinWork = 1e11
 
 
 class QuantWeights:
-    """One projection's weights [G, Kd, N] in 8 bits, in the order DGRAD contracts (q) and the order FWD
-    contracts (qt), each with its scales."""
+    """One projection's weights [G, Kd, N] in 8 bits, in the order FWD contracts (qt) and, with `dgrad`, the
+    order DGRAD contracts (q), each with its scales."""
 
-    def __init__(self, w):
+    def __init__(self, w, dgrad=True):
         G, Kd, N = w.shape
         u8 = dict(dtype=torch.uint8, device=w.device)
-        self.q = torch.zeros((G, Kd, N), **u8).view(torch.float8_e4m3fn)
+        self.q = self.q_scale = None
+        if dgrad:
+            self.q = torch.zeros((G, Kd, N), **u8).view(torch.float8_e4m3fn)
+            self.q_scale = torch.full((G, -(-Kd // 128), scale_row_bytes(N)), 127, **u8)
         self.qt = torch.zeros((G, N, Kd), **u8).view(torch.float8_e4m3fn)
-        self.q_scale = torch.full((G, -(-Kd // 128), scale_row_bytes(N)), 127, **u8)
         self.qt_scale = torch.full((G, -(-N // 128), scale_row_bytes(Kd)), 127, **u8)
 
     def tensors(self):
@@ -162,7 +164,7 @@ class LayerStep:
         self.y_all = torch.zeros((s.R * s.SK, s.H), **act)
         self.out = torch.zeros((s.S, s.H), **act)
         if self.scaled:
-            self.q_up, self.q_down = QuantWeights(self.w_up), QuantWeights(self.w_down)
+            self.q_up, self.q_down = (QuantWeights(w, dgrad=backward) for w in (self.w_up, self.w_down))
             self.quantised_from = None   # what quantise_weights() read (_weights)
             e4 = torch.float8_e4m3fn
             self.xq, self.zq = QuantRows(s.SK, s.H, e4, device), QuantRows(s.SK, s.Hp, e4, device)
@@ -226,7 +228,7 @@ class LayerStep:
             raise ValueError("quantise_weights: the layer's GEMMs are not in 8 bits")
         E = self.s.E
         for w, qw in ((self.w_up, self.q_up), (self.w_down, self.q_down)):
-            moe_quant_weight(w[:E], *(t[:E] for t in qw.tensors()))
+            moe_quant_weight(w[:E], *(None if t is None else t[:E] for t in qw.tensors()))
         self.quantised_from = self._weights()
 
     def _check_logits(self, logits):

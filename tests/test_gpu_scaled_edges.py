@@ -189,3 +189,22 @@ def test_a_kept_norm_stays(m):
         kept.append(L.clip_gradients(1e9))
         assert captured.item() == pytest.approx(n * one, rel=1e-6)
     assert [k.item() for k in kept] == pytest.approx([n * one for n in (1.0, 2.0, 6.0, 8.0, 10.0)], rel=1e-6)
+
+
+def test_forward_only_layer(m):
+    """A layer without a backward holds the weights in the order FWD reads, and gives the same results."""
+    both, one = (layer_step(gemm="scaled", backward=b) for b in (True, False))
+    for L in (both, one):
+        L.y_all.zero_()
+        L.quantise_weights()
+        L.forward()
+    assert one.q_up.q is None and one.q_down.q_scale is None
+    assert both.q_up.q is not None
+    for k in ("z", "y", "out"):
+        assert torch.equal(getattr(one, k), getattr(both, k))
+    one.w_up.mul_(2.0)
+    with pytest.raises(ValueError, match="quantise_weights"):
+        one.forward()
+    one.quantise_weights()
+    one.step()
+    assert torch.equal(one.z, 2 * both.z)       # a scale one step up, the same 8-bit values

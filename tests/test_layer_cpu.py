@@ -139,3 +139,28 @@ def test_weights_made_in_inference_mode(layer, monkeypatch):
         L.quantise_weights()
         with pytest.raises(Reached):
             L.forward()
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_a_forward_only_layer_keeps_one_order_of_weights(layer, monkeypatch, backward):
+    """The input gradients' order is neither held nor written nor moved to the slots without a backward."""
+    L, calls = scaled_step(layer, monkeypatch, backward_enabled=backward)
+    L.q_up, L.q_down = (layer.QuantWeights(w, dgrad=backward) for w in (L.w_up, L.w_down))
+    L.quantise_weights()
+    for (w, q, q_scale, qt, qt_scale), whole in zip(calls, (L.w_up, L.w_down)):
+        assert w.shape[0] == qt.shape[0] == qt_scale.shape[0] == 6 and w.data_ptr() == whole.data_ptr()
+        assert (q is not None) == (q_scale is not None) == backward
+    assert [t is None for t in L.q_up.tensors()] == [not backward] * 2 + [False] * 2
+    moved = []
+    for name in ("moe_plan", "moe_dispatch_layout"):
+        monkeypatch.setattr(layer, name, lambda *a: None)
+    monkeypatch.setattr(layer, "moe_prefetch", lambda d, r, plan, t: moved.append(t))
+
+    def rows(*a, **k):
+        raise Reached
+    monkeypatch.setattr(layer, "moe_quant_rows", rows)
+    for name in ("cu", "dest", "src", "x_all", "xp", "xq"):
+        setattr(L, name, layer.QuantRows(1, 16, torch.float8_e4m3fn, "cpu") if name == "xq" else None)
+    with pytest.raises(Reached):
+        L.forward()
+    assert len(moved) == (8 if backward else 4) and all(t is not None for t in moved)
