@@ -147,9 +147,9 @@ class LayerStep:
         ws = max(plan_workspace_bytes(self.d), dispatch_layout_workspace_bytes(self.d))
         self.ws = torch.zeros(ws, dtype=torch.uint8, device=device)
         # the FWD and DGRAD GEMMs' scratch (split of their last round of tiles); the calls
-        # run one after another on one stream, so they share it
+        # run one after another on one stream, so they share it.  (The 8-bit ones take none.)
         self.gemm_ws = torch.empty(group_gemm_workspace_bytes(GEMM_FWD), dtype=torch.uint8,
-                                   device=device) if dtype == torch.bfloat16 else None
+                                   device=device) if dtype == torch.bfloat16 and not self.scaled else None
         self.cu = torch.zeros(s.G + 1, **i32)
         self.dest = torch.zeros(s.R * s.SK, **i32)
         self.src = torch.zeros(s.SK, **i32)

@@ -208,3 +208,14 @@ def test_forward_only_layer(m):
     one.quantise_weights()
     one.step()
     assert torch.equal(one.z, 2 * both.z)       # a scale one step up, the same 8-bit values
+
+
+def test_8_bit_layer_without_the_16_bit_scratch(m):
+    """Its products take no workspace and its weight gradients neither: none is allocated."""
+    L = layer_step(gemm="scaled")
+    assert L.gemm_ws is None and layer_step().gemm_ws is not None
+    for k in ("y_all", "dout_all", "dxp_all"):
+        getattr(L, k).normal_()
+    L.quantise_weights()
+    L.step()
+    assert L.dw_up.isfinite().all() and L.dw_up.any()
