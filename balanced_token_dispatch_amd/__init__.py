@@ -239,7 +239,8 @@ def moe_replica_grad_fold(d, rank, plan, dw, stream=None):
 
 
 # ---- 8-bit operands, router, gradient clipping ------------------------------------------------
-# These calls check their tensors: on the current device, contiguous, of the right type and size.
+# These calls check their tensors: on the current device (as a stream given to them has to be), contiguous, of
+# the right type and size.
 
 _FP8 = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
 _SCALE = (torch.uint8, torch.float8_e8m0fnu)
@@ -276,8 +277,12 @@ def _int32(*sizes):
 
 
 def _on(dev, stream):
-    """The handle of a stream, or of device dev's current one."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    """The handle of a stream of device dev, or of its current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise MoeError(f"stream of device {stream.device_index}, tensors on device {dev}")
+    return stream.cuda_stream
 
 
 def scale_row_bytes(columns):
