@@ -421,7 +421,8 @@ def moe_grad_sumsq(grads, sumsq, ws, stream=None):
 
 def moe_grad_clip(grads, sumsq, max_norm, norm=None, out=None, stream=None):
     """Scales a list of gradients by min(1, max_norm / (sqrt(sumsq) + 1e-6)), in place or into the
-    tensors of `out`; norm (one float32, optional) receives sqrt(sumsq)."""
+    tensors of `out`; norm (one float32, optional) receives sqrt(sumsq).  No two of the tensors may share
+    memory, but for a gradient and its own place in `out`: only equal addresses are found and refused."""
     dev = _current("sumsq", sumsq)
     ptr, numel, dt = _table(dev, grads)
     optr = ptr
