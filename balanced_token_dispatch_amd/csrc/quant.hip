@@ -139,9 +139,10 @@ __global__ __launch_bounds__(kQuantMaxThreads) void k_quant_rows(
         const long long at = i * width + c0 + 64 * h;
         if (c0 + 64 * h >= width) continue;
         const unsigned long long bytes = __builtin_bit_cast(unsigned long long, r.template pack<FMT>(h, es));
-        // Past the caches or not, as measured (32768 rows of 7168, us): plain bf16 rows with a copy 165
-        // so, 188 with both stores past them, 191 with neither; weighted 183, 204 (the copy alone);
-        // fp32 rows of 2048 without a copy 47, 58 through them.
+        // q past the caches or not, the copy past them, as measured (32768 rows gathered from 16384, of 7168, us; q
+        // through / past): bf16 rows with a copy 168 / 191 (193 with neither past), weighted 207 / 186, fp32 345 / 339;
+        // 32768 fp32 rows of 2048 without a copy 58 / 50.  At other shapes the two lie within a tenth of each other,
+        // either way: weighted bf16 rows of 2048 with a copy 52 / 56, of 7168 without one 138 / 128.
         if constexpr (BF16 && !WEIGHTED)
           *(unsigned long long *)(q + at) = bytes;
         else

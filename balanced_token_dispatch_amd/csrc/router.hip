@@ -3,10 +3,12 @@
 //
 // Several tokens share a wave (16 lanes each up to 256 experts) where there are enough of them.
 //
-// Latency-bound at small T (one token of 256 experts, K = 8: 3.6 us, launch included), and by the K rounds of
-// selection at large: 4096 x 256 fp32 logits 5.4 us where reading them takes 0.8, 65536 x 256 22 us where
-// it takes 11.  The gradient of 8192 x 384 bf16 logits (6.3 MB written) takes 5.2 us, of 65536 x 256 fp32
-// ones (67 MB) 21.
+// Latency-bound at small T (one token of 256 experts, K = 8: 3.4 us, launch included), and by the K rounds of
+// selection at large: 4096 x 256 fp32 logits 4.9 us where reading them takes 0.8, 65536 x 256 20 us where
+// it takes 11.  With a bias, by a 64-bit exponential and division for each expert and 64-bit keys: 65536 x 256 take
+// 52 us on the logits themselves, 56 on the logistic, 59 on the softmax over all; 4096 x 256 7.4, 7.6, 9.3.  The
+// gradient of 8192 x 384 bf16 logits (6.3 MB written) takes 4.6 us (logistic 4.9), of 65536 x 256 fp32 ones (67 MB)
+// 17.5: every row goes through LDS, also where all but K of its entries are 0.
 #include <type_traits>
 
 #include "common.hpp"
@@ -444,9 +446,10 @@ struct Router {
 
 // Lanes and experts per lane.  Few lanes share the wave's instructions among more tokens; all 64 make a
 // token's own time shortest, which is what counts while there are not two tokens for each SIMD.
-// moe_router_topk of fp32 logits, K = 8, us a launch (16 lanes / 64 lanes): 1 x 256 4.7 / 3.6, 1024 x 256
-// 5.4 / 4.2, 4096 x 256 5.4 / 5.5, 65536 x 256 22 / 42; K = 6: 1 x 64 3.2 / 3.3, 65536 x 64 12 / 37.
-// 8 experts more a lane cost: 65536 x 1024 with 32 lanes of 32 113 / 109, 65536 x 64 with 8 a lane 13 / 11.
+// moe_router_topk of fp32 logits, K = 8, us a launch (16 lanes / 64 lanes): 1 x 256 4.3 / 3.3, 1024 x 256
+// 4.9 / 4.0, 4096 x 256 4.9 / 5.2, 65536 x 256 21 / 40; K = 6: 1 x 64 2.8 / 3.0, 65536 x 64 11 / 34.
+// More experts a lane cost: 65536 x 1024, K = 16, with 32 lanes of 32 111 / 64 lanes of 16 106, 65536 x 64 with 8 a
+// lane 13 / with 4 10.
 template <bool BF16, class F>
 static void with_shape(int E, int64_t T, F f) {
   const bool few = T <= 8LL * device_cu_count();

@@ -32,9 +32,9 @@ constexpr long long kScMaxTiles = 1LL << 30;
 // v_mfma_scale_f32_16x16x128 (every weight byte is used once per 16 rows, so staging it in LDS would
 // gain nothing), and the W sums are added in wave order through LDS.
 //
-// Bound by the weights' bytes: 512 rows on 264 experts of 7168 x 2048 read 3.27 GB in 535 us, 6.1 TB/s,
-// where torch's copy of 4 GiB moves 4.8 TB/s.  With few weights, by the launch and two trips to memory:
-// 6 rows on 6 experts of 2048 x 1408 (17 MB, 3 us at that rate) take 8.2 us.
+// Bound by the weights' bytes: 512 rows on 264 experts of 7168 x 2048 read 3.27 GB in 531 to 560 us, 6.2 to 5.8
+// TB/s, where torch's copy of 4 GiB moves 4.8 TB/s.  With few weights, by the launch and two trips to memory:
+// 6 rows on 6 experts of 2048 x 1408 (17 MB, 3 us at that rate) take 7.7 us.
 constexpr int kFewRows = 16, kFewCols = 16;
 
 // Segment table in LDS: sCu (clamped to [0, M_total]) and sStart[rho] = first tile of `tile`
@@ -179,12 +179,12 @@ __global__ __launch_bounds__(64 * W) void k_scaled_few(
 // 128-byte lines of each operand's rows, loaded straight into LDS (buffer_load .. lds), in a ring of
 // R stages.
 //
-// What bounds it.  32768 rows on 264 experts of 7168 x 2048 (4.24 GB) take 821 us, 5.2 TB/s: memory.
-// With one expert (32768 x 7168 x 2048, 256 x 256 tiles) 374 to 390 us, 2.6 to 2.5 PFLOP/s, for normal
+// What bounds it.  32768 rows on 264 experts of 7168 x 2048 (4.24 GB) take 829 us, 5.1 TB/s: memory.
+// With one expert (32768 x 7168 x 2048, 256 x 256 tiles) 372 to 390 us, 2.6 to 2.5 PFLOP/s, for normal
 // and for random bytes, where torch's library product takes 310 to 325 and the bare matrix
 // instructions reach 4.7-5.0: the chip's power sets the clock there (1.75 GHz; 303 us on zeros, the
 // library 229), and the matrix units are busy 61% of the cycles.  Between them, with 1408 of
-// contraction (24576 rows, 68 experts, 128 x 256 tiles: 111 us, floor 56), what costs is the tiles' last
+// contraction (24576 rows, 68 experts, 128 x 256 tiles: 107 us, floor 56), what costs is the tiles' last
 // rows (15% more than the rows there are), the last round of tiles (8 for 7.1) and 11 stages a tile
 // against one start of the ring and one store of the results.
 constexpr int kTileThreads = 256, kTileWaves = 4;
@@ -441,7 +441,7 @@ __global__ __launch_bounds__(kTileThreads) void k_scaled_tiles(
   //   wait until only those are in flight (stage s + 1 has landed), barrier;
   //   sub-step 1: issues the other loads; reads all fragments and the scales of stage s + 1, those of its
   //     sub-step 1 into registers that alternate from stage to stage; asks for the next piece of scales.
-  // (32768 x 1 x 7168 x 2048: 381 us; loads over one sub-step 403, over both 384.)
+  // (32768 x 1 x 7168 x 2048, all in one run: 381 us; loads over one sub-step 403, over both 384.)
   // Loads and stores complete in order, so where the stores of the tile before came after the loads
   // waited for (stage 0), they are counted in; the loads of the scales only make a wait stricter.
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
@@ -709,20 +709,27 @@ static void launch_tiles(const uint8_t *a, const uint8_t *as, const uint8_t *b,
 
 // Which kernel: by the rows a segment has on average and by how many tiles of a size there are
 // likely to be (a full tile for each of its rows, and half a tile more for each segment), since the
-// segments themselves are only known on the device.  Measured, us a launch (rows, segments,
-// contraction x columns; few rows / 64 x 64 / 64 x 128 / 128 x 256 / 256 x 256 tiles):
-//   6, 68, 2048x1408          8.2 /  9.9 / 11.6 / 17.6 / 24
-//   16, 1, 7168x7168           17 /   22 /   27 /   44 / 68
-//   512, 264, 7168x2048       545 /  544 /  542 /  541 / 658
-//   256, 1, 4096x4096          53 / 15.2 / 17.8 / 30.1 / 45
-//   1000, 16, 1024x1024        18 / 11.5 /  9.2 / 14.3 / 17.3
-//   1024, 68, 2048x1408        53 /   43 /   40 /   43 / 55
-//   4096, 264, 7168x2048      971 /  661 /  666 /  693 / 826
-//   5003, 18, 1408x2064         - /   55 /   35 /   28 / 39
-//   24576, 68, 1408x2048        - /  232 /  159 /  114 / 118
-//   32768, 264, 7168x2048       - / 1474 / 1111 /  826 / 942
-//   2000, 1, 7168x7168          - /  252 /  155 /  100 / 92
-//   32768, 1, 7168x2048         - / 1146 /  734 /  446 / 395
+// segments themselves are only known on the device.  Measured, us a launch in a graph (rows, segments,
+// contraction x columns; few rows / 64 x 64 / 64 x 128 / 128 x 256 / 256 x 256 tiles; * the rule's):
+//   6, 68, 2048x1408         *7.7 / 10.1 / 12.0 / 17.7 / 24
+//   16, 1, 7168x7168         * 17 /   22 /   28 /   45 / 68
+//   512, 264, 7168x2048      *560 /  525 /  527 /  529 / 566
+//   256, 1, 4096x4096          53 /*15.6 / 17.7 / 32.3 / 45
+//   1000, 16, 1024x1024        18 / 11.8 /  8.8*/ 14.0 / 17.7
+//   1024, 68, 2048x1408        49 /   41 /   34*/   38 / 44
+//   4096, 264, 7168x2048      954 /  649 /  658*/  671 / 717
+//   5003, 18, 1408x2064         - /   61 /   37 /  *31 / 26
+//   24576, 68, 1408x2048        - /  245 /  156 / *107 / 103
+//   32768, 264, 7168x2048       - / 1433 / 1111 / *831 / 848
+//   2000, 1, 7168x7168       1206 /  241 /  148 /  101 / 89*
+//   32768, 1, 7168x2048         - / 1097 /  713 /  440 / 375*
+// The rows of these lie on all of their segments.  Where most segments are empty, as in a rank's layout (its
+// E / R home experts and its slots of E + B segments), the average is far below what a segment with rows has,
+// and the rule takes a kernel for shorter ones; the host knows no better from these arguments (rows on 9 segments):
+//   2048 on 9 of 264, 7168x2048  *362 / 93 / 64 / 52 / 81
+//   32768 on 9 of 264, 7168x2048    - / 1112 / 734 / *470 / 424
+//   1536 on 9 of 68, 2048x1408     58 / 23 / *18 / 20 / 29
+//   24576 on 9 of 68, 2048x1408     - / 210 / 124 / *83 / 83
 template <int FMT>
 static void launch_scaled(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
                           const int32_t *cu, uint16_t *out, int G, int M_total, int K, int N,
