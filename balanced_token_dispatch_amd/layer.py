@@ -217,9 +217,14 @@ class LayerStep:
     @property
     def weights_quantised(self):
         """Whether the 8-bit weights are the present ones', as far as torch counts the changes: not those by
-        kernels of other libraries, fused optimizers or .data."""
+        kernels of other libraries, fused optimizers or .data.  To be set by a caller that writes the 8-bit
+        weights itself."""
         was = self.quantised_from
         return was is not None and all(w is v and n == k for (w, n), (v, k) in zip(self._weights(), was))
+
+    @weights_quantised.setter
+    def weights_quantised(self, done):
+        self.quantised_from = self._weights() if done else None
 
     def quantise_weights(self):
         """The home experts' weights into 8 bits (gemm="scaled"): after every change of w_up or w_down.
@@ -229,7 +234,7 @@ class LayerStep:
         E = self.s.E
         for w, qw in ((self.w_up, self.q_up), (self.w_down, self.q_down)):
             moe_quant_weight(w[:E], *(None if t is None else t[:E] for t in qw.tensors()))
-        self.quantised_from = self._weights()
+        self.weights_quantised = True
 
     def _check_logits(self, logits):
         if tuple(logits.shape) != (self.s.S, self.s.E):

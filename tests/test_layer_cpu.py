@@ -164,3 +164,18 @@ def test_a_forward_only_layer_keeps_one_order_of_weights(layer, monkeypatch, bac
     with pytest.raises(Reached):
         L.forward()
     assert len(moved) == (8 if backward else 4) and all(t is not None for t in moved)
+
+
+def test_weights_put_into_8_bits_elsewhere(layer, monkeypatch):
+    """A caller that writes q_up and q_down itself (from a checkpoint in 8 bits) says so."""
+    L, calls = scaled_step(layer, monkeypatch)
+    L.weights_quantised = True
+    assert not calls and L.weights_quantised
+    with pytest.raises(Reached):
+        L.forward()
+    L.w_up.add_(1.0)
+    assert not L.weights_quantised
+    L.weights_quantised = True
+    L.weights_quantised = False
+    with pytest.raises(ValueError, match="quantise_weights"):
+        L.forward()
