@@ -25,6 +25,7 @@ F32, BF16 = 0, 1
 GEMM_FWD, GEMM_DGRAD, GEMM_WGRAD = 0, 1, 2
 E4M3, E5M2 = 0, 1
 SCORES = {"softmax_topk": 0, "softmax": 1, "sigmoid": 2}   # moe_score
+NORMS = {"layer": 0, "rms": 1}                             # moe_norm_kind
 
 EXPORTS = ("moe_status_string", "moe_plan_words", "moe_plan_workspace_bytes", "moe_plan",
            "moe_dispatch_layout_workspace_bytes", "moe_dispatch_layout", "moe_prefetch",
@@ -34,7 +35,9 @@ EXPORTS = ("moe_status_string", "moe_plan_words", "moe_plan_workspace_bytes", "m
            "moe_group_gemm_gather", "moe_scale_row_bytes", "moe_quant_rows", "moe_quant_weight",
            "moe_group_gemm_scaled", "moe_router_topk",
            "moe_router_backward", "moe_grad_sumsq_workspace_bytes", "moe_grad_sumsq",
-           "moe_grad_clip")
+           "moe_grad_clip", "moe_dropout", "moe_layer_norm", "moe_layer_norm_backward_workspace_bytes",
+           "moe_layer_norm_backward", "moe_expert_counts", "moe_balance_loss_workspace_bytes",
+           "moe_balance_loss", "moe_balance_loss_backward")
 
 PLAN_NOALLOC_SCRATCH_BYTES = 4 << 20   # MOE_PLAN_NOALLOC_SCRATCH_BYTES in moe.h
 
@@ -86,6 +89,20 @@ _lib.moe_router_backward.argtypes = [ctypes.c_int, ctypes.c_int, _I64, _I32, _I3
                                      ctypes.c_float, _P, _P]
 _lib.moe_grad_sumsq.argtypes = [_I32, _P, _P, _P, _P, _P, _SZ, _P]
 _lib.moe_grad_clip.argtypes = [_I32, _P, _P, _P, _P, ctypes.c_double, _P, _P, _P]
+_F64 = ctypes.c_double
+_lib.moe_dropout.argtypes = [ctypes.c_int, _I64, _P, _P, _F64, _P, _I64, _P, _P]
+_lib.moe_layer_norm.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, _I64, _I64, _P, _P, _P, _P, _F64, _F64,
+                                _P, _I64, _P, _P, _P, _P, _P]
+_lib.moe_layer_norm_backward_workspace_bytes.restype = _SZ
+_lib.moe_layer_norm_backward_workspace_bytes.argtypes = [_I64, _I64]
+_lib.moe_layer_norm_backward.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, _I64, _I64, _P, _P, _P, _P, _P,
+                                         _P, _F64, _P, _I64, _P, _P, _P, _P, _I32, _P, _SZ, _P]
+_lib.moe_expert_counts.argtypes = [_I64, _I32, _I32, _P, _I32, _P, _P, _P]
+_lib.moe_balance_loss_workspace_bytes.restype = _SZ
+_lib.moe_balance_loss_workspace_bytes.argtypes = [_I64, _I32]
+_lib.moe_balance_loss.argtypes = [ctypes.c_int, ctypes.c_int, _I64, _I32, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P]
+_lib.moe_balance_loss_backward.argtypes = [ctypes.c_int, ctypes.c_int, _I64, _I32, _P, _I32, _P, _P, _P, _P, _P, _P,
+                                           _P]
 for _n in EXPORTS[3:]:
     if _n.endswith("_bytes"):
         continue
@@ -238,7 +255,7 @@ def moe_replica_grad_fold(d, rank, plan, dw, stream=None):
                                       dw[0].numel(), _stream(stream)), "moe_replica_grad_fold")
 
 
-# ---- 8-bit operands, router, gradient clipping ------------------------------------------------
+# ---- 8-bit operands, router, gradient clipping, norm, dropout, balance loss ---------------------
 # These calls check their tensors: on the current device (as a stream given to them has to be), contiguous, of
 # the right type and size.
 
@@ -437,3 +454,152 @@ def moe_grad_clip(grads, sumsq, max_norm, norm=None, out=None, stream=None):
     _check(_lib.moe_grad_clip(len(grads), _at(ptr), _at(numel), _at(dt),
                               _take(dev, "sumsq", sumsq, (torch.float64,), 1), max_norm, np_, _at(optr),
                               _on(dev, stream)), "moe_grad_clip")
+
+
+def _maybe(dev, name, t, dtypes, numel):
+    """The address of a tensor that may be left out."""
+    return None if t is None else _take(dev, name, t, dtypes, numel)
+
+
+def _drop_args(dev, p, rng, offset):
+    """(p, address of the seed and offset, the further offset) of a dropout."""
+    if not 0.0 <= p <= 1.0:
+        raise MoeError(f"p {p}, expected 0 to 1")
+    if p > 0.0 and rng is None:
+        raise MoeError("dropout without rng (int64: seed, offset)")
+    if not -(1 << 63) <= offset < 1 << 63:
+        raise MoeError(f"offset {offset}, expected a 64-bit number")
+    return p, _maybe(dev, "rng", rng, (torch.int64,), 2), offset
+
+
+def moe_dropout(x, out, p, rng, residual=None, offset=0, stream=None):
+    """out = residual + x with a share p of its values 0 and the others scaled; the mask is a function of
+    rng (two int64 on the device: seed, offset), `offset` and each value's place.  The gradient of x is the
+    same call on out's gradient, without the residual."""
+    dev = _current("x", x)
+    p, rp, offset = _drop_args(dev, p, rng, offset)
+    same = (x.dtype,)
+    _check(_lib.moe_dropout(_dtype(x), x.numel(), _take(dev, "x", x, _FLOATS, None),
+                            _maybe(dev, "residual", residual, same, x.numel()), p, rp, offset,
+                            _take(dev, "out", out, same, x.numel()), _on(dev, stream)), "moe_dropout")
+
+
+def _kind(kind):
+    if kind not in NORMS:
+        raise MoeError(f"kind {kind!r}, expected one of {', '.join(NORMS)}")
+    return NORMS[kind]
+
+
+def _rows(name, x):
+    """Rows and width of x: its last dimension is a row."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise MoeError(f"{name}: shape {tuple(x.shape)}, expected rows of at least one value")
+    return x.numel() // x.shape[-1], x.shape[-1]
+
+
+def moe_layer_norm(x, weight, y, bias=None, eps=1e-5, kind="layer", residual=None, total=None, mean=None, rstd=None,
+                   p=0.0, rng=None, offset=0, stream=None):
+    """y = (h - mean) rstd weight + bias over the last dimension, h = residual + dropout(x) (see moe_dropout);
+    total receives h, mean and rstd (fp32) what the backward takes.  kind "rms": mean 0."""
+    dev = _current("x", x)
+    rows, width = _rows("x", x)
+    p, rp, offset = _drop_args(dev, p, rng, offset)
+    same, n = (x.dtype,), x.numel()
+    _check(_lib.moe_layer_norm(_dtype(x), _kind(kind), _dtype(weight), rows, width, _take(dev, "x", x, _FLOATS, None),
+                               _maybe(dev, "residual", residual, same, n),
+                               _take(dev, "weight", weight, _FLOATS, width),
+                               _maybe(dev, "bias", bias, (weight.dtype,), width), eps, p, rp, offset,
+                               _maybe(dev, "total", total, same, n), _take(dev, "y", y, same, n),
+                               _maybe(dev, "mean", mean, (torch.float32,), rows),
+                               _maybe(dev, "rstd", rstd, (torch.float32,), rows), _on(dev, stream)), "moe_layer_norm")
+
+
+def layer_norm_backward_workspace_bytes(rows, width):
+    return _lib.moe_layer_norm_backward_workspace_bytes(rows, width)
+
+
+def moe_layer_norm_backward(total, weight, rstd, dy, dx, dweight=None, ws=None, dbias=None, mean=None, kind="layer",
+                            dtotal=None, dresidual=None, accumulate=False, p=0.0, rng=None, offset=0, stream=None):
+    """The gradients of moe_layer_norm: dx, dresidual (of the residual; dx itself where p is 0), dweight and dbias
+    (fp32, added to what they hold with accumulate).  total is h, dtotal the gradient that reaches it by other ways;
+    ws: scratch of layer_norm_backward_workspace_bytes(rows, width) bytes for dweight and dbias."""
+    dev = _current("total", total)
+    rows, width = _rows("total", total)
+    p, rp, offset = _drop_args(dev, p, rng, offset)
+    same, n, f32 = (total.dtype,), total.numel(), (torch.float32,)
+    _check(_lib.moe_layer_norm_backward(
+        _dtype(total), _kind(kind), _dtype(weight), rows, width, _take(dev, "total", total, _FLOATS, None),
+        _take(dev, "weight", weight, _FLOATS, width), _maybe(dev, "mean", mean, f32, rows),
+        _take(dev, "rstd", rstd, f32, rows), _take(dev, "dy", dy, same, n), _maybe(dev, "dtotal", dtotal, same, n),
+        p, rp, offset, _take(dev, "dx", dx, same, n), _maybe(dev, "dresidual", dresidual, same, n),
+        _maybe(dev, "dweight", dweight, f32, width), _maybe(dev, "dbias", dbias, f32, width), int(bool(accumulate)),
+        None if ws is None else _take(dev, "ws", ws, (ws.dtype,), None),
+        0 if ws is None else ws.numel() * ws.element_size(), _on(dev, stream)), "moe_layer_norm_backward")
+
+
+def _sequences(dev, cu_tokens):
+    """(number of sequences, address of their bounds)."""
+    if cu_tokens is None:
+        return 1, None
+    cp = _take(dev, "cu_tokens", cu_tokens, (torch.int32,), None)
+    n = cu_tokens.numel() - 1
+    if not 1 <= n <= 1 << 20:
+        raise MoeError(f"cu_tokens: {n} sequences, expected 1 to 2^20")
+    return n, cp
+
+
+def moe_expert_counts(topk_idx, counts, cu_tokens=None, stream=None):
+    """counts[b, e] = copies that the tokens of sequence b, [cu_tokens[b], cu_tokens[b + 1]), send to expert e;
+    topk_idx [T, K].  Without cu_tokens all tokens are one sequence."""
+    if topk_idx.dim() != 2 or counts.dim() < 1:
+        raise MoeError(f"moe_expert_counts: topk_idx of shape {tuple(topk_idx.shape)}, counts {tuple(counts.shape)}, "
+                       "expected [T, K] and [sequences, E]")
+    dev = _current("topk_idx", topk_idx)
+    (T, K), E = topk_idx.shape, counts.shape[-1]
+    n, cp = _sequences(dev, cu_tokens)
+    _int32(K, E)
+    _check(_lib.moe_expert_counts(T, E, K, _take(dev, "topk_idx", topk_idx, (torch.int32,), None), n, cp,
+                                  _take(dev, "counts", counts, (torch.int32,), n * E), _on(dev, stream)),
+           "moe_expert_counts")
+
+
+def balance_loss_workspace_bytes(tokens, sequences=1):
+    _int32(sequences)
+    return _lib.moe_balance_loss_workspace_bytes(tokens, sequences)
+
+
+def _logits(name, logits, cu_tokens):
+    """Device, T, E, number of sequences and the address of their bounds."""
+    if logits.dim() != 2:
+        raise MoeError(f"{name}: logits has {logits.dim()} dimensions, expected 2")
+    dev = _current("logits", logits)
+    T, E = logits.shape
+    _int32(E)
+    return (dev, T, E, *_sequences(dev, cu_tokens))
+
+
+def moe_balance_loss(logits, counts, balance, ws, zloss=None, score="softmax_topk", cu_tokens=None, stream=None):
+    """balance[b] = E / sum(counts[b]) * mean over the sequence's tokens of sum_e counts[b, e] P[s, e], and
+    zloss[b] = mean logsumexp^2, from logits [T, E]; P: softmax, or the logistic over its sum (score "sigmoid").
+    ws: scratch of balance_loss_workspace_bytes(T, sequences) bytes."""
+    dev, T, E, n, cp = _logits("moe_balance_loss", logits, cu_tokens)
+    f32 = (torch.float32,)
+    _check(_lib.moe_balance_loss(_dtype(logits), _score(score), T, E, _take(dev, "logits", logits, _FLOATS, None), n, cp,
+                                 _take(dev, "counts", counts, (torch.int32,), n * E),
+                                 _take(dev, "balance", balance, f32, n), _maybe(dev, "zloss", zloss, f32, n),
+                                 _take(dev, "ws", ws, (ws.dtype,), None), ws.numel() * ws.element_size(),
+                                 _on(dev, stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_backward(logits, counts, dlogits, dbalance=None, dzloss=None, score="softmax_topk",
+                              cu_tokens=None, add=None, stream=None):
+    """dlogits = add + the gradient of sum_b dbalance[b] balance[b] + dzloss[b] zloss[b], the counts held fixed; add
+    may be dlogits itself.  Rows of tokens in no sequence are left as they are."""
+    dev, T, E, n, cp = _logits("moe_balance_loss_backward", logits, cu_tokens)
+    f32, same = (torch.float32,), (logits.dtype,)
+    _check(_lib.moe_balance_loss_backward(_dtype(logits), _score(score), T, E,
+                                          _take(dev, "logits", logits, _FLOATS, None), n, cp,
+                                          _take(dev, "counts", counts, (torch.int32,), n * E),
+                                          _maybe(dev, "dbalance", dbalance, f32, n), _maybe(dev, "dzloss", dzloss, f32, n),
+                                          _maybe(dev, "add", add, same, T * E), _take(dev, "dlogits", dlogits, same, T * E),
+                                          _on(dev, stream)), "moe_balance_loss_backward")

@@ -1,0 +1,85 @@
+// Runs of eight values as a thread's step, at any alignment, and checks of what a call's tensors share.
+#pragma once
+
+#include "common.hpp"
+
+namespace moe {
+
+// n (1 to 8) values of a tensor from element i, as fp32; the rest 0.  Eight are read in vectors at any
+// alignment of the element.
+template <bool BF16>
+__device__ inline void load_8(const void *p, long long i, int n, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint16_t *q = (const uint16_t *)p + i;
+    if (n >= 8) {
+      u32x4 t;
+      __builtin_memcpy(&t, q, 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[2 * j] = bf16_lo(t[j]), v[2 * j + 1] = bf16_hi(t[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < n ? __builtin_bit_cast(float, (uint32_t)q[j] << 16) : 0.0f;
+    }
+  } else {
+    const float *q = (const float *)p + i;
+    if (n >= 8) {
+      f32x4 t[2];
+      __builtin_memcpy(t, q, 32);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = t[j >> 2][j & 3];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < n ? q[j] : 0.0f;
+    }
+  }
+}
+
+// The first n of eight values to a tensor from element i on, rounded to its type.
+template <bool BF16>
+__device__ inline void store_8(void *p, long long i, int n, const float (&v)[8]) {
+  if constexpr (BF16) {
+    uint16_t *q = (uint16_t *)p + i;
+    u32x4 t;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+    if (n >= 8) {
+      __builtin_memcpy(q, &t, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) q[j] = (uint16_t)(j & 1 ? t[j >> 1] >> 16 : t[j >> 1]);
+    }
+  } else {
+    float *q = (float *)p + i;
+    if (n >= 8) {
+      const f32x4 t[2] = {{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}};
+      __builtin_memcpy(q, t, 32);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) q[j] = v[j];
+    }
+  }
+}
+
+// Whether two ranges share memory.  Ranges that are the same one are told apart by `same`.
+inline bool shares(const void *a, size_t an, const void *b, size_t bn, bool same) {
+  if (!a || !b || !an || !bn) return false;
+  if (same && a == b) return false;
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + bn && y < x + an;
+}
+
+// Whether output o (bytes long) shares memory with no input but, whole, one of `same`, and no other range.
+struct Range {
+  const void *p;
+  size_t bytes;
+  bool may_be;  // the output may be this very range
+};
+inline bool stands_alone(const void *o, size_t bytes, const Range *r, int n) {
+  for (int i = 0; i < n; ++i)
+    if (shares(o, bytes, r[i].p, r[i].bytes, r[i].may_be && r[i].bytes == bytes)) return false;
+  return true;
+}
+
+}  // namespace moe

@@ -24,6 +24,9 @@
  *   around it: moe_router_topk (the ids and weights above, from the gate's
  *             logits) and moe_router_backward; moe_grad_sumsq and
  *             moe_grad_clip before the optimizer
+ *   in a block: moe_layer_norm on the way in (residual sum and dropout taken
+ *             along), moe_dropout with the residual sum on the way out;
+ *             moe_expert_counts and moe_balance_loss beside the router
  *
  * Conventions shared by every entry point
  *   - Every pointer argument is DEVICE memory owned by the caller, except
@@ -90,6 +93,11 @@ typedef enum {
   MOE_SCORE_SOFTMAX = 1,      /* softmax over all E logits, not renormalised  */
   MOE_SCORE_SIGMOID = 2       /* logistic of each logit, over the chosen sum  */
 } moe_score;
+
+typedef enum {
+  MOE_NORM_LAYER = 0, /* (h - mean) / sqrt(variance + eps)                    */
+  MOE_NORM_RMS = 1    /* h / sqrt(mean of squares + eps)                      */
+} moe_norm_kind;
 
 typedef enum {
   MOE_GEMM_FWD = 0,   /* out[seg] = a[seg] @ W[rho]                          */
@@ -501,6 +509,121 @@ moe_status_t moe_grad_sumsq(int32_t n, const void *const *grads, const int64_t *
 moe_status_t moe_grad_clip(int32_t n, const void *const *grads, const int64_t *numel,
                            const moe_dtype *dtype, const double *sumsq, double max_norm,
                            float *norm, void *const *outs, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Dropout.  The mask is never stored: it is a function of a seed, an offset
+ * and the element's place, worked out again wherever it is needed.  Element i
+ * of a row-major tensor takes 16 bits of Philox4x32-10 (Salmon, Moraes, Dror
+ * and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) with counter
+ * (i / 8, rng[1] + offset), low words first, and key rng[0]: the half i % 8 of
+ * the four words, low halves first.  It is dropped (0, whatever it held) where
+ * these are below t = floor(65536 p + 1/2), and scaled by 65536 / (65536 - t)
+ * (fp32) elsewhere: p is met to within 2^-17, and the mean exactly for the p
+ * that is met.
+ *   rng    2 int64 (seed, offset), device memory, read when the kernel runs, so
+ *          that a captured graph draws anew where rng[1] moves between replays.
+ *   offset is added to rng[1]: one for each dropout of a step.  Two tensors
+ *          with the same seed and sum share their mask.
+ *   p      in [0, 1]; with p = 0 rng is not read and may be NULL.
+ * The pages name no dropout, norm or balance loss; these are the usual parts
+ * of a transformer block around the layer.
+ *
+ * moe_dropout -- out = residual + drop(x), the sum in fp32 and rounded once.
+ * Its own backward: drop(dout) with the same rng and offset is the gradient of
+ * x, dout that of the residual.
+ *   x, residual (nullable), out: n values of dtype, aligned to the element; out
+ *   may be x or residual itself and overlaps them in no other way.
+ * ------------------------------------------------------------------------- */
+moe_status_t moe_dropout(moe_dtype dtype, int64_t n, const void *x, const void *residual, double p,
+                         const int64_t *rng, int64_t offset, void *out, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_layer_norm -- rows h = residual + drop(x) (either part may be absent),
+ * normalised: y = (h - mean) rstd weight + bias, rstd = 1 / sqrt(var + eps), var
+ * the mean of (h - mean)^2; MOE_NORM_RMS takes 0 for the mean.  All in fp32 on
+ * the unrounded h; y and total (h) are rounded once.
+ *   x, residual (nullable), total, y  [rows, width] of dtype.  total may be NULL
+ *         where h is x (no residual, p = 0).  total and y may each be x or
+ *         residual itself; nothing overlaps in another way.
+ *   weight, bias (nullable)  [width] of w_dtype.
+ *   mean, rstd  [rows] fp32, nullable (not kept); mean NULL for MOE_NORM_RMS.
+ *   rows >= 0, 1 <= width <= 2^22, eps >= 0; all aligned to their element.
+ * A row with a NaN or infinity gives NaN.
+ *
+ * moe_layer_norm_backward -- with xh = (total - mean) rstd and g = dy weight:
+ *   dh = rstd (g - mean(g) - xh mean(g xh)) + dtotal    (RMS: without mean(g))
+ *   dresidual = dh, dx = drop(dh), each rounded once;
+ *   dweight = sum over rows of dy xh, dbias = sum of dy, in fp32 and a fixed
+ *   order, added to what is there where accumulate is 1.
+ *   total, dy, dtotal (nullable: the gradient that reaches h by other ways),
+ *   dx, dresidual (nullable)  [rows, width] of dtype; dx and dresidual may each
+ *   be dy or dtotal itself and overlap nothing in another way.
+ *   dweight, dbias  [width] fp32, nullable.  mean is NULL for MOE_NORM_RMS.
+ *   ws    >= moe_layer_norm_backward_workspace_bytes(rows, width) bytes, 16-byte
+ *         aligned, used while dweight or dbias is given (else it may be NULL).
+ *         Calls that share one workspace must not overlap.
+ *   Without rows the sums are 0.
+ * ------------------------------------------------------------------------- */
+moe_status_t moe_layer_norm(moe_dtype dtype, moe_norm_kind kind, moe_dtype w_dtype, int64_t rows,
+                            int64_t width, const void *x, const void *residual, const void *weight,
+                            const void *bias, double eps, double p, const int64_t *rng,
+                            int64_t offset, void *total, void *y, float *mean, float *rstd,
+                            hipStream_t stream);
+size_t moe_layer_norm_backward_workspace_bytes(int64_t rows, int64_t width);
+moe_status_t moe_layer_norm_backward(moe_dtype dtype, moe_norm_kind kind, moe_dtype w_dtype,
+                                     int64_t rows, int64_t width, const void *total,
+                                     const void *weight, const float *mean, const float *rstd,
+                                     const void *dy, const void *dtotal, double p,
+                                     const int64_t *rng, int64_t offset, void *dx, void *dresidual,
+                                     float *dweight, float *dbias, int32_t accumulate, void *ws,
+                                     size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Sequences.  The calls below take the tokens of n_seq packed sequences:
+ * sequence b is the tokens [cu_tokens[b], cu_tokens[b+1]) (int32 [n_seq + 1],
+ * not falling, within [0, T]; an empty one is allowed).  With cu_tokens NULL,
+ * n_seq is 1 and the sequence all T tokens.  Tokens before the first sequence
+ * and behind the last take no part.  Numbers that fall or leave [0, T] give
+ * unspecified results; every access stays inside the buffers.
+ *
+ * moe_expert_counts -- counts[b, e] = copies (s, k) of sequence b's tokens with
+ * topk_idx[s, k] == e; an id outside [0, E) is not counted.  Ranks that share
+ * a loss add their counts (an all-reduce of int32) before moe_balance_loss.
+ *   topk_idx [T, K] int32, counts [n_seq, E] int32 (set, not added to).
+ *
+ * moe_balance_loss -- for each sequence, with P[s, e] the softmax of token s's
+ * logits (SOFTMAX and SOFTMAX_TOPK) or their logistic over its sum (SIGMOID):
+ *   balance[b] = E / (sum_e counts[b, e]) * mean_s sum_e counts[b, e] P[s, e]
+ *                (1 where counts and P are even; 0 without tokens or counts)
+ *   zloss[b]   = mean_s (log sum_e exp logits[s, e])^2     (any score)
+ * A token whose logits are all -inf adds 0 to both.  A NaN logit makes its
+ * sequence's losses NaN, +inf those that take a softmax or the logarithm.
+ *   logits [T, E] of dtype; balance, zloss (nullable) [n_seq] fp32.
+ *   ws     >= moe_balance_loss_workspace_bytes(T, n_seq) bytes, 8-byte aligned.
+ *          Calls that share one workspace must not overlap.
+ *
+ * moe_balance_loss_backward -- dlogits = add + the gradient of
+ * sum_b dbalance[b] balance[b] + dzloss[b] zloss[b], counts held fixed; one
+ * rounding.  Rows of tokens in no sequence are left as they are.
+ *   dbalance, dzloss [n_seq] fp32, either may be NULL (0); add (nullable, the
+ *   gradient from elsewhere, moe_router_backward's) and dlogits [T, E] of dtype;
+ *   dlogits may be add itself, not logits.
+ *
+ *   0 <= T < 2^31, 1 <= E <= 1024, 1 <= K <= E, T K < 2^31, 1 <= n_seq <= 2^20.
+ * ------------------------------------------------------------------------- */
+moe_status_t moe_expert_counts(int64_t T, int32_t E, int32_t K, const int32_t *topk_idx,
+                               int32_t n_seq, const int32_t *cu_tokens, int32_t *counts,
+                               hipStream_t stream);
+size_t moe_balance_loss_workspace_bytes(int64_t T, int32_t n_seq);
+moe_status_t moe_balance_loss(moe_dtype dtype, moe_score score, int64_t T, int32_t E,
+                              const void *logits, int32_t n_seq, const int32_t *cu_tokens,
+                              const int32_t *counts, float *balance, float *zloss, void *ws,
+                              size_t ws_bytes, hipStream_t stream);
+moe_status_t moe_balance_loss_backward(moe_dtype dtype, moe_score score, int64_t T, int32_t E,
+                                       const void *logits, int32_t n_seq,
+                                       const int32_t *cu_tokens, const int32_t *counts,
+                                       const float *dbalance, const float *dzloss, const void *add,
+                                       void *dlogits, hipStream_t stream);
 
 #ifdef __cplusplus
 }
