@@ -362,8 +362,8 @@ extern "C" moe_status_t moe_balance_loss(moe_dtype dtype, moe_score score, int64
   if ((uintptr_t)logits % size || ((uintptr_t)counts | (uintptr_t)balance | (uintptr_t)zloss) % 4) return MOE_EINVAL;
   if (ws_bytes < need) return MOE_ENOSPACE;
   const size_t o_bytes = (size_t)n_seq * 4;
-  const Range in[] = {{logits, (size_t)T * E * size, false}, {counts, o_bytes * E, false},
-                      {cu_tokens, o_bytes + 4, false}, {ws, need, false}, {zloss, o_bytes, false}};
+  const Range in[] = {{logits, (size_t)T * E * size}, {counts, o_bytes * E},
+                      {cu_tokens, o_bytes + 4}, {ws, need}, {zloss, o_bytes}};
   if (!stands_alone(balance, o_bytes, in, 5) || !stands_alone(zloss, o_bytes, in, 4) || !stands_alone(ws, need, in, 3))
     return MOE_EINVAL;
   const Sequences s{cu_tokens, n_seq, (int)T};
@@ -394,9 +394,9 @@ extern "C" moe_status_t moe_balance_loss_backward(moe_dtype dtype, moe_score sco
   if (((uintptr_t)logits | (uintptr_t)add | (uintptr_t)dlogits) % size ||
       ((uintptr_t)counts | (uintptr_t)dbalance | (uintptr_t)dzloss) % 4)
     return MOE_EINVAL;
-  const Range in[] = {{add, bytes, true}, {logits, bytes, false}, {counts, o_bytes * E, false},
-                      {cu_tokens, o_bytes + 4, false}, {dbalance, o_bytes, false}, {dzloss, o_bytes, false}};
-  if (!stands_alone(dlogits, bytes, in, 6)) return MOE_EINVAL;
+  const Range in[] = {{add, bytes, true}, {logits, bytes}, {counts, o_bytes * E},
+                      {cu_tokens, o_bytes + 4}, {dbalance, o_bytes}, {dzloss, o_bytes}};
+  if (!stands_alone(dlogits, bytes, in, 6, true)) return MOE_EINVAL;
   const Sequences s{cu_tokens, n_seq, (int)T};
   auto go = [&](auto bf16, auto sigmoid) {
     with_lanes(E, [&](auto l, auto v) {

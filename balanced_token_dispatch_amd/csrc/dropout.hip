@@ -16,8 +16,9 @@ __global__ __launch_bounds__(kDropThreads) void k_dropout(const void *x, const v
     float v[8], r[8];
     load_8<BF16>(x, 8 * b, m, v);
     if (RES) load_8<BF16>(residual, 8 * b, m, r);
-    if (DROP) drop_8(philox((unsigned long long)b, key), d, v);
-    if (RES)
+    if (DROP && RES) drop_8(philox((unsigned long long)b, key), d, v, r);
+    if (DROP && !RES) drop_8(philox((unsigned long long)b, key), d, v);
+    if (!DROP && RES)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += r[j];
     store_8<BF16>(out, 8 * b, m, v);

@@ -7,25 +7,73 @@
 #include <type_traits>
 
 #include "dropout.hpp"
+#include "lanes.hpp"
 
 namespace moe {
 
-constexpr int kNormMaxWaves = 16;
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormMaxWaves = kNormMaxThreads / kWave;
+constexpr int kNormParts = 1024; // at most as many sums of columns a backward call makes, then adds up
+constexpr int kColParts = 64;    // the same of rows that are read again
+constexpr int kNormLanesThreads = 256;  // where several rows share a workgroup
 
-// Sum over the WAVES waves of a row, the same in all its threads, in a fixed order.
-template <int WAVES>
-__device__ inline float row_sum(float v, float *part) {
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) v += __shfl_xor(v, off, kWave);
-  if constexpr (WAVES > 1) {
-    __syncthreads();  // the sums before are read
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) v += part[w];
+// The threads of a row: LANES of a wave, or (LANES 0) a workgroup.  Sums are the same in all of them, in a fixed order.
+template <int LANES>
+struct RowThreads {
+  int t, count;  // this thread's place, threads a row
+  long long row, step;
+  float (*part)[kNormMaxWaves];
+  int slot = 0;
+  __device__ inline RowThreads(float (*p)[kNormMaxWaves]) : part(p) {
+    if constexpr (LANES > 0) {
+      constexpr int ROWS = kNormLanesThreads / LANES;
+      t = threadIdx.x % LANES, count = LANES;
+      row = (long long)blockIdx.x * ROWS + threadIdx.x / LANES, step = (long long)gridDim.x * ROWS;
+    } else {
+      t = threadIdx.x, count = blockDim.x;
+      row = blockIdx.x, step = gridDim.x;
+    }
   }
-  return v;
+  __device__ inline float sum(float v) {
+    if constexpr (LANES > 0) {
+      return token_sum<LANES>(v);
+    } else {
+      v = token_sum<kWave>(v);
+      if (blockDim.x == kWave) return v;
+      // two places in turn: who writes one again has passed the barrier behind the other's reads
+      float *p = part[slot ^= 1];
+      if ((threadIdx.x & 63) == 0) p[threadIdx.x >> 6] = v;
+      __syncthreads();
+      const int w = threadIdx.x & 15;
+      return token_sum<16>(w < (int)(blockDim.x >> 6) ? p[w] : 0.0f);
+    }
+  }
+};
+
+// Where a step's eight columns begin, and how many of them an earlier thread has already: the last run of a row whose
+// width is no multiple of 8 is moved back to end with the row (a thread without columns has the row's last eight, all
+// of them others').  So every load is whole, and what two threads write is the same.
+struct Run {
+  int at, skip;
+  __device__ inline Run(int t, int count, int i, int W) {
+    const int c = 8 * (t + i * count);
+    at = min(c, W - 8);
+    skip = min(c - at, 8);
+  }
+};
+
+// Sum of f(j) over the columns of a run that are this thread's.
+template <class F>
+__device__ inline float run_sum(const Run &r, F f) {
+  float s = 0.0f;
+  if (r.skip == 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += f(j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += j >= r.skip ? f(j) : 0.0f;
+  }
+  return s;
 }
 
 __device__ inline void load_w(const void *w, bool bf16, long long i, int n, float (&v)[8]) {
@@ -38,23 +86,109 @@ struct NormArgs {
   float *mean, *rstd;
   long long rows;
   int width;
-  bool w_bf16;
+  bool w_bf16, late;  // late: the next row's residual is fetched only when a row is written
   float eps;
   Drop drop;
 };
 
-// WAVES waves a row, CHUNKS steps of 8 values a thread (0: as many as the row has, read again for each sum).
-template <bool BF16, bool RMS, bool DROP, int WAVES, int CHUNKS>
-__global__ __launch_bounds__(WAVES * kWave) void k_norm(NormArgs a) {
-  constexpr int T = WAVES * kWave, KEEP = CHUNKS ? CHUNKS : 1;
-  __shared__ float part[WAVES];
-  const int W = a.width, steps = CHUNKS ? CHUNKS : (W + 8 * T - 1) / (8 * T);
+// Rows of 8 to 8 CHUNKS threads columns.  The next row's loads are under way while a row is summed and written.
+template <bool BF16, bool RMS, bool DROP, int LANES, int CHUNKS>
+__global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k_norm(NormArgs a) {
+  __shared__ float part[2][kNormMaxWaves];
+  RowThreads<LANES> me(part);
+  const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  float w[CHUNKS][8], b[CHUNKS][8];
+  Raw<BF16> x[CHUNKS], r[CHUNKS];
+  auto fetch = [&](Raw<BF16> *to, const void *from, long long row) {
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i)
+      to[i].load(row_at(from, bytes_of<BF16>(row * W)), Run(me.t, me.count, i, W).at);
+  };
+  const bool early = a.residual && !a.late, late = a.residual && a.late;
+  if (me.row < a.rows) {
+    fetch(x, a.x, me.row);
+    if (a.residual) fetch(r, a.residual, me.row);
+  }
+  auto weights = [&](int i) {
+    const Run u(me.t, me.count, i, W);
+    load_w(a.weight, a.w_bf16, u.at, 8, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[i][j] = 0.0f;
+    if (a.bias) load_w(a.bias, a.w_bf16, u.at, 8, b[i]);
+  };
+  constexpr bool KEEP = CHUNKS == 1;
+  if (KEEP) weights(0);
+  const float rw = 1.0f / W;
+  for (long long row = me.row; row < a.rows; row += me.step) {
     const long long base = row * W;
-    float kept[KEEP][8];
-    // h of step i (of which n > 0 columns are in the row)
+    float h[CHUNKS][8], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+      const Run u(me.t, me.count, i, W);
+      x[i].values(h[i]);
+      float v[8] = {};
+      if (a.residual) r[i].values(v);
+      if (DROP) {
+        drop_8(drop_bits((unsigned long long)(base + u.at), key), a.drop, h[i], v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] += v[j];
+      }
+      sum += run_sum(u, [&](int j) { return RMS ? h[i][j] * h[i][j] : h[i][j]; });
+    }
+    const bool more = row + me.step < a.rows;
+    if (more) fetch(x, a.x, row + me.step);
+    if (more && early) fetch(r, a.residual, row + me.step);
+    sum = me.sum(sum) * rw;
+    // from here on every thread has its columns: an output may take their place
+    if (a.total)
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+        const Run u(me.t, me.count, i, W);
+        if (u.skip < 8) Raw<BF16>(h[i]).store(row_at(a.total, bytes_of<BF16>(base)), u.at);
+      }
+    const float mean = RMS ? 0.0f : sum;
+    float var = sum;
+    if (!RMS) {
+      float sq = 0.0f;
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] -= mean;
+        sq += run_sum(Run(me.t, me.count, i, W), [&](int j) { return h[i][j] * h[i][j]; });
+      }
+      var = me.sum(sq) * rw;
+    }
+    const float rstd = __builtin_amdgcn_rsqf(var + a.eps);  // within one step
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+      const Run u(me.t, me.count, i, W);
+      if (u.skip == 8) continue;
+      if (!KEEP) weights(i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = fmaf(h[i][j] * rstd, w[i][j], b[i][j]);
+      Raw<BF16>(h[i]).store(row_at(a.y, bytes_of<BF16>(base)), u.at);
+    }
+    if (more && late) fetch(r, a.residual, row + me.step);
+    if (me.t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+  }
+}
+
+// Rows of any width, read again for each sum.
+template <bool BF16, bool RMS, bool DROP>
+__global__ __launch_bounds__(kNormMaxThreads) void k_norm_any(NormArgs a) {
+  __shared__ float part[2][kNormMaxWaves];
+  RowThreads<0> me(part);
+  const int W = a.width;
+  DropKey key{};
+  if (DROP) key = drop_key(a.drop);
+  for (long long row = me.row; row < a.rows; row += me.step) {
+    const long long base = row * W;
     auto read = [&](int at, int n, float (&v)[8]) {
       load_8<BF16>(a.x, base + at, n, v);
       if (DROP) drop_8(drop_bits((unsigned long long)(base + at), key), a.drop, v);
@@ -65,54 +199,35 @@ __global__ __launch_bounds__(WAVES * kWave) void k_norm(NormArgs a) {
         for (int j = 0; j < 8; ++j) v[j] += r[j];
       }
     };
-    auto h = [&](int i, int at, int n, float (&v)[8]) {
-      if constexpr (CHUNKS > 0) {
+    float mean = 0.0f, sum = 0.0f, sq = 0.0f;
+    if (!RMS) {
+      for (int at = 8 * me.t; at < W; at += 8 * me.count) {
+        float v[8];
+        read(at, W - at, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = kept[i][j];
-      } else {
-        read(at, n, v);
+        for (int j = 0; j < 8; ++j) sum += at + j < W ? v[j] : 0.0f;
       }
-    };
-    float sum = 0.0f;
-#pragma unroll KEEP
-    for (int i = 0; i < steps; ++i) {
-      const int at = 8 * (threadIdx.x + i * T), n = W - at;
-      float v[8] = {};
-      if (n > 0) read(at, n, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j < n) sum += v[j];
-        if (CHUNKS > 0) kept[i][j] = v[j];
-      }
+      mean = me.sum(sum) / W;
     }
-    float mean = 0.0f;
-    if (!RMS) mean = row_sum<WAVES>(sum, part) / W;
-    float sq = 0.0f;
-#pragma unroll KEEP
-    for (int i = 0; i < steps; ++i) {
-      const int at = 8 * (threadIdx.x + i * T), n = W - at;
-      if (n <= 0) continue;
+    for (int at = 8 * me.t; at < W; at += 8 * me.count) {
       float v[8];
-      h(i, at, n, v);
+      read(at, W - at, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) sq += (v[j] - mean) * (v[j] - mean);
+      for (int j = 0; j < 8; ++j) sq += at + j < W ? (v[j] - mean) * (v[j] - mean) : 0.0f;
     }
-    const float rstd = 1.0f / sqrtf(row_sum<WAVES>(sq, part) / W + a.eps);
-#pragma unroll KEEP
-    for (int i = 0; i < steps; ++i) {
-      const int at = 8 * (threadIdx.x + i * T), n = W - at;
-      if (n <= 0) continue;
+    const float rstd = 1.0f / sqrtf(me.sum(sq) / W + a.eps);
+    for (int at = 8 * me.t; at < W; at += 8 * me.count) {
+      const int n = W - at;
       float v[8], w[8], b[8] = {};
-      h(i, at, n, v);
+      read(at, n, v);
       load_w(a.weight, a.w_bf16, at, n, w);
       if (a.bias) load_w(a.bias, a.w_bf16, at, n, b);
       if (a.total) store_8<BF16>(a.total, base + at, n, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (v[j] - mean) * rstd * w[j] + b[j];
+      for (int j = 0; j < 8; ++j) v[j] = fmaf((v[j] - mean) * rstd, w[j], b[j]);
       store_8<BF16>(a.y, base + at, n, v);
     }
-    if (threadIdx.x == 0) {
+    if (me.t == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
@@ -130,80 +245,173 @@ struct NormBwdArgs {
   Drop drop;
 };
 
-template <bool BF16, bool RMS, bool DROP, int WAVES, int CHUNKS>
-__global__ __launch_bounds__(WAVES * kWave) void k_norm_bwd(NormBwdArgs a) {
-  constexpr int T = WAVES * kWave, KEEP = CHUNKS ? CHUNKS : 1;
-  __shared__ float part[WAVES];
-  const int W = a.width, steps = CHUNKS ? CHUNKS : (W + 8 * T - 1) / (8 * T);
+template <bool BF16, bool RMS, bool DROP, int LANES, int CHUNKS>
+__global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k_norm_bwd(NormBwdArgs a) {
+  __shared__ float part[2][kNormMaxWaves];
+  RowThreads<LANES> me(part);
+  const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
-  float dw[KEEP][8] = {}, db[KEEP][8] = {};
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const long long base = row * W;
-    const float mean = RMS ? 0.0f : a.mean[row], rstd = a.rstd[row];
-    float kept_h[KEEP][8], kept_g[KEEP][8];
-    // xh and g of a step
-    auto read = [&](int at, int n, float (&xh)[8], float (&g)[8], float (&d)[8]) {
-      float w[8];
-      load_8<BF16>(a.total, base + at, n, xh);
-      load_8<BF16>(a.dy, base + at, n, d);
-      load_w(a.weight, a.w_bf16, at, n, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) xh[j] = (xh[j] - mean) * rstd, g[j] = d[j] * w[j];
-    };
-    float sg = 0.0f, sgx = 0.0f;
-#pragma unroll KEEP
-    for (int i = 0; i < steps; ++i) {
-      const int at = 8 * (threadIdx.x + i * T), n = W - at;
-      float xh[8] = {}, g[8] = {}, d[8] = {};
-      if (n > 0) read(at, n, xh, g, d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j < n) {
-          sg += g[j];
-          sgx += g[j] * xh[j];
-        }
-        if (CHUNKS > 0) {
-          kept_h[i][j] = xh[j], kept_g[i][j] = g[j];
-          if (j < n) dw[i][j] += d[j] * xh[j], db[i][j] += d[j];
-        }
-      }
-    }
-    if (!RMS) sg = row_sum<WAVES>(sg, part) / W;
-    sgx = row_sum<WAVES>(sgx, part) / W;
-#pragma unroll KEEP
-    for (int i = 0; i < steps; ++i) {
-      const int at = 8 * (threadIdx.x + i * T), n = W - at;
-      if (n <= 0) continue;
-      float xh[8], g[8], d[8];
-      if constexpr (CHUNKS > 0) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) xh[j] = kept_h[i][j], g[j] = kept_g[i][j];
-      } else {
-        read(at, n, xh, g, d);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = rstd * (g[j] - (RMS ? 0.0f : sg) - xh[j] * sgx);
-      if (a.dtotal) {
-        float t[8];
-        load_8<BF16>(a.dtotal, base + at, n, t);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] += t[j];
-      }
-      if (a.dresidual) store_8<BF16>(a.dresidual, base + at, n, d);
-      if (DROP) drop_8(drop_bits((unsigned long long)(base + at), key), a.drop, d);
-      store_8<BF16>(a.dx, base + at, n, d);
-    }
-  }
-  if constexpr (CHUNKS > 0) {
-    if (!a.parts) return;
-    float *p = a.parts + (long long)blockIdx.x * 2 * W;
+  // Sums of the columns: with two runs a thread in LDS (each thread its own), since the registers of 1024 threads do
+  // not hold them (spilled, 4096 x 16384 bf16 took 212 us).
+  constexpr bool LDS = CHUNKS > 1;
+  __shared__ f32x4 held[LDS ? CHUNKS * 4 : 1][LDS ? kNormMaxThreads : 1];
+  float w[CHUNKS][8], dw[LDS ? 1 : CHUNKS][8], db[LDS ? 1 : CHUNKS][8];
+  Raw<BF16> t[CHUNKS], d[CHUNKS], q[CHUNKS];
+  float mean = 0.0f, rstd = 0.0f;
+  auto fetch = [&](long long row) {
+    const long long bytes = bytes_of<BF16>(row * W);
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int at = 8 * (threadIdx.x + i * T), n = W - at;
-      if (n <= 0) continue;
-      store_8<false>(p, at, n, dw[i]);
-      store_8<false>(p + W, at, n, db[i]);
+      const Run u(me.t, me.count, i, W);
+      t[i].load(row_at(a.total, bytes), u.at);
+      d[i].load(row_at(a.dy, bytes), u.at);
+      if (a.dtotal) q[i].load(row_at(a.dtotal, bytes), u.at);
+    }
+    if (!RMS) mean = a.mean[row];
+    rstd = a.rstd[row];
+  };
+  if (me.row < a.rows) fetch(me.row);
+#pragma unroll
+  for (int i = 0; i < CHUNKS; ++i) {
+    load_w(a.weight, a.w_bf16, Run(me.t, me.count, i, W).at, 8, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[LDS ? 0 : i][j] = db[LDS ? 0 : i][j] = 0.0f;
+    if (LDS)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) held[4 * i + k][threadIdx.x] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const float rw = 1.0f / W;
+  for (long long row = me.row; row < a.rows; row += me.step) {
+    const long long base = row * W;
+    const float rs = rstd;
+    float xh[CHUNKS][8], g[CHUNKS][8], sg = 0.0f, sgx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+      const Run u(me.t, me.count, i, W);
+      float v[8];
+      t[i].values(xh[i]);
+      d[i].values(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        xh[i][j] = (xh[i][j] - mean) * rs;
+        g[i][j] = v[j] * w[i][j];
+        if (!LDS) dw[i][j] = fmaf(v[j], xh[i][j], dw[i][j]), db[i][j] += v[j];
+      }
+      if (LDS)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f32x4 s = held[4 * i + k][threadIdx.x];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * (k & 1) + j;
+            s[j] = k < 2 ? fmaf(v[e], xh[i][e], s[j]) : s[j] + v[e];
+          }
+          held[4 * i + k][threadIdx.x] = s;
+        }
+      if (!RMS) sg += run_sum(u, [&](int j) { return g[i][j]; });
+      sgx += run_sum(u, [&](int j) { return g[i][j] * xh[i][j]; });
+      if (a.dtotal) q[i].values(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[i][j] = fmaf(rs, g[i][j], a.dtotal ? v[j] : 0.0f);
+    }
+    if (row + me.step < a.rows) fetch(row + me.step);
+    if (!RMS) sg = me.sum(sg) * rw * rs;
+    sgx = me.sum(sgx) * rw * rs;
+    // from here on every thread has its columns: an output may take their place
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+      const Run u(me.t, me.count, i, W);
+      if (u.skip == 8) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[i][j] = fmaf(-xh[i][j], sgx, g[i][j]);
+        if (!RMS) g[i][j] -= sg;
+      }
+      if (a.dresidual) Raw<BF16>(g[i]).store(row_at(a.dresidual, bytes_of<BF16>(base)), u.at);
+      if (DROP) drop_8(drop_bits((unsigned long long)(base + u.at), key), a.drop, g[i]);
+      Raw<BF16>(g[i]).store(row_at(a.dx, bytes_of<BF16>(base)), u.at);
+    }
+  }
+  if (!a.parts) return;
+  float *p = a.parts + (long long)blockIdx.x * 2 * W;
+  auto keep = [&](const Run &u, const float (&v)[8], const float (&s)[8]) {
+    if (u.skip == 0) {
+      store_8<false>(p, u.at, 8, v);
+      store_8<false>(p + W, u.at, 8, s);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= u.skip) p[u.at + j] = v[j], p[W + u.at + j] = s[j];
+    }
+  };
+  if constexpr (LANES == 0) {
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+      if (LDS)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dw[0][j] = held[4 * i + (j >> 2)][threadIdx.x][j & 3];
+          db[0][j] = held[4 * i + 2 + (j >> 2)][threadIdx.x][j & 3];
+        }
+      keep(Run(me.t, me.count, i, W), dw[LDS ? 0 : i], db[LDS ? 0 : i]);
+    }
+  } else {
+    static_assert(CHUNKS == 1, "a lane's one run");
+    __shared__ float sums[kNormLanesThreads][16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[threadIdx.x][j] = dw[0][j], sums[threadIdx.x][8 + j] = db[0][j];
+    __syncthreads();
+    if ((int)threadIdx.x >= LANES) return;
+    for (int k = 1; k < kNormLanesThreads / LANES; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[0][j] += sums[k * LANES + threadIdx.x][j];
+        db[0][j] += sums[k * LANES + threadIdx.x][8 + j];
+      }
+    keep(Run(me.t, me.count, 0, W), dw[0], db[0]);
+  }
+}
+
+// dx and dresidual of rows of any width, read again for the result.
+template <bool BF16, bool RMS, bool DROP>
+__global__ __launch_bounds__(kNormMaxThreads) void k_norm_bwd_any(NormBwdArgs a) {
+  __shared__ float part[2][kNormMaxWaves];
+  RowThreads<0> me(part);
+  const int W = a.width;
+  DropKey key{};
+  if (DROP) key = drop_key(a.drop);
+  for (long long row = me.row; row < a.rows; row += me.step) {
+    const long long base = row * W;
+    const float mean = RMS ? 0.0f : a.mean[row], rstd = a.rstd[row];
+    auto read = [&](int at, int n, float (&xh)[8], float (&g)[8]) {
+      float w[8];
+      load_8<BF16>(a.total, base + at, n, xh);
+      load_8<BF16>(a.dy, base + at, n, g);
+      load_w(a.weight, a.w_bf16, at, n, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) xh[j] = (xh[j] - mean) * rstd, g[j] *= w[j];  // g is 0 behind the row
+    };
+    float sg = 0.0f, sgx = 0.0f;
+    for (int at = 8 * me.t; at < W; at += 8 * me.count) {
+      float xh[8], g[8];
+      read(at, W - at, xh, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at + j < W) sg += g[j], sgx = fmaf(g[j], xh[j], sgx);
+    }
+    if (!RMS) sg = me.sum(sg) / W;
+    sgx = me.sum(sgx) / W;
+    for (int at = 8 * me.t; at < W; at += 8 * me.count) {
+      const int n = W - at;
+      float xh[8], g[8], q[8] = {};
+      read(at, n, xh, g);
+      if (a.dtotal) load_8<BF16>(a.dtotal, base + at, n, q);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = fmaf(rstd, g[j] - (RMS ? 0.0f : sg) - xh[j] * sgx, q[j]);
+      if (a.dresidual) store_8<BF16>(a.dresidual, base + at, n, g);
+      if (DROP) drop_8(drop_bits((unsigned long long)(base + at), key), a.drop, g);
+      store_8<BF16>(a.dx, base + at, n, g);
     }
   }
 }
@@ -243,8 +451,21 @@ __global__ __launch_bounds__(kPartsThreads) void k_norm_parts(const float *__res
   if (!out) return;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = blockIdx.x * kWave + lane;
   float v = 0.0f;
-  if (c < W)
-    for (int i = w; i < n; i += WAVES) v += parts[((long long)i * 2 + blockIdx.y) * W + c];
+  if (c < W) {
+    // all loads of a lane under way together: the parts come from other caches
+    const float *p = parts + (long long)blockIdx.y * W + c;
+    constexpr int FLIGHT = 32;
+    for (int i0 = w; i0 < n; i0 += WAVES * FLIGHT) {
+      float t[FLIGHT];
+#pragma unroll
+      for (int k = 0; k < FLIGHT; ++k) {
+        const int i = i0 + WAVES * k;
+        t[k] = i < n ? p[(long long)i * 2 * W] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < FLIGHT; ++k) v += t[k];
+    }
+  }
   s[w][lane] = v;
   __syncthreads();
   if (w || c >= W) return;
@@ -254,31 +475,48 @@ __global__ __launch_bounds__(kPartsThreads) void k_norm_parts(const float *__res
   out[c] = accumulate ? out[c] + v : v;
 }
 
-// Calls f with the waves a row and the steps a thread for a width.
+// Widths that a row's threads keep in registers; others go through the kernels that read a row again.
+constexpr int kNormNarrowest = 8;
+constexpr int kNormWidest = 16 * kNormMaxThreads;
+constexpr int kNormMaxWidth = 1 << 22;
+
+static bool row_kept(int64_t width) { return width >= kNormNarrowest && width <= kNormWidest; }
+
+// Calls f with the lanes of a row (0: a workgroup), the steps of a thread, the workgroup's threads and its rows.
 template <class F>
 static void with_row(int W, F f) {
-  auto of = [&](auto w, auto c) { return f(w, c); };
   using std::integral_constant;
-#define MOE_ROW(w, c) of(integral_constant<int, w>{}, integral_constant<int, c>{})
-  if (W <= 512) MOE_ROW(1, 1);
-  else if (W <= 1024) MOE_ROW(1, 2);
-  else if (W <= 2048) MOE_ROW(2, 2);
-  else if (W <= 4096) MOE_ROW(4, 2);
-  else if (W <= 8192) MOE_ROW(8, 2);
-  else if (W <= 16384) MOE_ROW(16, 2);
-  else MOE_ROW(16, 0);
+#define MOE_ROW(l, c, threads, rows) f(integral_constant<int, l>{}, integral_constant<int, c>{}, threads, rows)
+  auto waves = [&](int chunks) { return ceil_div(W, 8 * chunks * kWave) * kWave; };
+  if (W <= 128) MOE_ROW(16, 1, kNormLanesThreads, 16);
+  else if (W <= 256) MOE_ROW(32, 1, kNormLanesThreads, 8);
+  else if (W <= 512) MOE_ROW(64, 1, kNormLanesThreads, 4);
+  else if (W <= 8 * kNormMaxThreads) MOE_ROW(0, 1, waves(1), 1);
+  else MOE_ROW(0, 2, waves(2), 1);
 #undef MOE_ROW
 }
 
-constexpr int kNormWidest = 16384;       // kept in registers
-constexpr int kNormMaxWidth = 1 << 22;
-constexpr int kNormParts = 512;          // sums of columns that a backward call makes, then adds up
-constexpr int kColParts = 64;            // the same for wider rows
-
-static int norm_parts(int64_t rows, int64_t width) {
-  const int most = width > kNormWidest ? kColParts : kNormParts;
-  return (int)(rows < most ? rows : most);
+// Workgroups per CU that walk the rows, from the bytes each has under way (the next row's loads): enough for the
+// memory's latency and no more, since what is under way beyond that only spreads the accesses (see k_norm).
+static int per_cu(int64_t under_way, int64_t wanted) {
+  const int64_t n = (wanted + under_way / 2) / under_way;
+  return (int)(n < 1 ? 1 : n > 8 ? 8 : n);
 }
+constexpr int64_t kNormUnderWay = 16 << 10, kNormBwdUnderWay = 24 << 10;
+
+static int norm_parts(int64_t rows, int64_t width, int64_t bytes) {
+  int64_t groups = rows, most = kColParts;
+  if (row_kept(width))
+    with_row((int)width, [&](auto, auto, int threads, int per) {
+      groups = (rows + per - 1) / per;
+      most = (int64_t)device_cu_count() * per_cu(bytes * per * width, kNormBwdUnderWay);
+    });
+  if (most > kNormParts) most = kNormParts;
+  return (int)(groups < most ? groups : most);
+}
+
+// Threads of the kernels that read a row again.
+static int any_threads(int64_t width) { return width >= 8 * kNormMaxThreads ? kNormMaxThreads : ceil_div(width, 8 * kWave) * kWave; }
 
 static bool norm_args_ok(moe_dtype dtype, moe_norm_kind kind, moe_dtype w_dtype, int64_t rows, int64_t width) {
   if ((dtype != MOE_BF16 && dtype != MOE_F32) || (w_dtype != MOE_BF16 && w_dtype != MOE_F32)) return false;
@@ -304,17 +542,25 @@ extern "C" moe_status_t moe_layer_norm(moe_dtype dtype, moe_norm_kind kind, moe_
       ((uintptr_t)weight | (uintptr_t)bias) % w_size || ((uintptr_t)mean | (uintptr_t)rstd) % 4)
     return MOE_EINVAL;
   const size_t bytes = (size_t)rows * width * size, w_bytes = width * w_size, s_bytes = rows * 4;
-  const Range in[] = {{x, bytes, true}, {residual, bytes, true}, {weight, w_bytes, false}, {bias, w_bytes, false},
-                      {rng, 16, false}, {total, bytes, false}, {mean, s_bytes, false}, {rstd, s_bytes, false}};
-  if (!stands_alone(y, bytes, in, 8) || !stands_alone(total, bytes, in, 5) || !stands_alone(mean, s_bytes, in, 6) ||
+  const Range in[] = {{x, bytes, true}, {residual, bytes, true}, {weight, w_bytes}, {bias, w_bytes},
+                      {rng, 16}, {total, bytes}, {mean, s_bytes}, {rstd, s_bytes}};
+  if (!stands_alone(y, bytes, in, 8, true) || !stands_alone(total, bytes, in, 5, true) || !stands_alone(mean, s_bytes, in, 6) ||
       !stands_alone(rstd, s_bytes, in, 7))
     return MOE_EINVAL;
-  NormArgs a{x, residual, weight, bias, total, y, mean, rstd, rows, (int)width, w_dtype == MOE_BF16, (float)eps,
+  NormArgs a{x, residual, weight, bias, total, y, mean, rstd, rows, (int)width, w_dtype == MOE_BF16, false, (float)eps,
              make_drop(p, rng, offset)};
   auto go = [&](auto bf16, auto rms, auto drop) {
-    with_row((int)width, [&](auto w, auto c) {
-      hipLaunchKernelGGL((k_norm<bf16.value, rms.value, drop.value, w.value, c.value>),
-                         dim3((unsigned)(rows < (1 << 22) ? rows : 1 << 22)), dim3(w.value * kWave), 0, stream, a);
+    if (!row_kept(width)) {
+      hipLaunchKernelGGL((k_norm_any<bf16.value, rms.value, drop.value>), dim3((unsigned)(rows < (1 << 22) ? rows : 1 << 22)),
+                         dim3(any_threads(width)), 0, stream, a);
+      return;
+    }
+    with_row((int)width, [&](auto l, auto c, int threads, int per) {
+      const int64_t groups = (rows + per - 1) / per, one = (int64_t)size * per * width;
+      a.late = 2 * one > kNormUnderWay + kNormUnderWay / 4;
+      const int64_t most = (int64_t)device_cu_count() * per_cu(residual && !a.late ? 2 * one : one, kNormUnderWay);
+      hipLaunchKernelGGL((k_norm<bf16.value, rms.value, drop.value, l.value, c.value>),
+                         dim3((unsigned)(groups < most ? groups : most)), dim3(threads), 0, stream, a);
     });
   };
   auto pick = [&](auto bf16, auto rms) { a.drop.below ? go(bf16, rms, std::true_type{}) : go(bf16, rms, std::false_type{}); };
@@ -325,7 +571,7 @@ extern "C" moe_status_t moe_layer_norm(moe_dtype dtype, moe_norm_kind kind, moe_
 
 extern "C" size_t moe_layer_norm_backward_workspace_bytes(int64_t rows, int64_t width) {
   if (rows < 0 || rows >= (1LL << 31) || width < 1 || width > kNormMaxWidth) return 0;
-  return (size_t)norm_parts(rows, width) * 2 * width * sizeof(float);
+  return (size_t)norm_parts(rows, width, 4) * 2 * width * sizeof(float);  // of two bf16 tensors: most parts
 }
 
 extern "C" moe_status_t moe_layer_norm_backward(moe_dtype dtype, moe_norm_kind kind, moe_dtype w_dtype,
@@ -351,24 +597,28 @@ extern "C" moe_status_t moe_layer_norm_backward(moe_dtype dtype, moe_norm_kind k
     if (ws_bytes < need) return MOE_ENOSPACE;
   }
   const size_t bytes = (size_t)rows * width * size, w_bytes = width * w_size, s_bytes = rows * 4, d_bytes = width * 4;
-  const Range in[] = {{dy, bytes, true},        {dtotal, bytes, true},       {total, bytes, false},   {weight, w_bytes, false},
-                      {mean, s_bytes, false},   {rstd, s_bytes, false},      {rng, 16, false},        {ws, sums ? need : 0, false},
-                      {dweight, d_bytes, false}, {dbias, d_bytes, false},    {dresidual, bytes, false}};
-  if (!stands_alone(dx, bytes, in, 11) || !stands_alone(dresidual, bytes, in, 10)) return MOE_EINVAL;
+  const Range in[] = {{dy, bytes, true},        {dtotal, bytes, true},       {total, bytes},   {weight, w_bytes},
+                      {mean, s_bytes},   {rstd, s_bytes},      {rng, 16},        {ws, sums ? need : 0},
+                      {dweight, d_bytes}, {dbias, d_bytes},    {dresidual, bytes}};
+  if (!stands_alone(dx, bytes, in, 11, true) || !stands_alone(dresidual, bytes, in, 10, true)) return MOE_EINVAL;
   if (sums && (!stands_alone(dweight, d_bytes, in, 8) || !stands_alone(dbias, d_bytes, in, 9) ||
                !stands_alone(ws, need, in, 7)))
     return MOE_EINVAL;
   NormBwdArgs a{total, weight, dy, dtotal, mean, rstd, dx, dresidual, sums ? (float *)ws : nullptr, rows, (int)width,
                 w_dtype == MOE_BF16, make_drop(p, rng, offset)};
-  const int parts = norm_parts(rows, width);
+  const int parts = norm_parts(rows, width, (int64_t)size * (dtotal ? 3 : 2));
   auto go = [&](auto bf16, auto rms, auto drop) {
-    if (sums && width > kNormWidest)  // before dx, which may take dy's place
-      hipLaunchKernelGGL((k_norm_cols<bf16.value, rms.value>), dim3(ceil_div(width, kColThreads), parts),
-                         dim3(kColThreads), 0, stream, a);
-    with_row((int)width, [&](auto w, auto c) {
-      const int64_t most = c.value ? kNormParts : 1 << 22;
-      hipLaunchKernelGGL((k_norm_bwd<bf16.value, rms.value, drop.value, w.value, c.value>),
-                         dim3((unsigned)(rows < most ? rows : most)), dim3(w.value * kWave), 0, stream, a);
+    if (!row_kept(width)) {
+      if (sums)  // before dx, which may take dy's place
+        hipLaunchKernelGGL((k_norm_cols<bf16.value, rms.value>), dim3(ceil_div(width, kColThreads), parts),
+                           dim3(kColThreads), 0, stream, a);
+      hipLaunchKernelGGL((k_norm_bwd_any<bf16.value, rms.value, drop.value>), dim3((unsigned)(rows < (1 << 22) ? rows : 1 << 22)),
+                         dim3(any_threads(width)), 0, stream, a);
+      return;
+    }
+    with_row((int)width, [&](auto l, auto c, int threads, int) {
+      hipLaunchKernelGGL((k_norm_bwd<bf16.value, rms.value, drop.value, l.value, c.value>), dim3(parts), dim3(threads), 0,
+                         stream, a);
     });
   };
   auto pick = [&](auto bf16, auto rms) { a.drop.below ? go(bf16, rms, std::true_type{}) : go(bf16, rms, std::false_type{}); };

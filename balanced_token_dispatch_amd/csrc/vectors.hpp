@@ -62,6 +62,51 @@ __device__ inline void store_8(void *p, long long i, int n, const float (&v)[8])
   }
 }
 
+// Bytes of i values.  A row's place as a pointer that is the same in all lanes and 32 bits of offset in it spares the
+// lanes 64-bit sums.
+template <bool BF16>
+__device__ inline long long bytes_of(long long i) { return i * (BF16 ? 2 : 4); }
+
+// Eight values as they lie in memory, at any alignment of the element: the values from `at` on of a row.
+template <bool BF16>
+struct Raw;
+
+template <>
+struct Raw<true> {
+  u32x4 t;
+  __device__ inline void load(const void *row, uint32_t at) { __builtin_memcpy(&t, (const char *)row + 2 * at, 16); }
+  __device__ inline void store(void *row, uint32_t at) const { __builtin_memcpy((char *)row + 2 * at, &t, 16); }
+  __device__ inline Raw() {}
+  __device__ inline Raw(const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  }
+  __device__ inline void values(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[2 * j] = bf16_lo(t[j]), v[2 * j + 1] = bf16_hi(t[j]);
+  }
+};
+
+template <>
+struct Raw<false> {
+  f32x4 t[2];
+  __device__ inline void load(const void *row, uint32_t at) { __builtin_memcpy(t, (const char *)row + 4 * at, 32); }
+  __device__ inline void store(void *row, uint32_t at) const { __builtin_memcpy((char *)row + 4 * at, t, 32); }
+  __device__ inline Raw() {}
+  __device__ inline Raw(const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j >> 2][j & 3] = v[j];
+  }
+  __device__ inline void values(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = t[j >> 2][j & 3];
+  }
+};
+
+// The row of a tensor that begins `bytes` into it.
+__device__ inline const char *row_at(const void *p, long long bytes) { return (const char *)p + bytes; }
+__device__ inline char *row_at(void *p, long long bytes) { return (char *)p + bytes; }
+
 // Whether two ranges share memory.  Ranges that are the same one are told apart by `same`.
 inline bool shares(const void *a, size_t an, const void *b, size_t bn, bool same) {
   if (!a || !b || !an || !bn) return false;
@@ -70,15 +115,16 @@ inline bool shares(const void *a, size_t an, const void *b, size_t bn, bool same
   return x < y + bn && y < x + an;
 }
 
-// Whether output o (bytes long) shares memory with no input but, whole, one of `same`, and no other range.
+// Whether output o (bytes long) shares memory with none of n ranges but, where it may take a place, with all of one that
+// may be taken.
 struct Range {
   const void *p;
   size_t bytes;
-  bool may_be;  // the output may be this very range
+  bool place = false;  // an output may take its place
 };
-inline bool stands_alone(const void *o, size_t bytes, const Range *r, int n) {
+inline bool stands_alone(const void *o, size_t bytes, const Range *r, int n, bool takes_place = false) {
   for (int i = 0; i < n; ++i)
-    if (shares(o, bytes, r[i].p, r[i].bytes, r[i].may_be && r[i].bytes == bytes)) return false;
+    if (shares(o, bytes, r[i].p, r[i].bytes, takes_place && r[i].place)) return false;
   return true;
 }
 

@@ -134,7 +134,7 @@ def test_norm_refusals(m):
                {13: None}, {9: -1e-5}, {9: float("nan")}, {9: float("inf")}, {10: 1.1}, {11: None}, {5: odd}, {7: V((3 << 24) + 2)},
                {16: V((9 << 24) + 2)}, {1: 1},                       # a mean without one
                {14: at(5)}, {13: V((1 << 24) + 256)}, {14: V((2 << 24) + 2)}, {14: at(2)}, {13: at(4)}, {15: at(8)},
-               {16: at(6)}, {15: at(0)}):
+               {16: at(6)}, {15: at(0)}, {3: 2, 4: 2, 0: 1, 15: at(0)}):
         assert call(lib.moe_layer_norm, fwd, kw) == m.MOE_EINVAL, kw
     assert call(lib.moe_layer_norm, fwd, {3: 0, 5: None}) == m.MOE_OK
     for kw in ({0: 2}, {1: 2}, {2: 5}, {3: -1}, {4: 0}, {5: None}, {6: None}, {7: None}, {8: None}, {9: None}, {14: None},
