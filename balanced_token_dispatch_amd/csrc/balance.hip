@@ -14,21 +14,59 @@ namespace moe {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalMaxE = 1024;
-constexpr int kTokens = 16;          // tokens per chunk
-constexpr int kCountTokens = 2048;   // tokens per workgroup of the counts
+constexpr int kTokens = 16;  // tokens per chunk
 
 struct Sequences {
   const int32_t *cu;  // NULL: one of all T tokens
   int n, T;
 };
 
-// The sequence of token t: -1 before the first one, n behind the last.  Whatever cu holds, a sequence b in
-// [0, n) has cu[b] <= t < cu[b + 1].
-__device__ inline int sequence_of(const Sequences &s, int t) {
-  if (!s.cu) return 0;
-  if (t < s.cu[0]) return -1;
-  if (t >= s.cu[s.n]) return s.n;
-  int lo = 0, hi = s.n;
+// The sequences that hold tokens first and last, by one wave: -1 before the first one, n behind the last.  Whatever cu
+// holds, a sequence b in [0, n) that comes out has cu[b] <= t < cu[b + 1].  Each step looks at 64 bounds.
+__device__ inline int2 sequences_of(const Sequences &s, int first, int last) {
+  if (!s.cu) return {0, 0};
+  const int lane = threadIdx.x & 63;
+  int lo[2] = {0, 0}, hi[2] = {s.n, s.n}, t[2] = {first, last};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    // cu[lo] <= t < cu[hi] from the first step on
+    bool open = true;
+    int step = (s.n + kWave - 1) / kWave;
+    while (open) {
+      const int i = min(lo[k] + lane * step, hi[k]);
+      const unsigned long long at = __ballot(s.cu[i] <= t[k]);
+      if (at == 0) {
+        lo[k] = -1;
+        break;
+      }
+      const int l = 63 - __clzll(at), from = __shfl(i, l, kWave);
+      if (from == s.n || (hi[k] == s.n && s.cu[s.n] <= t[k])) {
+        lo[k] = s.n;
+        break;
+      }
+      hi[k] = min(from + step, hi[k]);
+      lo[k] = from;
+      open = step > 1;
+      step = (hi[k] - lo[k] + kWave - 1) / kWave;
+    }
+    if (k == 0 && first == last) return {lo[0], lo[0]};
+  }
+  return {lo[0], lo[1]};
+}
+
+// The sequence of token t, which lies between two tokens of sequences lo and hi (as sequences_of gives them).
+__device__ inline int sequence_between(const Sequences &s, int t, int2 at) {
+  int lo = at.x, hi = at.y;
+  if (lo == hi) return lo;
+  if (lo < 0) {
+    if (t < s.cu[0]) return -1;
+    lo = 0;
+  }
+  if (hi >= s.n) {
+    if (t >= s.cu[s.n]) return s.n;
+    hi = s.n - 1;
+  }
+  ++hi;  // cu[lo] <= t < cu[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (s.cu[mid] <= t) lo = mid; else hi = mid;
@@ -42,32 +80,77 @@ __device__ inline int last_token(const Sequences &s, int b) { return s.cu ? min(
 
 // ---- counts ------------------------------------------------------------------------------------
 
-__global__ __launch_bounds__(kBalThreads) void k_count_zero(int32_t *__restrict__ counts, long long n) {
-  for (long long i = (long long)blockIdx.x * kBalThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kBalThreads)
+constexpr int kCountThreads = 1024;
+constexpr int kCountCopies = 4;      // of the bins, lanes taking turns: a popular expert's ids meet in one place less often
+constexpr int kCountIds = 8192;      // about as many ids a workgroup
+constexpr int kCountAlone = 16384;   // ids of a sequence that one workgroup counts by itself
+constexpr int kCountAlonePeak = 65536;
+
+struct Bins {
+  int32_t n[kCountCopies][kBalMaxE + 8];
+  __device__ inline void clear(int E) {
+    for (int e = threadIdx.x; e < E; e += kCountThreads)
+#pragma unroll
+      for (int c = 0; c < kCountCopies; ++c) n[c][e] = 0;
+  }
+  // ids [from, to) of idx
+  __device__ inline void add(const int32_t *__restrict__ idx, int from, int to, int E) {
+    int32_t *mine = n[threadIdx.x % kCountCopies];
+    for (unsigned i = from + 4 * threadIdx.x; i < (unsigned)to; i += 4 * kCountThreads) {
+      int id[4];
+      if (to - i >= 4)
+        __builtin_memcpy(id, idx + i, 16);
+      else
+        for (int j = 0; j < 4; ++j) id[j] = i + j < (unsigned)to ? idx[i + j] : -1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((unsigned)id[j] < (unsigned)E) atomicAdd(&mine[id[j]], 1);
+    }
+  }
+  __device__ inline int32_t of(int e) const {
+    int32_t v = 0;
+#pragma unroll
+    for (int c = 0; c < kCountCopies; ++c) v += n[c][e];
+    return v;
+  }
+};
+
+// A workgroup per sequence.
+__global__ __launch_bounds__(kCountThreads) void k_count_sequences(const int32_t *__restrict__ idx, Sequences s, int E,
+                                                                  int K, int32_t *__restrict__ counts) {
+  __shared__ Bins bins;
+  const int b = blockIdx.x, lo = first_token(s, b), hi = max(last_token(s, b), lo);
+  bins.clear(E);
+  __syncthreads();
+  bins.add(idx, lo * K, hi * K, E);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kCountThreads) counts[(long long)b * E + e] = bins.of(e);
+}
+
+__global__ __launch_bounds__(kCountThreads) void k_count_zero(int32_t *__restrict__ counts, long long n) {
+  for (long long i = (long long)blockIdx.x * kCountThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kCountThreads)
     counts[i] = 0;
 }
 
-// Adds the ids of kCountTokens tokens, sequence by sequence, in LDS and then to counts (whole numbers: their
-// order changes nothing).
-__global__ __launch_bounds__(kBalThreads) void k_expert_counts(const int32_t *__restrict__ idx, Sequences s, int E,
-                                                              int K, int32_t *__restrict__ counts) {
-  __shared__ int32_t bins[kBalMaxE];
-  int t = (int)min((long long)blockIdx.x * kCountTokens, (long long)s.T);
-  const int end = (int)min((long long)t + kCountTokens, (long long)s.T);
+// Adds the ids of `tokens` tokens, sequence by sequence (whole numbers: the order of the additions changes nothing).
+__global__ __launch_bounds__(kCountThreads) void k_count_chunks(const int32_t *__restrict__ idx, Sequences s, int E, int K,
+                                                               int tokens, int32_t *__restrict__ counts) {
+  __shared__ Bins bins;
+  int t = (int)min((long long)blockIdx.x * tokens, (long long)s.T);
+  const int end = (int)min((long long)t + tokens, (long long)s.T);
   while (t < end) {
-    const int b = sequence_of(s, t);
+    const int b = sequences_of(s, t, t).x;
     if (b >= s.n) break;
     const int stop = !s.cu ? end : min(end, b < 0 ? s.cu[0] : s.cu[b + 1]);  // above t
     if (b >= 0) {
-      for (int e = threadIdx.x; e < E; e += kBalThreads) bins[e] = 0;
+      bins.clear(E);
       __syncthreads();
-      for (long long i = (long long)t * K + threadIdx.x; i < (long long)stop * K; i += kBalThreads) {
-        const int e = idx[i];
-        if ((unsigned)e < (unsigned)E) atomicAdd(&bins[e], 1);
+      bins.add(idx, t * K, stop * K, E);
+      __syncthreads();
+      for (int e = threadIdx.x; e < E; e += kCountThreads) {
+        const int32_t v = bins.of(e);
+        if (v) atomicAdd(&counts[(long long)b * E + e], v);
       }
-      __syncthreads();
-      for (int e = threadIdx.x; e < E; e += kBalThreads)
-        if (bins[e]) atomicAdd(&counts[(long long)b * E + e], bins[e]);
       __syncthreads();
     }
     t = stop;
@@ -75,6 +158,11 @@ __global__ __launch_bounds__(kBalThreads) void k_expert_counts(const int32_t *__
 }
 
 // ---- rows of logits ----------------------------------------------------------------------------
+
+constexpr float kLog2e = 1.44269504f;
+
+// exp(d): the argument is rounded in the product with log2(e), below 2^-126 the result is 0.
+__device__ inline float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
 // Group i of lane l of a token's L lanes: 4 experts from 4 (l + L i) on; -inf behind the last expert.
 template <bool BF16>
@@ -99,207 +187,277 @@ __device__ inline f32x4 experts_4(const void *p, long long row, int E, int e) {
   return v;
 }
 
-// Largest value of a token's lanes; a NaN passes by (it comes back through the sums).
+// Largest value of a token's lanes; a NaN passes by (it comes back through the sums).  0 where all are -inf, so that
+// no difference of infinities arises.
 template <int L>
 __device__ inline float lanes_max(float m) {
   const uint32_t k = token_max<L>(m == -__builtin_inff() ? 0u : order_key(m));
-  return k ? key_value(k) : -__builtin_inff();
+  return k ? key_value(k) : 0.0f;
 }
 
-// A token's logits as numerators of its probabilities: p over sp for the balance loss, and the maximum m and sum sz
-// of exp(x - m) for the z loss.  With softmax scores the two are one.
-template <int L, int G, bool SIGMOID>
+// A token's logits as numerators of its probabilities: p over sp for the balance loss, z over sz (exp(x - m)) for the
+// z loss.  With softmax scores the two are one.  The logistic is 1 / (1 + t) or t / (1 + t) with t = exp(-|x|); where
+// the largest logit is so low that 1 + t is 1, its ratios are the softmax's.
+constexpr float kLowLogit = -60.0f;
+template <int L, int G, bool SIGMOID, bool Z>
 struct TokenRow {
-  f32x4 x[G], p[G];
+  f32x4 p[G], z[SIGMOID && Z ? G : 1], rest[SIGMOID ? G : 1];  // rest: 1 - logistic
   float m, sp, sz;
-  template <bool BF16>
-  __device__ inline void read(const void *logits, long long t, int E, int l, bool z) {
-    const float ninf = -__builtin_inff();
-    m = ninf;
+  __device__ inline void work(const f32x4 (&x)[G]) {
+    m = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      x[i] = experts_4<BF16>(logits, t, E, 4 * (l + L * i));
+    for (int i = 0; i < G; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) m = fmaxf(m, x[i][j]);
-    }
     m = lanes_max<L>(m);
     sp = sz = 0.0f;
-    const float base = fminf(m, 0.0f);
 #pragma unroll
     for (int i = 0; i < G; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float v = x[i][j];
-        if (SIGMOID) {
-          p[i][j] = logistic_over(v, base);
-          if (z) sz += v == ninf ? 0.0f : expf(v - m);
+        if constexpr (SIGMOID) {
+          const float t = exp_of(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.0f + t), tr = t * r;
+          p[i][j] = v >= 0.0f ? r : tr;
+          rest[i][j] = v >= 0.0f ? tr : r;
+          if (m < kLowLogit) p[i][j] = exp_of(v - m);
+          if constexpr (Z) sz += z[i][j] = exp_of(v - m);
         } else {
-          p[i][j] = v == ninf ? 0.0f : expf(v - m);
+          p[i][j] = exp_of(v - m);
         }
         sp += p[i][j];
       }
     sp = token_sum<L>(sp);
-    sz = SIGMOID ? (z ? token_sum<L>(sz) : 0.0f) : sp;
+    sz = !SIGMOID ? sp : Z ? token_sum<L>(sz) : 0.0f;
+  }
+  __device__ inline float znum(int i, int j) const {
+    if constexpr (SIGMOID && Z) return z[i][j];
+    return p[i][j];
   }
   // log of the sum of exp(logits); 0 where all are -inf
   __device__ inline float lse() const { return sz == 0.0f ? 0.0f : m + logf(sz); }
 };
 
+template <int L, int G, bool BF16>
+__device__ inline void read_row(const void *logits, long long t, int E, int l, f32x4 (&x)[G]) {
+#pragma unroll
+  for (int i = 0; i < G; ++i) x[i] = experts_4<BF16>(logits, t, E, 4 * (l + L * i));
+}
+
 // Counts of sequence b as this lane's experts have them; 0 behind the last expert.
 template <int L, int G>
 __device__ inline void read_counts(const int32_t *counts, int b, int E, int l, f32x4 (&c)[G]) {
+  const int32_t *of = counts + (long long)b * E;
 #pragma unroll
-  for (int i = 0; i < G; ++i)
+  for (int i = 0; i < G; ++i) {
+    const int e = 4 * (l + L * i);
+    int v[4] = {0, 0, 0, 0};
+    if (e + 4 <= E)
+      __builtin_memcpy(v, of + e, 16);
+    else
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = 4 * (l + L * i) + j;
-      c[i][j] = e < E ? (float)counts[(long long)b * E + e] : 0.0f;
-    }
+      for (int j = 0; j < 4; ++j)
+        if (e + j < E) v[j] = of[e + j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[i][j] = (float)v[j];
+  }
 }
 
-// A workgroup per chunk of tokens: parts[chunk + sequence] = sums of sum_e c_e P_e and of lse^2.
-template <int L, int V, bool BF16, bool SIGMOID>
+// sum_e c_e P_e of token t (E / sum(c) is left out) and its lse^2, in all its lanes.
+template <int L, int V, bool BF16, bool SIGMOID, bool Z>
+__device__ inline float2 token_losses(const void *logits, const int32_t *counts, long long t, int b, int E, int l) {
+  constexpr int G = V / 4;
+  f32x4 x[G], c[G];
+  read_row<L, G, BF16>(logits, t, E, l, x);
+  read_counts<L, G>(counts, b, E, l, c);
+  TokenRow<L, G, SIGMOID, Z> r;
+  r.work(x);
+  float d = 0.0f;
+#pragma unroll
+  for (int q = 0; q < G; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d = fmaf(c[q][j], r.p[q][j], d);
+  d = token_sum<L>(d);
+  const float lse = Z ? r.lse() : 0.0f;
+  return {r.sp == 0.0f ? 0.0f : d / r.sp, lse * lse};
+}
+
+// A workgroup per chunk of tokens: parts[chunk + sequence] = sums of what token_losses gives.
+template <int L, int V, bool BF16, bool SIGMOID, bool Z>
 __global__ __launch_bounds__(kBalThreads) void k_balance_rows(const void *__restrict__ logits, Sequences s,
-                                                             const int32_t *__restrict__ counts, int E, bool z,
+                                                             const int32_t *__restrict__ counts, int E, int chunks,
                                                              float2 *__restrict__ parts) {
-  constexpr int G = V / 4, GROUPS = kBalThreads / L;
+  constexpr int GROUPS = kBalThreads / L;
   __shared__ float2 sum_of[kTokens];
   __shared__ int seq_of[kTokens];
   const int l = threadIdx.x % L;
-  for (int i = threadIdx.x / L; i < kTokens; i += GROUPS) {
-    const long long t = (long long)blockIdx.x * kTokens + i;
-    const int b = t < s.T ? sequence_of(s, (int)t) : s.n;
-    float2 v = {0.0f, 0.0f};
-    if (b >= 0 && b < s.n) {
-      TokenRow<L, G, SIGMOID> r;
-      r.template read<BF16>(logits, t, E, l, z);
-      f32x4 c[G];
-      read_counts<L, G>(counts, b, E, l, c);
-      float d = 0.0f;
-#pragma unroll
-      for (int q = 0; q < G; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) d += c[q][j] * r.p[q][j];
-      d = token_sum<L>(d);
-      v.x = r.sp == 0.0f ? 0.0f : d / r.sp;
-      v.y = r.lse() * r.lse();
+  for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+    const int t0 = chunk * kTokens, tn = min(kTokens, s.T - t0);
+    const int2 at = sequences_of(s, t0, t0 + tn - 1);
+    for (int i = threadIdx.x / L; i < kTokens; i += GROUPS) {
+      const int b = i < tn ? sequence_between(s, t0 + i, at) : s.n;
+      float2 v = {0.0f, 0.0f};
+      if (b >= 0 && b < s.n) v = token_losses<L, V, BF16, SIGMOID, Z>(logits, counts, t0 + i, b, E, l);
+      if (l == 0) sum_of[i] = v, seq_of[i] = b;
     }
-    if (l == 0) sum_of[i] = v, seq_of[i] = b;
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i < kTokens) {
+      const int b = seq_of[i];
+      if (b >= 0 && b < s.n && (i == 0 || seq_of[i - 1] != b)) {
+        float2 v = {0.0f, 0.0f};
+        for (int k = i; k < kTokens && seq_of[k] == b; ++k) v.x += sum_of[k].x, v.y += sum_of[k].y;
+        parts[(long long)chunk + b] = v;
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  const int i = threadIdx.x;
-  if (i >= kTokens) return;
-  const int b = seq_of[i];
-  if (b < 0 || b >= s.n || (i > 0 && seq_of[i - 1] == b)) return;
-  float2 v = {0.0f, 0.0f};
-  for (int k = i; k < kTokens && seq_of[k] == b; ++k) v.x += sum_of[k].x, v.y += sum_of[k].y;
-  parts[(long long)blockIdx.x + b] = v;
 }
 
-// Sum of one value per thread, the same in every thread, in a fixed order.
-__device__ inline double block_total(double v) {
-  __shared__ double part[kBalThreads / kWave];
+// Sum of one value over a wave, the same in every lane, in a fixed order.
+__device__ inline double wave_total(double v) {
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) v += __shfl_xor(v, off, kWave);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double sum = 0.0;
-#pragma unroll
-  for (int w = 0; w < kBalThreads / kWave; ++w) sum += part[w];
-  return sum;
+  return v;
+}
+
+// The losses of sequence b of n tokens: d and z summed over its tokens, c over its counts.
+__device__ inline void write_losses(int b, int n, int E, double d, double z, double c, float *balance, float *zloss) {
+  balance[b] = c > 0.0 ? (float)(d * E / (c * max(n, 1))) : 0.0f;
+  if (zloss) zloss[b] = (float)(z / max(n, 1));
 }
 
 // A workgroup per sequence: its partial sums added up, in 64 bits (there may be millions of tokens).
 __global__ __launch_bounds__(kBalThreads) void k_balance_total(const float2 *__restrict__ parts, Sequences s,
                                                               const int32_t *__restrict__ counts, int E,
                                                               float *__restrict__ balance, float *__restrict__ zloss) {
+  __shared__ double part[3][kBalThreads / kWave];
   const int b = blockIdx.x, lo = first_token(s, b), hi = last_token(s, b);
-  double d = 0.0, z = 0.0, c = 0.0;
+  double v[3] = {0.0, 0.0, 0.0};
   if (lo < hi) {
-    for (int i = lo / kTokens + threadIdx.x; i <= (hi - 1) / kTokens; i += kBalThreads) {
-      const float2 v = parts[(long long)i + b];
-      d += v.x, z += v.y;
+    const int last = (hi - 1) / kTokens;
+    for (int i0 = lo / kTokens + threadIdx.x; i0 <= last; i0 += 4 * kBalThreads) {
+      float2 t[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] = i0 + k * kBalThreads <= last ? parts[(long long)i0 + k * kBalThreads + b] : float2{0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[0] += t[k].x, v[1] += t[k].y;
     }
-    for (int e = threadIdx.x; e < E; e += kBalThreads) c += counts[(long long)b * E + e];
+    for (int e = threadIdx.x; e < E; e += kBalThreads) v[2] += counts[(long long)b * E + e];
   }
-  d = block_total(d);
-  z = block_total(z);
-  c = block_total(c);
-  if (threadIdx.x == 0) {
-    const double n = max(hi - lo, 1);
-    balance[b] = c > 0.0 ? (float)(d * E / (c * n)) : 0.0f;
-    if (zloss) zloss[b] = (float)(z / n);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    v[k] = wave_total(v[k]);
+    if ((threadIdx.x & 63) == 0) part[k][threadIdx.x >> 6] = v[k];
+  }
+  __syncthreads();
+  if (threadIdx.x) return;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    v[k] = 0.0;
+    for (int w = 0; w < kBalThreads / kWave; ++w) v[k] += part[k][w];
+  }
+  write_losses(b, hi - lo, E, v[0], v[1], v[2], balance, zloss);
+}
+
+// Few tokens: one workgroup for all of it.
+constexpr int kAloneThreads = 1024;
+constexpr int kAloneTokens = 256, kAloneSequences = 64;
+template <int L, int V, bool BF16, bool SIGMOID, bool Z>
+__global__ __launch_bounds__(kAloneThreads) void k_balance_alone(const void *__restrict__ logits, Sequences s,
+                                                                const int32_t *__restrict__ counts, int E,
+                                                                float *__restrict__ balance, float *__restrict__ zloss) {
+  constexpr int GROUPS = kAloneThreads / L;
+  __shared__ float2 sum_of[kAloneTokens];
+  const int l = threadIdx.x % L;
+  const int2 at = sequences_of(s, 0, max(s.T - 1, 0));
+  for (int t = threadIdx.x / L; t < s.T; t += GROUPS) {
+    const int b = sequence_between(s, t, at);
+    if (b < 0 || b >= s.n) continue;
+    const float2 v = token_losses<L, V, BF16, SIGMOID, Z>(logits, counts, t, b, E, l);
+    if (l == 0) sum_of[t] = v;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  for (int b = threadIdx.x >> 6; b < s.n; b += kAloneThreads / kWave) {
+    const int lo = first_token(s, b), hi = last_token(s, b);
+    double d = 0.0, z = 0.0, c = 0.0;
+    for (int t = lo + lane; t < hi; t += kWave) d += sum_of[t].x, z += sum_of[t].y;
+    if (lo < hi)
+      for (int e = lane; e < E; e += kWave) c += counts[(long long)b * E + e];
+    d = wave_total(d), z = wave_total(z), c = wave_total(c);
+    if (lane == 0) write_losses(b, hi - lo, E, d, z, c, balance, zloss);
   }
 }
 
 // dlogits of a token, with f_e = E c_e / sum(c) and D = sum_e f_e P_e:
 //   dbalance / n * P_e (f_e - D) [* (1 - logistic(x_e))]  +  2 dzloss / n * lse * softmax_e
-template <int L, int V, bool BF16, bool SIGMOID>
+template <int L, int V, bool BF16, bool SIGMOID, bool Z>
 __global__ __launch_bounds__(kBalThreads) void k_balance_bwd(const void *__restrict__ logits, Sequences s,
-                                                            const int32_t *__restrict__ counts, int E,
+                                                            const int32_t *__restrict__ counts, int E, int chunks,
                                                             const float *__restrict__ dbalance,
                                                             const float *__restrict__ dzloss, const void *add,
                                                             void *dlogits) {
   constexpr int G = V / 4, GROUPS = kBalThreads / L;
   const int l = threadIdx.x % L;
-  const float ninf = -__builtin_inff();
-  for (long long t = (long long)blockIdx.x * GROUPS + threadIdx.x / L; t < s.T; t += (long long)gridDim.x * GROUPS) {
-    const int b = sequence_of(s, (int)t);
-    if (b < 0 || b >= s.n) continue;
-    TokenRow<L, G, SIGMOID> r;
-    r.template read<BF16>(logits, t, E, l, dzloss != nullptr);
-    f32x4 c[G];
-    read_counts<L, G>(counts, b, E, l, c);
-    float d = 0.0f, total = 0.0f;
+  for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+    const int t0 = chunk * kTokens, tn = min(kTokens, s.T - t0);
+    const int2 at = sequences_of(s, t0, t0 + tn - 1);
+    for (int i = threadIdx.x / L; i < tn; i += GROUPS) {
+      const long long t = t0 + i;
+      f32x4 x[G], c[G], a[G];
+      read_row<L, G, BF16>(logits, t, E, l, x);
+      if (add) read_row<L, G, BF16>(add, t, E, l, a);
+      const int b = sequence_between(s, (int)t, at);
+      if (b < 0 || b >= s.n) continue;
+      read_counts<L, G>(counts, b, E, l, c);
+      const float rn = __builtin_amdgcn_rcpf((float)max(last_token(s, b) - first_token(s, b), 1));
+      float db = dbalance ? dbalance[b] * rn : 0.0f, dz = Z ? 2.0f * dzloss[b] * rn : 0.0f;
+      TokenRow<L, G, SIGMOID, Z> r;
+      r.work(x);
+      float d = 0.0f, total = 0.0f;
 #pragma unroll
-    for (int q = 0; q < G; ++q)
+      for (int q = 0; q < G; ++q)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d += c[q][j] * r.p[q][j], total += c[q][j];
-    d = token_sum<L>(d);
-    total = token_sum<L>(total);
-    const float n = (float)max(last_token(s, b) - first_token(s, b), 1);
-    const float rs = r.sp == 0.0f ? 0.0f : 1.0f / r.sp;
-    const float db = dbalance && total > 0.0f ? dbalance[b] / n * ((float)E / total) * rs : 0.0f;
-    const float dz = dzloss && r.sz != 0.0f ? 2.0f * dzloss[b] / n * r.lse() / r.sz : 0.0f;
-    d *= rs;
+        for (int j = 0; j < 4; ++j) d = fmaf(c[q][j], r.p[q][j], d), total += c[q][j];
+      d = token_sum<L>(d);
+      total = token_sum<L>(total);
+      const float rs = r.sp == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(r.sp);
+      db = total > 0.0f ? db * ((float)E * __builtin_amdgcn_rcpf(total)) * rs : 0.0f;
+      d *= rs;
+      if (Z) dz = r.sz == 0.0f ? 0.0f : dz * r.lse() * __builtin_amdgcn_rcpf(r.sz);
 #pragma unroll
-    for (int q = 0; q < G; ++q) {
-      const int e = 4 * (l + L * q);
-      if (e >= E) continue;
-      f32x4 g;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = r.x[q][j];
-        g[j] = db * r.p[q][j] * (c[q][j] - d);
-        if (SIGMOID) {
-          g[j] = x == ninf ? 0.0f : g[j] / (1.0f + expf(x));
-          if (dzloss) g[j] += x == ninf ? 0.0f : dz * expf(x - r.m);
-        } else {
-          g[j] += dz * r.p[q][j];
-        }
-      }
-      if (add) {
-        const f32x4 a = experts_4<BF16>(add, t, E, e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) g[j] += a[j];
-      }
-      const long long at = t * E + e;
-      if (e + 4 <= E) {
-        if constexpr (BF16) {
-          const uint2 o = {pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3])};
-          __builtin_memcpy((uint16_t *)dlogits + at, &o, 8);
-        } else {
-          __builtin_memcpy((float *)dlogits + at, &g, 16);
-        }
-      } else {
+      for (int q = 0; q < G; ++q) {
+        const int e = 4 * (l + L * q);
+        if (e >= E) continue;
+        f32x4 g;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (e + j >= E) continue;
-          if constexpr (BF16)
-            ((uint16_t *)dlogits)[at + j] = (uint16_t)pack_bf16x2(g[j], 0.0f);
-          else
-            ((float *)dlogits)[at + j] = g[j];
+          if constexpr (SIGMOID) {
+            g[j] = db * r.p[q][j] * (c[q][j] - d) * r.rest[q][j];
+            if (Z) g[j] = fmaf(dz, r.znum(q, j), g[j]);
+          } else {
+            g[j] = r.p[q][j] * fmaf(db, c[q][j] - d, dz);
+          }
+          if (add) g[j] += a[q][j];
+        }
+        const long long o = t * E + e;
+        if (e + 4 <= E) {
+          if constexpr (BF16) {
+            const uint2 w = {pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3])};
+            __builtin_memcpy((uint16_t *)dlogits + o, &w, 8);
+          } else {
+            __builtin_memcpy((float *)dlogits + o, &g, 16);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (e + j >= E) continue;
+            if constexpr (BF16)
+              ((uint16_t *)dlogits)[o + j] = (uint16_t)pack_bf16x2(g[j], 0.0f);
+            else
+              ((float *)dlogits)[o + j] = g[j];
+          }
         }
       }
     }
@@ -317,6 +475,21 @@ static void with_lanes(int E, F f) {
   else if (E <= 512) MOE_LANES(32, 16);
   else MOE_LANES(64, 16);
 #undef MOE_LANES
+}
+
+// Calls f with the type, the score and whether there is a z loss.
+template <class F>
+static void with_kind(moe_dtype dtype, moe_score score, bool z, F f) {
+  using std::bool_constant;
+  auto third = [&](auto bf16, auto sigmoid) { z ? f(bf16, sigmoid, std::true_type{}) : f(bf16, sigmoid, std::false_type{}); };
+  auto second = [&](auto bf16) { score == MOE_SCORE_SIGMOID ? third(bf16, std::true_type{}) : third(bf16, std::false_type{}); };
+  dtype == MOE_BF16 ? second(std::true_type{}) : second(std::false_type{});
+}
+
+// Workgroups that walk the chunks: as many as the chip holds.
+static int chunk_grid(int chunks) {
+  const int most = 8 * device_cu_count();
+  return chunks < most ? chunks : most;
 }
 
 static bool sequences_ok(int64_t T, int32_t E, int32_t n_seq, const int32_t *cu) {
@@ -338,11 +511,15 @@ extern "C" moe_status_t moe_expert_counts(int64_t T, int32_t E, int32_t K, const
       shares(counts, c_bytes, cu_tokens, ((size_t)n_seq + 1) * 4, false))
     return MOE_EINVAL;
   const Sequences s{cu_tokens, n_seq, (int)T};
-  const int64_t n = (int64_t)n_seq * E, fill = (n + kBalThreads - 1) / kBalThreads;
-  hipLaunchKernelGGL(k_count_zero, dim3((unsigned)(fill < 4096 ? fill : 4096)), dim3(kBalThreads), 0, stream, counts, n);
-  if (T)
-    hipLaunchKernelGGL(k_expert_counts, dim3(ceil_div(T, kCountTokens)), dim3(kBalThreads), 0, stream, topk_idx, s, E, K,
-                       counts);
+  if (T * K <= (int64_t)kCountAlone * n_seq && T * K <= kCountAlonePeak) {
+    hipLaunchKernelGGL(k_count_sequences, dim3(n_seq), dim3(kCountThreads), 0, stream, topk_idx, s, E, K, counts);
+    return launch_status();
+  }
+  const int64_t n = (int64_t)n_seq * E, fill = (n + kCountThreads - 1) / kCountThreads;
+  hipLaunchKernelGGL(k_count_zero, dim3((unsigned)(fill < 4096 ? fill : 4096)), dim3(kCountThreads), 0, stream, counts, n);
+  const int tokens = kCountIds / K < 1 ? 1 : kCountIds / K;
+  hipLaunchKernelGGL(k_count_chunks, dim3(ceil_div(T, tokens)), dim3(kCountThreads), 0, stream, topk_idx, s, E, K, tokens,
+                     counts);
   return launch_status();
 }
 
@@ -368,16 +545,22 @@ extern "C" moe_status_t moe_balance_loss(moe_dtype dtype, moe_score score, int64
     return MOE_EINVAL;
   const Sequences s{cu_tokens, n_seq, (int)T};
   float2 *parts = (float2 *)ws;
-  auto go = [&](auto bf16, auto sigmoid) {
-    with_lanes(E, [&](auto l, auto v) {
-      hipLaunchKernelGGL((k_balance_rows<l.value, v.value, bf16.value, sigmoid.value>), dim3(ceil_div(T, kTokens)),
-                         dim3(kBalThreads), 0, stream, logits, s, counts, E, zloss != nullptr, parts);
+  const bool alone = T <= kAloneTokens && n_seq <= kAloneSequences;
+  const int chunks = ceil_div(T, kTokens);
+  if (T)
+    with_kind(dtype, score, zloss != nullptr, [&](auto bf16, auto sigmoid, auto z) {
+      with_lanes(E, [&](auto l, auto v) {
+        if (alone)
+          hipLaunchKernelGGL((k_balance_alone<l.value, v.value, bf16.value, sigmoid.value, z.value>), dim3(1),
+                             dim3(kAloneThreads), 0, stream, logits, s, counts, E, balance, zloss);
+        else
+          hipLaunchKernelGGL((k_balance_rows<l.value, v.value, bf16.value, sigmoid.value, z.value>), dim3(chunk_grid(chunks)),
+                             dim3(kBalThreads), 0, stream, logits, s, counts, E, chunks, parts);
+      });
     });
-  };
-  auto scores = [&](auto bf16) { score == MOE_SCORE_SIGMOID ? go(bf16, std::true_type{}) : go(bf16, std::false_type{}); };
-  if (T) dtype == MOE_BF16 ? scores(std::true_type{}) : scores(std::false_type{});
-  hipLaunchKernelGGL(k_balance_total, dim3(n_seq), dim3(kBalThreads), 0, stream, (const float2 *)parts, s, counts, E,
-                     balance, zloss);
+  if (!T || !alone)
+    hipLaunchKernelGGL(k_balance_total, dim3(n_seq), dim3(kBalThreads), 0, stream, (const float2 *)parts, s, counts, E,
+                       balance, zloss);
   return launch_status();
 }
 
@@ -398,15 +581,12 @@ extern "C" moe_status_t moe_balance_loss_backward(moe_dtype dtype, moe_score sco
                       {cu_tokens, o_bytes + 4}, {dbalance, o_bytes}, {dzloss, o_bytes}};
   if (!stands_alone(dlogits, bytes, in, 6, true)) return MOE_EINVAL;
   const Sequences s{cu_tokens, n_seq, (int)T};
-  auto go = [&](auto bf16, auto sigmoid) {
+  const int chunks = ceil_div(T, kTokens);
+  with_kind(dtype, score, dzloss != nullptr, [&](auto bf16, auto sigmoid, auto z) {
     with_lanes(E, [&](auto l, auto v) {
-      const int64_t groups = kBalThreads / l.value, blocks = (T + groups - 1) / groups;
-      hipLaunchKernelGGL((k_balance_bwd<l.value, v.value, bf16.value, sigmoid.value>),
-                         dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(kBalThreads), 0, stream, logits, s,
-                         counts, E, dbalance, dzloss, add, dlogits);
+      hipLaunchKernelGGL((k_balance_bwd<l.value, v.value, bf16.value, sigmoid.value, z.value>), dim3(chunk_grid(chunks)),
+                         dim3(kBalThreads), 0, stream, logits, s, counts, E, chunks, dbalance, dzloss, add, dlogits);
     });
-  };
-  auto scores = [&](auto bf16) { score == MOE_SCORE_SIGMOID ? go(bf16, std::true_type{}) : go(bf16, std::false_type{}); };
-  dtype == MOE_BF16 ? scores(std::true_type{}) : scores(std::false_type{});
+  });
   return launch_status();
 }
