@@ -92,7 +92,7 @@ struct NormArgs {
 };
 
 // Rows of 8 to 8 CHUNKS threads columns.  The next row's loads are under way while a row is summed and written.
-template <bool BF16, bool RMS, bool DROP, int LANES, int CHUNKS>
+template <bool BF16, bool RMS, bool DROP, bool STREAM, int LANES, int CHUNKS>
 __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k_norm(NormArgs a) {
   __shared__ float part[2][kNormMaxWaves];
   RowThreads<LANES> me(part);
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
   auto fetch = [&](Raw<BF16> *to, const void *from, long long row) {
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i)
-      to[i].load(row_at(from, bytes_of<BF16>(row * W)), Run(me.t, me.count, i, W).at);
+      to[i].template load<STREAM>(row_at(from, bytes_of<BF16>(row * W)), Run(me.t, me.count, i, W).at);
   };
   const bool early = a.residual && !a.late, late = a.residual && a.late;
   if (me.row < a.rows) {
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
 #pragma unroll
       for (int i = 0; i < CHUNKS; ++i) {
         const Run u(me.t, me.count, i, W);
-        if (u.skip < 8) Raw<BF16>(h[i]).store(row_at(a.total, bytes_of<BF16>(base)), u.at);
+        if (u.skip < 8) Raw<BF16>(h[i]).template store<STREAM>(row_at(a.total, bytes_of<BF16>(base)), u.at);
       }
     const float mean = RMS ? 0.0f : sum;
     float var = sum;
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
       if (!KEEP) weights(i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] = fmaf(h[i][j] * rstd, w[i][j], b[i][j]);
-      Raw<BF16>(h[i]).store(row_at(a.y, bytes_of<BF16>(base)), u.at);
+      Raw<BF16>(h[i]).template store<STREAM>(row_at(a.y, bytes_of<BF16>(base)), u.at);
     }
     if (more && late) fetch(r, a.residual, row + me.step);
     if (me.t == 0) {
@@ -245,7 +245,7 @@ struct NormBwdArgs {
   Drop drop;
 };
 
-template <bool BF16, bool RMS, bool DROP, int LANES, int CHUNKS>
+template <bool BF16, bool RMS, bool DROP, bool STREAM, int LANES, int CHUNKS>
 __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k_norm_bwd(NormBwdArgs a) {
   __shared__ float part[2][kNormMaxWaves];
   RowThreads<LANES> me(part);
@@ -264,9 +264,9 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
       const Run u(me.t, me.count, i, W);
-      t[i].load(row_at(a.total, bytes), u.at);
-      d[i].load(row_at(a.dy, bytes), u.at);
-      if (a.dtotal) q[i].load(row_at(a.dtotal, bytes), u.at);
+      t[i].template load<STREAM>(row_at(a.total, bytes), u.at);
+      d[i].template load<STREAM>(row_at(a.dy, bytes), u.at);
+      if (a.dtotal) q[i].template load<STREAM>(row_at(a.dtotal, bytes), u.at);
     }
     if (!RMS) mean = a.mean[row];
     rstd = a.rstd[row];
@@ -328,9 +328,9 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
         g[i][j] = fmaf(-xh[i][j], sgx, g[i][j]);
         if (!RMS) g[i][j] -= sg;
       }
-      if (a.dresidual) Raw<BF16>(g[i]).store(row_at(a.dresidual, bytes_of<BF16>(base)), u.at);
+      if (a.dresidual) Raw<BF16>(g[i]).template store<STREAM>(row_at(a.dresidual, bytes_of<BF16>(base)), u.at);
       if (DROP) drop_8(drop_bits((unsigned long long)(base + u.at), key), a.drop, g[i]);
-      Raw<BF16>(g[i]).store(row_at(a.dx, bytes_of<BF16>(base)), u.at);
+      Raw<BF16>(g[i]).template store<STREAM>(row_at(a.dx, bytes_of<BF16>(base)), u.at);
     }
   }
   if (!a.parts) return;
@@ -482,32 +482,40 @@ constexpr int kNormMaxWidth = 1 << 22;
 
 static bool row_kept(int64_t width) { return width >= kNormNarrowest && width <= kNormWidest; }
 
-// Calls f with the lanes of a row (0: a workgroup), the steps of a thread, the workgroup's threads and its rows.
+// Calls f with whether a call that moves so many bytes streams them, the lanes of a row (0: a workgroup), the steps of a
+// thread, the workgroup's threads and its rows.
 template <class F>
-static void with_row(int W, F f) {
+static void with_row(int W, int64_t moved, F f) {
+  using std::false_type;
   using std::integral_constant;
-#define MOE_ROW(l, c, threads, rows) f(integral_constant<int, l>{}, integral_constant<int, c>{}, threads, rows)
+  using std::true_type;
+#define MOE_ROW(s, l, c, threads, rows) f(s, integral_constant<int, l>{}, integral_constant<int, c>{}, threads, rows)
   auto waves = [&](int chunks) { return ceil_div(W, 8 * chunks * kWave) * kWave; };
-  if (W <= 128) MOE_ROW(16, 1, kNormLanesThreads, 16);
-  else if (W <= 256) MOE_ROW(32, 1, kNormLanesThreads, 8);
-  else if (W <= 512) MOE_ROW(64, 1, kNormLanesThreads, 4);
-  else if (W <= 8 * kNormMaxThreads) MOE_ROW(0, 1, waves(1), 1);
-  else MOE_ROW(0, 2, waves(2), 1);
+  const bool stream = moved >= kStreamBytes;
+  if (W <= 128) MOE_ROW(false_type{}, 16, 1, kNormLanesThreads, 16);
+  else if (W <= 256) MOE_ROW(false_type{}, 32, 1, kNormLanesThreads, 8);
+  else if (W <= 512) MOE_ROW(false_type{}, 64, 1, kNormLanesThreads, 4);
+  else if (W <= 8 * kNormMaxThreads && stream) MOE_ROW(true_type{}, 0, 1, waves(1), 1);
+  else if (W <= 8 * kNormMaxThreads) MOE_ROW(false_type{}, 0, 1, waves(1), 1);
+  else if (stream) MOE_ROW(true_type{}, 0, 2, waves(2), 1);
+  else MOE_ROW(false_type{}, 0, 2, waves(2), 1);
 #undef MOE_ROW
 }
 
-// Workgroups per CU that walk the rows, from the bytes each has under way (the next row's loads): enough for the
-// memory's latency and no more, since what is under way beyond that only spreads the accesses (see k_norm).
+// Workgroups per CU that walk the rows, from the bytes each has under way (the next row's loads): enough for the memory's
+// latency and no more, since more of them only spread the accesses.  32768 x 4096 bf16 rms with residual (16 KB under way
+// in each) take 181 us with 1 and 199 with 2, 65536 x 2048 (8 KB) 253, 180 and 206 with 1, 2 and 4; without residual
+// 32768 x 7168 (14 KB) 221 and 187 with 1 and 2; the gradient of 16384 x 2048 (12 KB) 71, 55, 57 and 62 with 1 to 4.
 static int per_cu(int64_t under_way, int64_t wanted) {
-  const int64_t n = (wanted + under_way / 2) / under_way;
-  return (int)(n < 1 ? 1 : n > 8 ? 8 : n);
+  const int64_t n = (wanted + under_way - 1) / under_way;
+  return (int)(n > 8 ? 8 : n);
 }
-constexpr int64_t kNormUnderWay = 16 << 10, kNormBwdUnderWay = 24 << 10;
+constexpr int64_t kNormUnderWay = 16 << 10, kNormBwdUnderWay = 20 << 10;
 
 static int norm_parts(int64_t rows, int64_t width, int64_t bytes) {
   int64_t groups = rows, most = kColParts;
   if (row_kept(width))
-    with_row((int)width, [&](auto, auto, int threads, int per) {
+    with_row((int)width, 0, [&](auto, auto, auto, int threads, int per) {
       groups = (rows + per - 1) / per;
       most = (int64_t)device_cu_count() * per_cu(bytes * per * width, kNormBwdUnderWay);
     });
@@ -515,7 +523,8 @@ static int norm_parts(int64_t rows, int64_t width, int64_t bytes) {
   return (int)(groups < most ? groups : most);
 }
 
-// Threads of the kernels that read a row again.
+// Threads of the kernels that read a row again, and their largest grid (2^32 threads are too many for a launch).
+constexpr int64_t kAnyMaxGrid = 1 << 20;
 static int any_threads(int64_t width) { return width >= 8 * kNormMaxThreads ? kNormMaxThreads : ceil_div(width, 8 * kWave) * kWave; }
 
 static bool norm_args_ok(moe_dtype dtype, moe_norm_kind kind, moe_dtype w_dtype, int64_t rows, int64_t width) {
@@ -551,15 +560,16 @@ extern "C" moe_status_t moe_layer_norm(moe_dtype dtype, moe_norm_kind kind, moe_
              make_drop(p, rng, offset)};
   auto go = [&](auto bf16, auto rms, auto drop) {
     if (!row_kept(width)) {
-      hipLaunchKernelGGL((k_norm_any<bf16.value, rms.value, drop.value>), dim3((unsigned)(rows < (1 << 22) ? rows : 1 << 22)),
+      hipLaunchKernelGGL((k_norm_any<bf16.value, rms.value, drop.value>), dim3((unsigned)(rows < kAnyMaxGrid ? rows : kAnyMaxGrid)),
                          dim3(any_threads(width)), 0, stream, a);
       return;
     }
-    with_row((int)width, [&](auto l, auto c, int threads, int per) {
+    with_row((int)width, (int64_t)bytes * (2 + (residual ? 1 : 0) + (total ? 1 : 0)), [&](auto st, auto l, auto c, int threads, int per) {
       const int64_t groups = (rows + per - 1) / per, one = (int64_t)size * per * width;
+      // a residual that would double what is under way beyond that waits (32768 x 7168: 359 us, 324 with it late)
       a.late = 2 * one > kNormUnderWay + kNormUnderWay / 4;
-      const int64_t most = (int64_t)device_cu_count() * per_cu(residual && !a.late ? 2 * one : one, kNormUnderWay);
-      hipLaunchKernelGGL((k_norm<bf16.value, rms.value, drop.value, l.value, c.value>),
+      const int64_t most = (int64_t)device_cu_count() * per_cu(residual ? 2 * one : one, kNormUnderWay);
+      hipLaunchKernelGGL((k_norm<bf16.value, rms.value, drop.value, st.value, l.value, c.value>),
                          dim3((unsigned)(groups < most ? groups : most)), dim3(threads), 0, stream, a);
     });
   };
@@ -612,12 +622,12 @@ extern "C" moe_status_t moe_layer_norm_backward(moe_dtype dtype, moe_norm_kind k
       if (sums)  // before dx, which may take dy's place
         hipLaunchKernelGGL((k_norm_cols<bf16.value, rms.value>), dim3(ceil_div(width, kColThreads), parts),
                            dim3(kColThreads), 0, stream, a);
-      hipLaunchKernelGGL((k_norm_bwd_any<bf16.value, rms.value, drop.value>), dim3((unsigned)(rows < (1 << 22) ? rows : 1 << 22)),
+      hipLaunchKernelGGL((k_norm_bwd_any<bf16.value, rms.value, drop.value>), dim3((unsigned)(rows < kAnyMaxGrid ? rows : kAnyMaxGrid)),
                          dim3(any_threads(width)), 0, stream, a);
       return;
     }
-    with_row((int)width, [&](auto l, auto c, int threads, int) {
-      hipLaunchKernelGGL((k_norm_bwd<bf16.value, rms.value, drop.value, l.value, c.value>), dim3(parts), dim3(threads), 0,
+    with_row((int)width, (int64_t)bytes * (3 + (dtotal ? 1 : 0) + (dresidual ? 1 : 0)), [&](auto st, auto l, auto c, int threads, int) {
+      hipLaunchKernelGGL((k_norm_bwd<bf16.value, rms.value, drop.value, st.value, l.value, c.value>), dim3(parts), dim3(threads), 0,
                          stream, a);
     });
   };
