@@ -44,16 +44,22 @@ projections.  The weight gradients stay on the 16-bit rows.
 Around the step: route() makes this rank's expert ids and weights from its gate's logits,
 route_backward() the logits' gradient from the step's router-weight gradient, and clip_gradients()
 scales the expert gradients (and any others given) to a largest global norm.
+In a transformer block (``norm="layer"`` or ``"rms"``): enter() adds the branch before the layer to the
+residual stream, with dropout, and normalises the sum into this rank's token rows; leave() adds the
+layer's output, with dropout; leave_backward() and enter_backward() are their gradients.
+count_experts(), balance_loss() and balance_loss_backward() are the gate's balance and z losses, for each
+of ``sequences`` packed sequences.
 """
 from dataclasses import dataclass
 
 import torch
 
-from . import (GEMM_DGRAD, GEMM_FWD, GEMM_WGRAD, MoeError, dims as _mk_dims, dispatch_layout_workspace_bytes,
-               grad_sumsq_workspace_bytes, group_gemm_workspace_bytes, moe_combine, moe_combine_weight_grad,
-               moe_dispatch_layout, moe_grad_clip, moe_grad_sumsq, moe_group_gemm,
-               moe_group_gemm_gather, moe_group_gemm_scaled, moe_group_gemm_swiglu,
-               moe_permute, moe_plan, moe_plan_noalloc,
+from . import (GEMM_DGRAD, GEMM_FWD, GEMM_WGRAD, NORMS, MoeError, balance_loss_workspace_bytes, dims as _mk_dims,
+               dispatch_layout_workspace_bytes, grad_sumsq_workspace_bytes, group_gemm_workspace_bytes,
+               layer_norm_backward_workspace_bytes, moe_balance_loss, moe_balance_loss_backward, moe_combine,
+               moe_combine_weight_grad, moe_dispatch_layout, moe_dropout, moe_expert_counts, moe_grad_clip,
+               moe_grad_sumsq, moe_group_gemm, moe_group_gemm_gather, moe_group_gemm_scaled, moe_group_gemm_swiglu,
+               moe_layer_norm, moe_layer_norm_backward, moe_permute, moe_plan, moe_plan_noalloc,
                moe_prefetch, moe_quant_rows, moe_quant_weight, moe_replica_grad_fold,
                moe_router_backward, moe_router_topk, moe_swiglu_backward, moe_unpermute_reduce,
                plan_words, plan_workspace_bytes, scale_row_bytes)
@@ -113,8 +119,12 @@ class LayerStep:
     def __init__(self, shape: Shape, rank: int = 0, dtype=torch.bfloat16, device="cuda",
                  backward: bool = True, activation: str = "identity", fused_gather: bool = False,
                  plan_noalloc: bool = False, overlap=None, gemm: str = "bf16",
-                 grad_format=torch.float8_e4m3fn):
+                 grad_format=torch.float8_e4m3fn, norm=None, sequences: int = 1):
         s = shape
+        if norm is not None and norm not in NORMS:
+            raise ValueError(f"norm {norm!r}")
+        if sequences < 1:
+            raise ValueError(f"sequences {sequences}")
         if activation not in ("identity", "swiglu"):
             raise ValueError(f"activation {activation!r}")
         if fused_gather and (activation != "identity" or dtype != torch.bfloat16):
@@ -168,6 +178,15 @@ class LayerStep:
             self.quantised_from = None   # what quantise_weights() read (_weights)
             e4 = torch.float8_e4m3fn
             self.xq, self.zq = QuantRows(s.SK, s.H, e4, device), QuantRows(s.SK, s.Hp, e4, device)
+        self.norm = norm
+        if norm is not None:  # the residual stream at the layer, and what enter() leaves for its gradient
+            self.total = torch.zeros((s.S, s.H), **act)
+            self.norm_mean = torch.zeros(s.S, **f32) if norm == "layer" else None
+            self.norm_rstd = torch.zeros(s.S, **f32)
+            self.norm_ws = torch.empty(layer_norm_backward_workspace_bytes(s.S, s.H) if backward else 0, dtype=torch.uint8,
+                                       device=device)
+        self.seq_counts = torch.zeros((sequences, s.E), **i32)
+        self.balance_ws = torch.empty(balance_loss_workspace_bytes(s.S, sequences), dtype=torch.uint8, device=device)
         self.backward_enabled = backward
         # the backward's side stream (default priority) and its fork/join events; by default
         # only where the GEMMs are long enough for the kernels beside them to gain more than
@@ -251,6 +270,64 @@ class LayerStep:
         self._check_logits(logits)
         moe_router_backward(logits, self.topk_idx[self.rank],
                             self.dtopk_w.view(self.s.S, self.s.K), dlogits, score, factor)
+
+    @property
+    def tokens(self):
+        """This rank's token rows (its slice of x_all): what enter() writes and the gate and the dispatch read."""
+        r, S = self.rank, self.s.S
+        return self.x_all[r * S:(r + 1) * S]
+
+    def _check_rows(self, **rows):
+        if self.norm is None:
+            raise ValueError("the layer was made without a norm")
+        for name, t in rows.items():
+            if t is not None and tuple(t.shape) != (self.s.S, self.s.H):
+                raise MoeError(f"{name} of shape {tuple(t.shape)}, expected (S, H) = ({self.s.S}, {self.s.H})")
+
+    def enter(self, x, weight, bias=None, residual=None, eps=1e-5, p=0.0, rng=None, offset=0):
+        """total = residual + dropout(x) (kept for leave()), normalised into this rank's token rows."""
+        self._check_rows(x=x, residual=residual)
+        moe_layer_norm(x, weight, self.tokens, bias=bias, eps=eps, kind=self.norm, residual=residual, total=self.total,
+                       mean=self.norm_mean, rstd=self.norm_rstd, p=p, rng=rng, offset=offset)
+
+    def leave(self, out, p=0.0, rng=None, offset=0):
+        """out = total + dropout(the layer's output): the residual stream behind the layer (out may be total)."""
+        self._check_rows(out=out)
+        moe_dropout(self.out, out, p, rng, residual=self.total, offset=offset)
+
+    def leave_backward(self, dout, p=0.0, rng=None, offset=0):
+        """This rank's rows of the layer's output gradient (dout_all) from the gradient behind leave(), with its p, rng and
+        offset; dout itself is total's (enter_backward's dtotal)."""
+        self._check_rows(dout=dout)
+        r, S = self.rank, self.s.S
+        moe_dropout(dout, self.dout_all[r * S:(r + 1) * S], p, rng, offset=offset)
+
+    def enter_backward(self, dy, weight, dx, dweight, dbias=None, dtotal=None, dresidual=None, accumulate=False, p=0.0,
+                       rng=None, offset=0):
+        """The gradients of enter(), with its weight, p, rng and offset, from the token rows' gradient dy (the layer's dx and
+        the gate's together) and total's by other ways (dtotal).  leave() has not written over total since."""
+        self._check_rows(dy=dy, dx=dx, dtotal=dtotal, dresidual=dresidual)
+        moe_layer_norm_backward(self.total, weight, self.norm_rstd, dy, dx, dweight, self.norm_ws, dbias=dbias,
+                                mean=self.norm_mean, kind=self.norm, dtotal=dtotal, dresidual=dresidual,
+                                accumulate=accumulate, p=p, rng=rng, offset=offset)
+
+    def count_experts(self, cu_tokens=None):
+        """Copies that this rank's tokens send to each expert, for each sequence [cu_tokens[b], cu_tokens[b + 1]) of them:
+        seq_counts [sequences, E], which balance_loss() and its gradient read.  Ranks that share the loss add theirs up
+        in between (an all-reduce)."""
+        moe_expert_counts(self.topk_idx[self.rank], self.seq_counts, cu_tokens)
+        return self.seq_counts
+
+    def balance_loss(self, logits, balance, zloss=None, score="softmax_topk", cu_tokens=None):
+        """The balance loss and z loss of each sequence (fp32 [sequences]) from the gate's logits [S, E] and seq_counts."""
+        self._check_logits(logits)
+        moe_balance_loss(logits, self.seq_counts, balance, self.balance_ws, zloss, score, cu_tokens)
+
+    def balance_loss_backward(self, logits, dlogits, dbalance=None, dzloss=None, score="softmax_topk", cu_tokens=None,
+                              add=None):
+        """dlogits = add + the losses' gradient; add may be dlogits itself, as route_backward() left it."""
+        self._check_logits(logits)
+        moe_balance_loss_backward(logits, self.seq_counts, dlogits, dbalance, dzloss, score, cu_tokens, add)
 
     def clip_gradients(self, max_norm, others=()):
         """Scales the experts' weight gradients of this rank, and the gradients in `others`, in place to a

@@ -179,3 +179,52 @@ def test_weights_put_into_8_bits_elsewhere(layer, monkeypatch):
     L.weights_quantised = False
     with pytest.raises(ValueError, match="quantise_weights"):
         L.forward()
+
+
+def test_a_block_takes_rows_of_this_layer(layer, monkeypatch):
+    """enter(), leave() and their gradients take [S, H] tensors, on a layer that was made with a norm."""
+    seen = []
+    for name in ("moe_layer_norm", "moe_layer_norm_backward", "moe_dropout"):
+        monkeypatch.setattr(layer, name, lambda *a, **k: seen.append((a, k)))
+    x = torch.zeros(4, 32)
+    L = step_of(layer, norm="rms", x_all=torch.zeros(8, 32), out=x.clone(), total=x.clone(), norm_mean=None,
+                norm_rstd=torch.zeros(4), norm_ws=torch.zeros(8), dout_all=torch.zeros(8, 32))
+    w = torch.ones(32)
+    calls = (lambda L, t: L.enter(t, w), lambda L, t: L.enter(x, w, residual=t), lambda L, t: L.leave(t),
+             lambda L, t: L.leave_backward(t), lambda L, t: L.enter_backward(t, w, x, w), lambda L, t: L.enter_backward(x, w, t, w),
+             lambda L, t: L.enter_backward(x, w, x, w, dtotal=t), lambda L, t: L.enter_backward(x, w, x, w, dresidual=t))
+    for call in calls:
+        for bad in (torch.zeros(5, 32), torch.zeros(4, 31), torch.zeros(128)):
+            with pytest.raises(layer.MoeError, match="expected"):
+                call(L, bad)
+        with pytest.raises(ValueError, match="without a norm"):
+            call(step_of(layer, norm=None), x)
+    assert not seen
+    for call in calls:
+        call(L, x)
+    assert len(seen) == len(calls)
+    # the rank's own rows: [4, 8) of x_all and dout_all
+    assert seen[0][0][2].data_ptr() == L.x_all[4:].data_ptr() and seen[3][0][1].data_ptr() == L.dout_all[4:].data_ptr()
+
+
+def test_balance_loss_takes_logits_of_this_layers_experts(layer, monkeypatch):
+    seen = []
+    for name in ("moe_expert_counts", "moe_balance_loss", "moe_balance_loss_backward"):
+        monkeypatch.setattr(layer, name, lambda *a, **k: seen.append(a))
+    L = step_of(layer, seq_counts=torch.zeros(1, 6, dtype=torch.int32), balance_ws=None)
+    for bad in (torch.zeros(4, 7), torch.zeros(5, 6), torch.zeros(24)):
+        with pytest.raises(layer.MoeError, match="logits"):
+            L.balance_loss(bad, torch.zeros(1))
+        with pytest.raises(layer.MoeError, match="logits"):
+            L.balance_loss_backward(bad, bad)
+    assert not seen
+    assert L.count_experts() is L.seq_counts
+    L.balance_loss(torch.zeros(4, 6), torch.zeros(1))
+    L.balance_loss_backward(torch.zeros(4, 6), torch.zeros(4, 6))
+    assert len(seen) == 3 and seen[0][0].data_ptr() == L.topk_idx[1].data_ptr()
+
+
+def test_norm_and_sequences_are_checked(layer):
+    for kw in (dict(norm="batch"), dict(sequences=0)):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            layer.LayerStep(layer.Shape(2, 4, 2, 6, 1, 32, 16), device="cpu", **kw)
