@@ -456,6 +456,9 @@ def moe_grad_clip(grads, sumsq, max_norm, norm=None, out=None, stream=None):
                               _on(dev, stream)), "moe_grad_clip")
 
 
+_F32, _INT32, _INT64 = (torch.float32,), (torch.int32,), (torch.int64,)
+
+
 def _maybe(dev, name, t, dtypes, numel):
     """The address of a tensor that may be left out."""
     return None if t is None else _take(dev, name, t, dtypes, numel)
@@ -463,13 +466,15 @@ def _maybe(dev, name, t, dtypes, numel):
 
 def _drop_args(dev, p, rng, offset):
     """(p, address of the seed and offset, the further offset) of a dropout."""
+    if p == 0.0:
+        return 0.0, None, 0
     if not 0.0 <= p <= 1.0:
         raise MoeError(f"p {p}, expected 0 to 1")
-    if p > 0.0 and rng is None:
+    if rng is None:
         raise MoeError("dropout without rng (int64: seed, offset)")
     if not -(1 << 63) <= offset < 1 << 63:
         raise MoeError(f"offset {offset}, expected a 64-bit number")
-    return p, _maybe(dev, "rng", rng, (torch.int64,), 2), offset
+    return p, _take(dev, "rng", rng, _INT64, 2), offset
 
 
 def moe_dropout(x, out, p, rng, residual=None, offset=0, stream=None):
@@ -478,10 +483,10 @@ def moe_dropout(x, out, p, rng, residual=None, offset=0, stream=None):
     same call on out's gradient, without the residual."""
     dev = _current("x", x)
     p, rp, offset = _drop_args(dev, p, rng, offset)
-    same = (x.dtype,)
-    _check(_lib.moe_dropout(_dtype(x), x.numel(), _take(dev, "x", x, _FLOATS, None),
-                            _maybe(dev, "residual", residual, same, x.numel()), p, rp, offset,
-                            _take(dev, "out", out, same, x.numel()), _on(dev, stream)), "moe_dropout")
+    dt, same, n = _dtype(x), (x.dtype,), x.numel()
+    _check(_lib.moe_dropout(dt, n, _take(dev, "x", x, same, n),
+                            None if residual is None else _take(dev, "residual", residual, same, n), p, rp, offset,
+                            _take(dev, "out", out, same, n), _on(dev, stream)), "moe_dropout")
 
 
 def _kind(kind):
@@ -491,10 +496,11 @@ def _kind(kind):
 
 
 def _rows(name, x):
-    """Rows and width of x: its last dimension is a row."""
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise MoeError(f"{name}: shape {tuple(x.shape)}, expected rows of at least one value")
-    return x.numel() // x.shape[-1], x.shape[-1]
+    """Rows, width and elements of x: its last dimension is a row."""
+    shape, n = x.shape, x.numel()
+    if not shape or shape[-1] < 1:
+        raise MoeError(f"{name}: shape {tuple(shape)}, expected rows of at least one value")
+    return n // shape[-1], shape[-1], n
 
 
 def moe_layer_norm(x, weight, y, bias=None, eps=1e-5, kind="layer", residual=None, total=None, mean=None, rstd=None,
@@ -502,16 +508,16 @@ def moe_layer_norm(x, weight, y, bias=None, eps=1e-5, kind="layer", residual=Non
     """y = (h - mean) rstd weight + bias over the last dimension, h = residual + dropout(x) (see moe_dropout);
     total receives h, mean and rstd (fp32) what the backward takes.  kind "rms": mean 0."""
     dev = _current("x", x)
-    rows, width = _rows("x", x)
+    rows, width, n = _rows("x", x)
     p, rp, offset = _drop_args(dev, p, rng, offset)
-    same, n = (x.dtype,), x.numel()
-    _check(_lib.moe_layer_norm(_dtype(x), _kind(kind), _dtype(weight), rows, width, _take(dev, "x", x, _FLOATS, None),
-                               _maybe(dev, "residual", residual, same, n),
-                               _take(dev, "weight", weight, _FLOATS, width),
-                               _maybe(dev, "bias", bias, (weight.dtype,), width), eps, p, rp, offset,
-                               _maybe(dev, "total", total, same, n), _take(dev, "y", y, same, n),
-                               _maybe(dev, "mean", mean, (torch.float32,), rows),
-                               _maybe(dev, "rstd", rstd, (torch.float32,), rows), _on(dev, stream)), "moe_layer_norm")
+    dt, same = _dtype(x), (x.dtype,)
+    _check(_lib.moe_layer_norm(
+        dt, _kind(kind), _dtype(weight), rows, width, _take(dev, "x", x, same, n),
+        None if residual is None else _take(dev, "residual", residual, same, n), _take(dev, "weight", weight, _FLOATS, width),
+        None if bias is None else _take(dev, "bias", bias, (weight.dtype,), width), eps, p, rp, offset,
+        None if total is None else _take(dev, "total", total, same, n), _take(dev, "y", y, same, n),
+        None if mean is None else _take(dev, "mean", mean, _F32, rows),
+        None if rstd is None else _take(dev, "rstd", rstd, _F32, rows), _on(dev, stream)), "moe_layer_norm")
 
 
 def layer_norm_backward_workspace_bytes(rows, width):
@@ -524,15 +530,17 @@ def moe_layer_norm_backward(total, weight, rstd, dy, dx, dweight=None, ws=None, 
     (fp32, added to what they hold with accumulate).  total is h, dtotal the gradient that reaches it by other ways;
     ws: scratch of layer_norm_backward_workspace_bytes(rows, width) bytes for dweight and dbias."""
     dev = _current("total", total)
-    rows, width = _rows("total", total)
+    rows, width, n = _rows("total", total)
     p, rp, offset = _drop_args(dev, p, rng, offset)
-    same, n, f32 = (total.dtype,), total.numel(), (torch.float32,)
+    dt, same = _dtype(total), (total.dtype,)
     _check(_lib.moe_layer_norm_backward(
-        _dtype(total), _kind(kind), _dtype(weight), rows, width, _take(dev, "total", total, _FLOATS, None),
-        _take(dev, "weight", weight, _FLOATS, width), _maybe(dev, "mean", mean, f32, rows),
-        _take(dev, "rstd", rstd, f32, rows), _take(dev, "dy", dy, same, n), _maybe(dev, "dtotal", dtotal, same, n),
-        p, rp, offset, _take(dev, "dx", dx, same, n), _maybe(dev, "dresidual", dresidual, same, n),
-        _maybe(dev, "dweight", dweight, f32, width), _maybe(dev, "dbias", dbias, f32, width), int(bool(accumulate)),
+        dt, _kind(kind), _dtype(weight), rows, width, _take(dev, "total", total, same, n),
+        _take(dev, "weight", weight, _FLOATS, width), None if mean is None else _take(dev, "mean", mean, _F32, rows),
+        _take(dev, "rstd", rstd, _F32, rows), _take(dev, "dy", dy, same, n),
+        None if dtotal is None else _take(dev, "dtotal", dtotal, same, n), p, rp, offset, _take(dev, "dx", dx, same, n),
+        None if dresidual is None else _take(dev, "dresidual", dresidual, same, n),
+        None if dweight is None else _take(dev, "dweight", dweight, _F32, width),
+        None if dbias is None else _take(dev, "dbias", dbias, _F32, width), int(bool(accumulate)),
         None if ws is None else _take(dev, "ws", ws, (ws.dtype,), None),
         0 if ws is None else ws.numel() * ws.element_size(), _on(dev, stream)), "moe_layer_norm_backward")
 
@@ -558,8 +566,8 @@ def moe_expert_counts(topk_idx, counts, cu_tokens=None, stream=None):
     (T, K), E = topk_idx.shape, counts.shape[-1]
     n, cp = _sequences(dev, cu_tokens)
     _int32(K, E)
-    _check(_lib.moe_expert_counts(T, E, K, _take(dev, "topk_idx", topk_idx, (torch.int32,), None), n, cp,
-                                  _take(dev, "counts", counts, (torch.int32,), n * E), _on(dev, stream)),
+    _check(_lib.moe_expert_counts(T, E, K, _take(dev, "topk_idx", topk_idx, _INT32, None), n, cp,
+                                  _take(dev, "counts", counts, _INT32, n * E), _on(dev, stream)),
            "moe_expert_counts")
 
 
@@ -583,10 +591,9 @@ def moe_balance_loss(logits, counts, balance, ws, zloss=None, score="softmax_top
     zloss[b] = mean logsumexp^2, from logits [T, E]; P: softmax, or the logistic over its sum (score "sigmoid").
     ws: scratch of balance_loss_workspace_bytes(T, sequences) bytes."""
     dev, T, E, n, cp = _logits("moe_balance_loss", logits, cu_tokens)
-    f32 = (torch.float32,)
     _check(_lib.moe_balance_loss(_dtype(logits), _score(score), T, E, _take(dev, "logits", logits, _FLOATS, None), n, cp,
-                                 _take(dev, "counts", counts, (torch.int32,), n * E),
-                                 _take(dev, "balance", balance, f32, n), _maybe(dev, "zloss", zloss, f32, n),
+                                 _take(dev, "counts", counts, _INT32, n * E),
+                                 _take(dev, "balance", balance, _F32, n), _maybe(dev, "zloss", zloss, _F32, n),
                                  _take(dev, "ws", ws, (ws.dtype,), None), ws.numel() * ws.element_size(),
                                  _on(dev, stream)), "moe_balance_loss")
 
@@ -596,10 +603,10 @@ def moe_balance_loss_backward(logits, counts, dlogits, dbalance=None, dzloss=Non
     """dlogits = add + the gradient of sum_b dbalance[b] balance[b] + dzloss[b] zloss[b], the counts held fixed; add
     may be dlogits itself.  Rows of tokens in no sequence are left as they are."""
     dev, T, E, n, cp = _logits("moe_balance_loss_backward", logits, cu_tokens)
-    f32, same = (torch.float32,), (logits.dtype,)
+    same = (logits.dtype,)
     _check(_lib.moe_balance_loss_backward(_dtype(logits), _score(score), T, E,
                                           _take(dev, "logits", logits, _FLOATS, None), n, cp,
-                                          _take(dev, "counts", counts, (torch.int32,), n * E),
-                                          _maybe(dev, "dbalance", dbalance, f32, n), _maybe(dev, "dzloss", dzloss, f32, n),
+                                          _take(dev, "counts", counts, _INT32, n * E),
+                                          _maybe(dev, "dbalance", dbalance, _F32, n), _maybe(dev, "dzloss", dzloss, _F32, n),
                                           _maybe(dev, "add", add, same, T * E), _take(dev, "dlogits", dlogits, same, T * E),
                                           _on(dev, stream)), "moe_balance_loss_backward")

@@ -14,7 +14,7 @@ namespace moe {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalMaxE = 1024;
-constexpr int kTokens = 16;  // tokens per chunk
+constexpr int kMinTokens = 4, kMaxTokens = 256;  // tokens per chunk
 
 struct Sequences {
   const int32_t *cu;  // NULL: one of all T tokens
@@ -82,8 +82,8 @@ __device__ inline int last_token(const Sequences &s, int b) { return s.cu ? min(
 
 constexpr int kCountThreads = 1024;
 constexpr int kCountCopies = 4;      // of the bins, lanes taking turns: a popular expert's ids meet in one place less often
-constexpr int kCountIds = 8192;      // about as many ids a workgroup
-constexpr int kCountAlone = 16384;   // ids of a sequence that one workgroup counts by itself
+constexpr int kCountIds = 2048;      // about as many ids a workgroup
+constexpr int kCountAlone = 32768;   // ids of a sequence that one workgroup counts by itself
 constexpr int kCountAlonePeak = 65536;
 
 struct Bins {
@@ -164,27 +164,48 @@ constexpr float kLog2e = 1.44269504f;
 // exp(d): the argument is rounded in the product with log2(e), below 2^-126 the result is 0.
 __device__ inline float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
-// Group i of lane l of a token's L lanes: 4 experts from 4 (l + L i) on; -inf behind the last expert.
+// Four logits as they lie in memory, -inf behind the last expert.
 template <bool BF16>
-__device__ inline f32x4 experts_4(const void *p, long long row, int E, int e) {
-  const float ninf = -__builtin_inff();
-  f32x4 v = {ninf, ninf, ninf, ninf};
-  const long long i = row * E + e;
-  const int n = E - e;
-  if (n >= 4) {
-    if constexpr (BF16) {
-      uint2 q;
-      __builtin_memcpy(&q, (const uint16_t *)p + i, 8);
-      v = (f32x4){bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+struct Raw4;
+
+template <>
+struct Raw4<true> {
+  uint2 t;
+  __device__ inline void load(const void *p, long long i, int n) {
+    const uint16_t *q = (const uint16_t *)p + i;
+    if (n >= 4) {
+      __builtin_memcpy(&t, q, 8);
     } else {
-      __builtin_memcpy(&v, (const float *)p + i, 16);
+      t.x = (n > 0 ? q[0] : 0xFF80u) | (n > 1 ? (uint32_t)q[1] : 0xFF80u) << 16;
+      t.y = (n > 2 ? q[2] : 0xFF80u) | 0xFF800000u;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < n) v[j] = load_logit<BF16>(p, i + j);
   }
-  return v;
+  __device__ inline f32x4 values() const { return (f32x4){bf16_lo(t.x), bf16_hi(t.x), bf16_lo(t.y), bf16_hi(t.y)}; }
+};
+
+template <>
+struct Raw4<false> {
+  f32x4 t;
+  __device__ inline void load(const void *p, long long i, int n) {
+    const float *q = (const float *)p + i;
+    if (n >= 4) {
+      __builtin_memcpy(&t, q, 16);
+    } else {
+      const float ninf = -__builtin_inff();
+      t = (f32x4){n > 0 ? q[0] : ninf, n > 1 ? q[1] : ninf, n > 2 ? q[2] : ninf, ninf};
+    }
+  }
+  __device__ inline f32x4 values() const { return t; }
+};
+
+// Token t's row in the registers of its L lanes: group i of lane l holds the 4 experts from 4 (l + L i) on.
+template <int L, int G, bool BF16>
+__device__ inline void read_row(const void *logits, long long t, int E, int l, Raw4<BF16> (&x)[G]) {
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int e = 4 * (l + L * i);
+    x[i].load(logits, t * E + e, E - e);
+  }
 }
 
 // Largest value of a token's lanes; a NaN passes by (it comes back through the sums).  0 where all are -inf, so that
@@ -203,7 +224,11 @@ template <int L, int G, bool SIGMOID, bool Z>
 struct TokenRow {
   f32x4 p[G], z[SIGMOID && Z ? G : 1], rest[SIGMOID ? G : 1];  // rest: 1 - logistic
   float m, sp, sz;
-  __device__ inline void work(const f32x4 (&x)[G]) {
+  template <bool BF16>
+  __device__ inline void work(const Raw4<BF16> (&raw)[G]) {
+    f32x4 x[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) x[i] = raw[i].values();
     m = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < G; ++i)
@@ -238,12 +263,6 @@ struct TokenRow {
   __device__ inline float lse() const { return sz == 0.0f ? 0.0f : m + logf(sz); }
 };
 
-template <int L, int G, bool BF16>
-__device__ inline void read_row(const void *logits, long long t, int E, int l, f32x4 (&x)[G]) {
-#pragma unroll
-  for (int i = 0; i < G; ++i) x[i] = experts_4<BF16>(logits, t, E, 4 * (l + L * i));
-}
-
 // Counts of sequence b as this lane's experts have them; 0 behind the last expert.
 template <int L, int G>
 __device__ inline void read_counts(const int32_t *counts, int b, int E, int l, f32x4 (&c)[G]) {
@@ -263,13 +282,9 @@ __device__ inline void read_counts(const int32_t *counts, int b, int E, int l, f
   }
 }
 
-// sum_e c_e P_e of token t (E / sum(c) is left out) and its lse^2, in all its lanes.
-template <int L, int V, bool BF16, bool SIGMOID, bool Z>
-__device__ inline float2 token_losses(const void *logits, const int32_t *counts, long long t, int b, int E, int l) {
-  constexpr int G = V / 4;
-  f32x4 x[G], c[G];
-  read_row<L, G, BF16>(logits, t, E, l, x);
-  read_counts<L, G>(counts, b, E, l, c);
+// sum_e c_e P_e of a token (E / sum(c) is left out) and its lse^2, in all its lanes.
+template <int L, int G, bool BF16, bool SIGMOID, bool Z>
+__device__ inline float2 token_losses(const Raw4<BF16> (&x)[G], const f32x4 (&c)[G]) {
   TokenRow<L, G, SIGMOID, Z> r;
   r.work(x);
   float d = 0.0f;
@@ -279,39 +294,63 @@ __device__ inline float2 token_losses(const void *logits, const int32_t *counts,
     for (int j = 0; j < 4; ++j) d = fmaf(c[q][j], r.p[q][j], d);
   d = token_sum<L>(d);
   const float lse = Z ? r.lse() : 0.0f;
-  return {r.sp == 0.0f ? 0.0f : d / r.sp, lse * lse};
+  return {r.sp == 0.0f ? 0.0f : d * __builtin_amdgcn_rcpf(r.sp), lse * lse};
 }
 
-// A workgroup per chunk of tokens: parts[chunk + sequence] = sums of what token_losses gives.
+// A workgroup per chunk of `tokens` tokens: parts[chunk + sequence] = sums of what token_losses gives.  Where the chunk
+// lies in one sequence, the counts stay in registers and a group adds up its tokens' by itself.
 template <int L, int V, bool BF16, bool SIGMOID, bool Z>
 __global__ __launch_bounds__(kBalThreads) void k_balance_rows(const void *__restrict__ logits, Sequences s,
-                                                             const int32_t *__restrict__ counts, int E, int chunks,
+                                                             const int32_t *__restrict__ counts, int E, int tokens,
                                                              float2 *__restrict__ parts) {
-  constexpr int GROUPS = kBalThreads / L;
-  __shared__ float2 sum_of[kTokens];
-  __shared__ int seq_of[kTokens];
-  const int l = threadIdx.x % L;
-  for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-    const int t0 = chunk * kTokens, tn = min(kTokens, s.T - t0);
-    const int2 at = sequences_of(s, t0, t0 + tn - 1);
-    for (int i = threadIdx.x / L; i < kTokens; i += GROUPS) {
-      const int b = i < tn ? sequence_between(s, t0 + i, at) : s.n;
-      float2 v = {0.0f, 0.0f};
-      if (b >= 0 && b < s.n) v = token_losses<L, V, BF16, SIGMOID, Z>(logits, counts, t0 + i, b, E, l);
-      if (l == 0) sum_of[i] = v, seq_of[i] = b;
+  constexpr int G = V / 4, GROUPS = kBalThreads / L;
+  __shared__ float2 sum_of[kMaxTokens];
+  __shared__ int seq_of[kMaxTokens];
+  const int l = threadIdx.x % L, group = threadIdx.x / L;
+  const int t0 = blockIdx.x * tokens, tn = min(tokens, s.T - t0);
+  Raw4<BF16> x[G];
+  if (group < tn) read_row<L, G, BF16>(logits, t0 + group, E, l, x);
+  const int2 at = sequences_of(s, t0, t0 + tn - 1);
+  f32x4 c[G];
+  if (at.x == at.y) {
+    const int b = at.x;
+    if (b < 0 || b >= s.n) return;
+    read_counts<L, G>(counts, b, E, l, c);
+    float2 v = {0.0f, 0.0f};
+    for (int i = group; i < tn; i += GROUPS) {
+      Raw4<BF16> now[G];
+#pragma unroll
+      for (int q = 0; q < G; ++q) now[q] = x[q];
+      if (i + GROUPS < tn) read_row<L, G, BF16>(logits, t0 + i + GROUPS, E, l, x);
+      const float2 one = token_losses<L, G, BF16, SIGMOID, Z>(now, c);
+      v.x += one.x, v.y += one.y;
     }
+    if (l == 0) sum_of[group] = v;
     __syncthreads();
-    const int i = threadIdx.x;
-    if (i < kTokens) {
-      const int b = seq_of[i];
-      if (b >= 0 && b < s.n && (i == 0 || seq_of[i - 1] != b)) {
-        float2 v = {0.0f, 0.0f};
-        for (int k = i; k < kTokens && seq_of[k] == b; ++k) v.x += sum_of[k].x, v.y += sum_of[k].y;
-        parts[(long long)chunk + b] = v;
-      }
-    }
-    __syncthreads();
+    if (threadIdx.x) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) v.x += sum_of[g].x, v.y += sum_of[g].y;
+    parts[(long long)blockIdx.x + b] = v;
+    return;
   }
+  for (int i = group; i < tn; i += GROUPS) {
+    const int b = sequence_between(s, t0 + i, at);
+    float2 v = {0.0f, 0.0f};
+    if (b >= 0 && b < s.n) {
+      read_row<L, G, BF16>(logits, t0 + i, E, l, x);
+      read_counts<L, G>(counts, b, E, l, c);
+      v = token_losses<L, G, BF16, SIGMOID, Z>(x, c);
+    }
+    if (l == 0) sum_of[i] = v, seq_of[i] = b;
+  }
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i >= tn) return;
+  const int b = seq_of[i];
+  if (b < 0 || b >= s.n || (i > 0 && seq_of[i - 1] == b)) return;
+  double d = 0.0, z = 0.0;
+  for (int k = i; k < tn && seq_of[k] == b; ++k) d += sum_of[k].x, z += sum_of[k].y;
+  parts[(long long)blockIdx.x + b] = {(float)d, (float)z};
 }
 
 // Sum of one value over a wave, the same in every lane, in a fixed order.
@@ -328,20 +367,20 @@ __device__ inline void write_losses(int b, int n, int E, double d, double z, dou
 }
 
 // A workgroup per sequence: its partial sums added up, in 64 bits (there may be millions of tokens).
-__global__ __launch_bounds__(kBalThreads) void k_balance_total(const float2 *__restrict__ parts, Sequences s,
+__global__ __launch_bounds__(kBalThreads) void k_balance_total(const float2 *__restrict__ parts, Sequences s, int tokens,
                                                               const int32_t *__restrict__ counts, int E,
                                                               float *__restrict__ balance, float *__restrict__ zloss) {
   __shared__ double part[3][kBalThreads / kWave];
   const int b = blockIdx.x, lo = first_token(s, b), hi = last_token(s, b);
   double v[3] = {0.0, 0.0, 0.0};
   if (lo < hi) {
-    const int last = (hi - 1) / kTokens;
-    for (int i0 = lo / kTokens + threadIdx.x; i0 <= last; i0 += 4 * kBalThreads) {
-      float2 t[4];
+    const int last = (hi - 1) / tokens;
+    for (int i0 = lo / tokens + threadIdx.x; i0 <= last; i0 += 8 * kBalThreads) {
+      float2 t[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) t[k] = i0 + k * kBalThreads <= last ? parts[(long long)i0 + k * kBalThreads + b] : float2{0.0f, 0.0f};
+      for (int k = 0; k < 8; ++k) t[k] = i0 + k * kBalThreads <= last ? parts[(long long)i0 + k * kBalThreads + b] : float2{0.0f, 0.0f};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[0] += t[k].x, v[1] += t[k].y;
+      for (int k = 0; k < 8; ++k) v[0] += t[k].x, v[1] += t[k].y;
     }
     for (int e = threadIdx.x; e < E; e += kBalThreads) v[2] += counts[(long long)b * E + e];
   }
@@ -374,7 +413,11 @@ __global__ __launch_bounds__(kAloneThreads) void k_balance_alone(const void *__r
   for (int t = threadIdx.x / L; t < s.T; t += GROUPS) {
     const int b = sequence_between(s, t, at);
     if (b < 0 || b >= s.n) continue;
-    const float2 v = token_losses<L, V, BF16, SIGMOID, Z>(logits, counts, t, b, E, l);
+    Raw4<BF16> x[V / 4];
+    f32x4 c[V / 4];
+    read_row<L, V / 4, BF16>(logits, t, E, l, x);
+    read_counts<L, V / 4>(counts, b, E, l, c);
+    const float2 v = token_losses<L, V / 4, BF16, SIGMOID, Z>(x, c);
     if (l == 0) sum_of[t] = v;
   }
   __syncthreads();
@@ -390,77 +433,114 @@ __global__ __launch_bounds__(kAloneThreads) void k_balance_alone(const void *__r
   }
 }
 
+// What a sequence brings to its tokens' gradients: its counts and their sum, dbalance / n E / sum(c), 2 dzloss / n.
+template <int L, int G, bool Z>
+struct SequenceGrad {
+  f32x4 c[G];
+  float kb, kz;
+  __device__ inline void read(const Sequences &s, const int32_t *counts, int b, int E, int l, const float *dbalance,
+                              const float *dzloss) {
+    read_counts<L, G>(counts, b, E, l, c);
+    const float n = (float)max(last_token(s, b) - first_token(s, b), 1);
+    const float db = dbalance ? dbalance[b] : 0.0f;
+    kz = Z ? 2.0f * dzloss[b] / n : 0.0f;
+    float total = 0.0f;
+#pragma unroll
+    for (int q = 0; q < G; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) total += c[q][j];
+    total = token_sum<L>(total);
+    kb = total > 0.0f ? db / n * ((float)E / total) : 0.0f;
+  }
+};
+
 // dlogits of a token, with f_e = E c_e / sum(c) and D = sum_e f_e P_e:
 //   dbalance / n * P_e (f_e - D) [* (1 - logistic(x_e))]  +  2 dzloss / n * lse * softmax_e
+template <int L, int G, bool BF16, bool SIGMOID, bool Z>
+__device__ inline void token_grad(const Raw4<BF16> (&x)[G], const Raw4<BF16> (&a)[G], bool add,
+                                  const SequenceGrad<L, G, Z> &s, void *dlogits, long long t, int E, int l) {
+  TokenRow<L, G, SIGMOID, Z> r;
+  r.work(x);
+  float d = 0.0f;
+#pragma unroll
+  for (int q = 0; q < G; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d = fmaf(s.c[q][j], r.p[q][j], d);
+  const float rs = r.sp == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(r.sp);
+  d = token_sum<L>(d) * rs;
+  const float kb = s.kb * rs, kz = Z && r.sz != 0.0f ? s.kz * r.lse() * __builtin_amdgcn_rcpf(r.sz) : 0.0f;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int e = 4 * (l + L * q);
+    if (e >= E) continue;
+    f32x4 g;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (SIGMOID) {
+        g[j] = kb * r.p[q][j] * (s.c[q][j] - d) * r.rest[q][j];
+        if (Z) g[j] = fmaf(kz, r.znum(q, j), g[j]);
+      } else {
+        g[j] = r.p[q][j] * fmaf(kb, s.c[q][j] - d, kz);
+      }
+    }
+    if (add) g += a[q].values();
+    const long long o = t * E + e;
+    if (e + 4 <= E) {
+      if constexpr (BF16) {
+        const uint2 w = {pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3])};
+        __builtin_memcpy((uint16_t *)dlogits + o, &w, 8);
+      } else {
+        __builtin_memcpy((float *)dlogits + o, &g, 16);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (e + j >= E) continue;
+        if constexpr (BF16)
+          ((uint16_t *)dlogits)[o + j] = (uint16_t)pack_bf16x2(g[j], 0.0f);
+        else
+          ((float *)dlogits)[o + j] = g[j];
+      }
+    }
+  }
+}
+
+// A workgroup per chunk of tokens, as in k_balance_rows.
 template <int L, int V, bool BF16, bool SIGMOID, bool Z>
 __global__ __launch_bounds__(kBalThreads) void k_balance_bwd(const void *__restrict__ logits, Sequences s,
-                                                            const int32_t *__restrict__ counts, int E, int chunks,
+                                                            const int32_t *__restrict__ counts, int E, int tokens,
                                                             const float *__restrict__ dbalance,
                                                             const float *__restrict__ dzloss, const void *add,
                                                             void *dlogits) {
   constexpr int G = V / 4, GROUPS = kBalThreads / L;
-  const int l = threadIdx.x % L;
-  for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-    const int t0 = chunk * kTokens, tn = min(kTokens, s.T - t0);
-    const int2 at = sequences_of(s, t0, t0 + tn - 1);
-    for (int i = threadIdx.x / L; i < tn; i += GROUPS) {
-      const long long t = t0 + i;
-      f32x4 x[G], c[G], a[G];
-      read_row<L, G, BF16>(logits, t, E, l, x);
-      if (add) read_row<L, G, BF16>(add, t, E, l, a);
-      const int b = sequence_between(s, (int)t, at);
-      if (b < 0 || b >= s.n) continue;
-      read_counts<L, G>(counts, b, E, l, c);
-      const float rn = __builtin_amdgcn_rcpf((float)max(last_token(s, b) - first_token(s, b), 1));
-      float db = dbalance ? dbalance[b] * rn : 0.0f, dz = Z ? 2.0f * dzloss[b] * rn : 0.0f;
-      TokenRow<L, G, SIGMOID, Z> r;
-      r.work(x);
-      float d = 0.0f, total = 0.0f;
+  const int l = threadIdx.x % L, group = threadIdx.x / L;
+  const int t0 = blockIdx.x * tokens, tn = min(tokens, s.T - t0);
+  Raw4<BF16> x[G], a[G];
+  auto fetch = [&](int i) {
+    read_row<L, G, BF16>(logits, t0 + i, E, l, x);
+    if (add) read_row<L, G, BF16>(add, t0 + i, E, l, a);
+  };
+  if (group < tn) fetch(group);
+  const int2 at = sequences_of(s, t0, t0 + tn - 1);
+  SequenceGrad<L, G, Z> of;
+  if (at.x == at.y) {
+    if (at.x < 0 || at.x >= s.n) return;
+    of.read(s, counts, at.x, E, l, dbalance, dzloss);
+    for (int i = group; i < tn; i += GROUPS) {
+      Raw4<BF16> now[G], plus[G];
 #pragma unroll
-      for (int q = 0; q < G; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) d = fmaf(c[q][j], r.p[q][j], d), total += c[q][j];
-      d = token_sum<L>(d);
-      total = token_sum<L>(total);
-      const float rs = r.sp == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(r.sp);
-      db = total > 0.0f ? db * ((float)E * __builtin_amdgcn_rcpf(total)) * rs : 0.0f;
-      d *= rs;
-      if (Z) dz = r.sz == 0.0f ? 0.0f : dz * r.lse() * __builtin_amdgcn_rcpf(r.sz);
-#pragma unroll
-      for (int q = 0; q < G; ++q) {
-        const int e = 4 * (l + L * q);
-        if (e >= E) continue;
-        f32x4 g;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (SIGMOID) {
-            g[j] = db * r.p[q][j] * (c[q][j] - d) * r.rest[q][j];
-            if (Z) g[j] = fmaf(dz, r.znum(q, j), g[j]);
-          } else {
-            g[j] = r.p[q][j] * fmaf(db, c[q][j] - d, dz);
-          }
-          if (add) g[j] += a[q][j];
-        }
-        const long long o = t * E + e;
-        if (e + 4 <= E) {
-          if constexpr (BF16) {
-            const uint2 w = {pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3])};
-            __builtin_memcpy((uint16_t *)dlogits + o, &w, 8);
-          } else {
-            __builtin_memcpy((float *)dlogits + o, &g, 16);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (e + j >= E) continue;
-            if constexpr (BF16)
-              ((uint16_t *)dlogits)[o + j] = (uint16_t)pack_bf16x2(g[j], 0.0f);
-            else
-              ((float *)dlogits)[o + j] = g[j];
-          }
-        }
-      }
+      for (int q = 0; q < G; ++q) now[q] = x[q], plus[q] = a[q];
+      if (i + GROUPS < tn) fetch(i + GROUPS);
+      token_grad<L, G, BF16, SIGMOID, Z>(now, plus, add != nullptr, of, dlogits, t0 + i, E, l);
     }
+    return;
+  }
+  for (int i = group; i < tn; i += GROUPS) {
+    const int b = sequence_between(s, t0 + i, at);
+    if (b < 0 || b >= s.n) continue;
+    fetch(i);
+    of.read(s, counts, b, E, l, dbalance, dzloss);
+    token_grad<L, G, BF16, SIGMOID, Z>(x, a, add != nullptr, of, dlogits, t0 + i, E, l);
   }
 }
 
@@ -486,10 +566,12 @@ static void with_kind(moe_dtype dtype, moe_score score, bool z, F f) {
   dtype == MOE_BF16 ? second(std::true_type{}) : second(std::false_type{});
 }
 
-// Workgroups that walk the chunks: as many as the chip holds.
-static int chunk_grid(int chunks) {
-  const int most = 8 * device_cu_count();
-  return chunks < most ? chunks : most;
+// Tokens per chunk: one for each group of lanes until the chip is full of workgroups.
+constexpr int kChunksPerCu = 8;
+static int chunk_tokens(int64_t T, int lanes) {
+  const int groups = kBalThreads / lanes;
+  const int64_t n = T / ((int64_t)groups * kChunksPerCu * device_cu_count()) * groups;
+  return (int)(n < groups ? groups : n > kMaxTokens ? kMaxTokens : n);
 }
 
 static bool sequences_ok(int64_t T, int32_t E, int32_t n_seq, const int32_t *cu) {
@@ -525,7 +607,7 @@ extern "C" moe_status_t moe_expert_counts(int64_t T, int32_t E, int32_t K, const
 
 extern "C" size_t moe_balance_loss_workspace_bytes(int64_t T, int32_t n_seq) {
   if (T < 0 || T >= (1LL << 31) || n_seq < 1) return 0;
-  return ((size_t)ceil_div(T, kTokens) + n_seq) * sizeof(float2);
+  return ((size_t)ceil_div(T, kMinTokens) + n_seq) * sizeof(float2);
 }
 
 extern "C" moe_status_t moe_balance_loss(moe_dtype dtype, moe_score score, int64_t T, int32_t E,
@@ -546,20 +628,21 @@ extern "C" moe_status_t moe_balance_loss(moe_dtype dtype, moe_score score, int64
   const Sequences s{cu_tokens, n_seq, (int)T};
   float2 *parts = (float2 *)ws;
   const bool alone = T <= kAloneTokens && n_seq <= kAloneSequences;
-  const int chunks = ceil_div(T, kTokens);
+  int tokens = kMinTokens;
   if (T)
     with_kind(dtype, score, zloss != nullptr, [&](auto bf16, auto sigmoid, auto z) {
       with_lanes(E, [&](auto l, auto v) {
+        tokens = chunk_tokens(T, l.value);
         if (alone)
           hipLaunchKernelGGL((k_balance_alone<l.value, v.value, bf16.value, sigmoid.value, z.value>), dim3(1),
                              dim3(kAloneThreads), 0, stream, logits, s, counts, E, balance, zloss);
         else
-          hipLaunchKernelGGL((k_balance_rows<l.value, v.value, bf16.value, sigmoid.value, z.value>), dim3(chunk_grid(chunks)),
-                             dim3(kBalThreads), 0, stream, logits, s, counts, E, chunks, parts);
+          hipLaunchKernelGGL((k_balance_rows<l.value, v.value, bf16.value, sigmoid.value, z.value>), dim3(ceil_div(T, tokens)),
+                             dim3(kBalThreads), 0, stream, logits, s, counts, E, tokens, parts);
       });
     });
   if (!T || !alone)
-    hipLaunchKernelGGL(k_balance_total, dim3(n_seq), dim3(kBalThreads), 0, stream, (const float2 *)parts, s, counts, E,
+    hipLaunchKernelGGL(k_balance_total, dim3(n_seq), dim3(kBalThreads), 0, stream, (const float2 *)parts, s, tokens, counts, E,
                        balance, zloss);
   return launch_status();
 }
@@ -581,11 +664,11 @@ extern "C" moe_status_t moe_balance_loss_backward(moe_dtype dtype, moe_score sco
                       {cu_tokens, o_bytes + 4}, {dbalance, o_bytes}, {dzloss, o_bytes}};
   if (!stands_alone(dlogits, bytes, in, 6, true)) return MOE_EINVAL;
   const Sequences s{cu_tokens, n_seq, (int)T};
-  const int chunks = ceil_div(T, kTokens);
   with_kind(dtype, score, dzloss != nullptr, [&](auto bf16, auto sigmoid, auto z) {
     with_lanes(E, [&](auto l, auto v) {
-      hipLaunchKernelGGL((k_balance_bwd<l.value, v.value, bf16.value, sigmoid.value, z.value>), dim3(chunk_grid(chunks)),
-                         dim3(kBalThreads), 0, stream, logits, s, counts, E, chunks, dbalance, dzloss, add, dlogits);
+      const int tokens = chunk_tokens(T, l.value);
+      hipLaunchKernelGGL((k_balance_bwd<l.value, v.value, bf16.value, sigmoid.value, z.value>), dim3(ceil_div(T, tokens)),
+                         dim3(kBalThreads), 0, stream, logits, s, counts, E, tokens, dbalance, dzloss, add, dlogits);
     });
   });
   return launch_status();

@@ -194,4 +194,4 @@ def test_binding_refuses_tensors_off_the_gpu(m):
     with pytest.raises(m.MoeError, match="kind"):
         m._kind("batch")
     with pytest.raises(m.MoeError, match="64-bit"):
-        m._drop_args(0, 0.0, None, 1 << 63)
+        m._drop_args(0, 0.5, torch.zeros(2, dtype=torch.int64), 1 << 63)
