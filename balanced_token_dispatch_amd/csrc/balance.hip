@@ -3,8 +3,15 @@
 //
 // balance[b] = E / sum(c) * mean_s sum_e c_e P[s, e] needs no mean of P: the counts are known before the
 // logits are read, so each token's sum over its experts stays in its lanes, and the tokens' sums are
-// added up in chunks of kTokens.  A chunk's tokens of one sequence give one partial sum, at place (chunk +
+// added up in chunks of tokens.  A chunk's tokens of one sequence give one partial sum, at place (chunk +
 // sequence): along the tokens one of the two grows with each new partial sum, so no place is taken twice.
+//
+// Latency-bound at usual sizes, by the exponentials at many tokens and by HBM at many experts; in a graph, us:
+//   tokens x experts, sequences      counts (K = 8)   losses   gradient (added to the router's)
+//   64 x 64, 1 (K = 6)                2.0              3.9      3.5
+//   8192 x 384 fp32, 4                3.8              8.9      8.5
+//   32768 x 256 bf16 logistic, 61     8.5              14       17     (25 MB and 50 MB move in 4 and 9)
+//   65536 x 1024 fp32, 16             7.8              47       161    (5.6 and 5.0 TB/s)
 #include <type_traits>
 
 #include "lanes.hpp"
@@ -401,7 +408,8 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_total(const float2 *__r
 
 // Few tokens: one workgroup for all of it.
 constexpr int kAloneThreads = 1024;
-constexpr int kAloneTokens = 256, kAloneSequences = 64;
+constexpr int kAlonePasses = 3;  // tokens a group of lanes (1.5 us each, where the second launch costs 2 and the host 2.7)
+constexpr int kAloneTokens = kAlonePasses * kAloneThreads / 16, kAloneSequences = 64;
 template <int L, int V, bool BF16, bool SIGMOID, bool Z>
 __global__ __launch_bounds__(kAloneThreads) void k_balance_alone(const void *__restrict__ logits, Sequences s,
                                                                 const int32_t *__restrict__ counts, int E,
@@ -627,12 +635,13 @@ extern "C" moe_status_t moe_balance_loss(moe_dtype dtype, moe_score score, int64
     return MOE_EINVAL;
   const Sequences s{cu_tokens, n_seq, (int)T};
   float2 *parts = (float2 *)ws;
-  const bool alone = T <= kAloneTokens && n_seq <= kAloneSequences;
+  bool alone = false;
   int tokens = kMinTokens;
   if (T)
     with_kind(dtype, score, zloss != nullptr, [&](auto bf16, auto sigmoid, auto z) {
       with_lanes(E, [&](auto l, auto v) {
         tokens = chunk_tokens(T, l.value);
+        alone = T <= kAlonePasses * kAloneThreads / l.value && n_seq <= kAloneSequences;
         if (alone)
           hipLaunchKernelGGL((k_balance_alone<l.value, v.value, bf16.value, sigmoid.value, z.value>), dim3(1),
                              dim3(kAloneThreads), 0, stream, logits, s, counts, E, balance, zloss);
@@ -641,7 +650,7 @@ extern "C" moe_status_t moe_balance_loss(moe_dtype dtype, moe_score score, int64
                              dim3(kBalThreads), 0, stream, logits, s, counts, E, tokens, parts);
       });
     });
-  if (!T || !alone)
+  if (!alone)
     hipLaunchKernelGGL(k_balance_total, dim3(n_seq), dim3(kBalThreads), 0, stream, (const float2 *)parts, s, tokens, counts, E,
                        balance, zloss);
   return launch_status();

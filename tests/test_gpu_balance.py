@@ -10,7 +10,11 @@ pytestmark = pytest.mark.gpu
 # tokens, experts, K, bounds of the sequences (None: one)
 CASES = [(1, 1, 1, None), (1, 64, 6, None), (5, 7, 3, [0, 5]), (33, 64, 6, [0, 0, 33]), (40, 65, 8, [3, 10, 10, 11, 38]),
          (130, 256, 8, None), (131, 257, 8, [0, 16, 32, 131]), (70, 384, 8, [1, 2, 3, 4, 70]), (50, 1000, 16, [0, 49, 50]),
-         (20, 1024, 16, None), (0, 64, 2, [0, 0, 0]), (300, 128, 2, list(range(0, 301, 3)))]
+         (20, 1024, 16, None), (0, 64, 2, [0, 0, 0]), (300, 128, 2, list(range(0, 301, 3))),
+         # the borders of the calls that one workgroup does by itself
+         (192, 9, 3, None), (193, 9, 3, None), (48, 600, 4, [0, 7, 48]), (49, 600, 4, [0, 7, 49]),
+         (90, 20, 2, sorted(i % 91 for i in range(0, 91 * 7, 7))[:64] + [90]),
+         (90, 20, 2, sorted(i % 91 for i in range(0, 91 * 7, 7))[:65] + [90])]
 
 
 @pytest.fixture(scope="module")
@@ -103,6 +107,43 @@ def test_losses_of_many_tokens(m, score):
     cu = [5, 9000, 9000, 9016, 20000]
     counts = counts_of(m, idx, E, cu)
     check_losses(x, counts, cu, score, *losses(m, x, counts, cu, score))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,cu", [(150001, 12, [0, 70000, 70001, 150000]), (20011, 1000, [3, 20011]), (40003, 300, None),
+                                    (150000, 64, list(range(0, 150001, 1000)))])
+def test_chunks_of_many_tokens(m, T, E, cu, score):
+    """Tokens enough for several of them a group of lanes: chunks inside a sequence and over its borders, against torch in
+    float64."""
+    x, idx = inputs(T, T, E, 2, F32)
+    counts = counts_of(m, idx, E, cu)
+    n, at = counts.shape[0], torch.from_numpy(bounds(cu, T)).cuda()
+    b, z = losses(m, x, counts, cu, score)
+    g = torch.Generator().manual_seed(1)
+    db, dz = torch.rand(n, generator=g).cuda(), torch.rand(n, generator=g).cuda()
+    got = gradient(m, x, counts, cu, db, dz, score).double()
+
+    which = torch.searchsorted(at[1:], torch.arange(T, device="cuda"), right=True)
+    inside = (torch.arange(T, device="cuda") >= at[0]) & (which < n)
+    which = which.clamp(max=n - 1)
+    xd, lens = x.double(), at.diff().clamp(min=1)
+    logs = xd if score == "softmax" else torch.nn.functional.logsigmoid(xd)
+    p, soft, lse = torch.softmax(logs, 1), torch.softmax(xd, 1), torch.logsumexp(xd, 1)
+    c = counts.double()
+    f = (E * c / c.sum(1, keepdim=True).clamp(min=1))[which]
+    d = (f * p).sum(1)
+    sums = torch.zeros(n, 2, dtype=torch.float64, device="cuda").index_add(0, which[inside], torch.stack([d, lse ** 2], 1)[inside])
+    rel = balance_bound(exactly(x), E) + 80 * U
+    wb, wz = (sums / lens[:, None]).unbind(1)
+    assert ((b - wb).abs() <= rel * wb).all() and ((z - wz).abs() <= 3 * rel * (wz + wz.sqrt() + 1)).all()
+    k = (1.0 / lens)[which][:, None]
+    want = p * (f - d[:, None])
+    if score == "sigmoid":
+        want = want * torch.sigmoid(-xd)
+    want = k * (db[which][:, None] * want + 2 * dz[which][:, None] * lse[:, None] * soft)
+    e = k * (db[which][:, None] * p * 2 * rel * (f + d[:, None]) + 2 * dz[which][:, None] * soft * (
+        2 * rel * (lse.abs()[:, None] + 1) + 4 * U * xd.abs().amax(1, keepdim=True))) + 2 * U * want.abs() + 1e-38
+    assert ((got - want).abs() <= e)[inside].all() and (got[~inside] == 7.0).all()
 
 
 def gradient(m, x, counts, cu, db, dz, score, add=None, out=None):

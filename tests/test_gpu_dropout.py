@@ -111,6 +111,23 @@ def test_over_32_bits(m):
     assert np.array_equal(exactly(x[:64]) != 0, ref.kept(64, 0.5, 6, 7))
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_more_than_the_caches_hold(m, dtype, residual):
+    """A call that streams past the caches begins and ends as calls on those parts alone do."""
+    n = (320 << 20) // (2 if dtype == BF16 else 4) + 5
+    x, rng = torch.randn(n, device="cuda").to(dtype), rng_of(12, 13)
+    res = torch.randn(n, device="cuda").to(dtype) if residual else None
+    out, few = torch.empty_like(x), torch.empty(100003, dtype=dtype, device="cuda")
+    m.moe_dropout(x, out, 0.2, rng, residual=res)
+    m.moe_dropout(x[:100003], few, 0.2, rng, residual=res[:100003] if residual else None)
+    assert torch.equal(out[:100003], few)
+    xs = np.where(ref.kept(77, 0.2, 12, 13, first=n - 77), exactly(x[-77:]) * 65536 / (65536 - ref.below(0.2)), 0.0)
+    want = xs + (exactly(res[-77:]) if residual else 0.0)
+    e = 2 * U * np.abs(xs) + U * np.abs(want)
+    assert (np.abs(exactly(out[-77:]) - want) <= e + rounding(dtype) * (np.abs(want) + e)).all()
+
+
 def test_captured_and_replayed(m):
     x, out, want = torch.ones(5000, device="cuda"), torch.empty(5000, device="cuda"), torch.empty(5000, device="cuda")
     rng = rng_of(2, 0)

@@ -10,7 +10,8 @@ pytestmark = pytest.mark.gpu
 EPS = 1e-5
 # rows, width: one value, part of a run of 8, the borders of every width that the kernels tell apart
 SHAPES = [(1, 1), (3, 5), (2, 8), (7, 33), (5, 512), (3, 513), (2, 1001), (4, 1024), (3, 1032), (2, 2048), (2, 2049), (1, 4096),
-          (3, 4100), (2, 7168), (1, 8192), (2, 8193), (1, 16384), (2, 16391), (1, 40000), (300, 64), (1100, 40)]
+          (3, 4100), (2, 7168), (1, 8192), (2, 8193), (1, 16384), (2, 16391), (1, 40000), (300, 64), (1100, 40),
+          (5, 200), (9, 256), (3, 129), (8200, 24)]
 
 
 @pytest.fixture(scope="module")
@@ -138,6 +139,28 @@ def test_gradient_against_differences(m, kind):
         assert abs(got - want) <= step ** 2 / 6 * 60 * size + 4 * 2.0 ** -22 * size / step
 
 
+def test_sixteen_bit_weights_on_fp32_rows(m):
+    c = Rows(11, 30, 1408, F32, "layer", True, w_dtype=BF16)
+    check_forward(c, forward(m, c), 0.0, 0, 0)
+    f = forward(m, c)
+    dy = torch.randn_like(c.x)
+    t = gradients(m, c, f["total"], f["mean"], f["rstd"], dy, None, 0.0, None)
+    h, mean, rstd = exactly(f["total"]), exactly(f["mean"]), exactly(f["rstd"])
+    dh, dw, db = ref.layer_norm_backward(h, exactly(c.w), mean, rstd, exactly(dy), "layer")
+    bh, bw, bb = norm_backward_bound(h, exactly(c.w), mean, rstd, exactly(dy), None, dh, "layer", F32)
+    assert (np.abs(exactly(t["dx"]) - dh) <= bh).all() and (np.abs(exactly(t["dweight"]) - dw) <= bw + U * np.abs(dw)).all()
+
+
+@pytest.mark.parametrize("width", [40, 2048, 1001, 20000])
+def test_total_of_rows_alone_is_their_copy(m, width):
+    """Without residual and dropout h is x, bit for bit (the sign of a zero too)."""
+    x = torch.randn(3, width, device="cuda").bfloat16()
+    x[0, ::3] = -0.0
+    y, total = torch.empty_like(x), torch.empty_like(x)
+    m.moe_layer_norm(x, torch.ones(width, device="cuda"), y, kind="rms", total=total)
+    assert torch.equal(total.view(torch.int16), x.view(torch.int16))
+
+
 def test_one_token_matches_many(m):
     """A row's result is its own: alone or among others, bit for bit where the kernel is the same, else within the bound."""
     c = Rows(8, 40, 7168, BF16, "layer", True)
@@ -263,6 +286,39 @@ def test_rows_over_32_bits(m):
     m.moe_layer_norm_backward(x[-4:].clone(), w, rstd[-4:].clone(), y[-4:].clone(), tail, kind="rms")
     # dx of y itself is 0 but for roundings: g - xh mean(g xh), both of size up to |xh|
     assert ((dx[-4:].float() - tail.float()).abs() <= 2.0 ** -7 * tail.float().abs() + 300 * U * 6).all()
+
+
+@pytest.mark.parametrize("width,dtype", [(7168, BF16), (5121, F32), (12000, BF16)])
+def test_more_than_the_caches_hold(m, width, dtype):
+    """Calls that stream past the caches: their first rows are bit for bit those of a call on them alone, the sums over
+    all rows those of float64."""
+    rows = (300 << 20) // (width * (2 if dtype == BF16 else 4))
+    c = Rows(7, 8, width, dtype, "layer", True)
+    c.x = torch.randn(rows, width, device="cuda").to(dtype)
+    c.residual = (torch.randn(rows, width, device="cuda") + 0.2).to(dtype)
+    rng = rng_of(21, 22)
+    t = forward(m, c, 0.1, rng)
+    dy, dt = (torch.randn(rows, width, device="cuda").to(dtype) for _ in range(2))
+    g = gradients(m, c, t["total"], t["mean"], t["rstd"], dy, dt, 0.1, rng)
+    few = Rows(7, 8, width, dtype, "layer", True)
+    few.x, few.residual = c.x[:70].clone(), c.residual[:70].clone()
+    f = forward(m, few, 0.1, rng)
+    h = gradients(m, few, f["total"], f["mean"], f["rstd"], dy[:70].clone(), dt[:70].clone(), 0.1, rng)
+    for k in ("y", "total", "mean", "rstd"):
+        assert torch.equal(t[k][:70], f[k]), k
+    for k in ("dx", "dresidual"):
+        assert torch.equal(g[k][:70], h[k]), k
+    dw, db, mw, mb = (torch.zeros(width, dtype=torch.float64, device="cuda") for _ in range(4))
+    for lo in range(0, rows, 4096):
+        r = slice(lo, lo + 4096)
+        xh = (t["total"][r].double() - t["mean"][r].double()[:, None]) * t["rstd"][r].double()[:, None]
+        d = dy[r].double()
+        dw += (d * xh).sum(0)
+        db += d.sum(0)
+        mw += (d * xh).abs().sum(0)
+        mb += d.abs().sum(0)
+    sums = (64 + rows // 64 + 8) * U
+    assert ((g["dweight"] - dw).abs() <= sums * mw).all() and ((g["dbias"] - db).abs() <= sums * mb).all()
 
 
 def test_refused(m):
