@@ -265,9 +265,10 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
   const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
-  // Sums of the columns: with two runs a thread in LDS (each thread its own), since the registers of 1024 threads do
-  // not hold them (spilled, 4096 x 16384 bf16 took 212 us).
-  constexpr bool LDS = CHUNKS > 1;
+  // With two runs a thread the registers of 1024 threads do not hold it all (spilled, 4096 x 16384 bf16 took 212 us).  The
+  // sums of the columns go to LDS then (each thread its own), dtotal is fetched when its row is begun, and the weights of
+  // fp32 rows are read again for each row (4 x 2^25 values in 12288 columns 125 us, 128 kept; bf16 67, 60 kept).
+  constexpr bool LDS = CHUNKS > 1, KEEP = !LDS || BF16;
   __shared__ f32x4 held[LDS ? CHUNKS * 4 : 1][LDS ? kNormMaxThreads : 1];
   float w[CHUNKS][8], dw[LDS ? 1 : CHUNKS][8], db[LDS ? 1 : CHUNKS][8];
   Raw<BF16> t[CHUNKS], d[CHUNKS], q[CHUNKS];
@@ -279,7 +280,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
       const Run u(me.t, me.count, i, W);
       t[i].template load<STREAM>(row_at(a.total, bytes), u.at);
       d[i].template load<STREAM>(row_at(a.dy, bytes), u.at);
-      if (a.dtotal) q[i].template load<STREAM>(row_at(a.dtotal, bytes), u.at);
+      if (!LDS && a.dtotal) q[i].template load<STREAM>(row_at(a.dtotal, bytes), u.at);
     }
     if (!RMS) mean = a.mean[row];
     rstd = a.rstd[row];
@@ -287,7 +288,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
   if (me.row < a.rows) fetch(me.row);
 #pragma unroll
   for (int i = 0; i < CHUNKS; ++i) {
-    load_w(a.weight, a.w_bf16, Run(me.t, me.count, i, W).at, 8, w[i]);
+    if (KEEP) load_w(a.weight, a.w_bf16, Run(me.t, me.count, i, W).at, 8, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[LDS ? 0 : i][j] = db[LDS ? 0 : i][j] = 0.0f;
     if (LDS)
@@ -298,10 +299,15 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
   for (long long row = me.row; row < a.rows; row += me.step) {
     const long long base = row * W;
     const float rs = rstd;
+    if (LDS && a.dtotal)
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i)
+        q[i].template load<STREAM>(row_at(a.dtotal, bytes_of<BF16>(base)), Run(me.t, me.count, i, W).at);
     float xh[CHUNKS][8], g[CHUNKS][8], sg = 0.0f, sgx = 0.0f;
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
       const Run u(me.t, me.count, i, W);
+      if (!KEEP) load_w(a.weight, a.w_bf16, u.at, 8, w[i]);
       float v[8];
       t[i].values(xh[i]);
       d[i].values(v);
@@ -324,9 +330,9 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
         }
       if (!RMS) sg += run_sum(u, [&](int j) { return g[i][j]; });
       sgx += run_sum(u, [&](int j) { return g[i][j] * xh[i][j]; });
-      if (a.dtotal) q[i].values(v);
+      if (!LDS && a.dtotal) q[i].values(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[i][j] = fmaf(rs, g[i][j], a.dtotal ? v[j] : 0.0f);
+      for (int j = 0; j < 8; ++j) g[i][j] = fmaf(rs, g[i][j], !LDS && a.dtotal ? v[j] : 0.0f);
     }
     if (row + me.step < a.rows) fetch(row + me.step);
     if (!RMS) sg = me.sum(sg) * rw * rs;
@@ -340,6 +346,12 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
       for (int j = 0; j < 8; ++j) {
         g[i][j] = fmaf(-xh[i][j], sgx, g[i][j]);
         if (!RMS) g[i][j] -= sg;
+      }
+      if (LDS && a.dtotal) {
+        float v[8];
+        q[i].values(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[i][j] += v[j];
       }
       if (a.dresidual) Raw<BF16>(g[i]).template store<STREAM>(row_at(a.dresidual, bytes_of<BF16>(base)), u.at);
       if (DROP) drop_8(drop_bits((unsigned long long)(base + u.at), key), a.drop, g[i]);
