@@ -30,14 +30,14 @@ struct RowThreads {
   long long row, step;
   float (*part)[kNormMaxWaves];
   int slot = 0;
-  __device__ inline RowThreads(float (*p)[kNormMaxWaves]) : part(p) {
+  __device__ inline RowThreads(float (*p)[kNormMaxWaves], int groups) : part(p) {
     if constexpr (LANES > 0) {
       constexpr int ROWS = kNormLanesThreads / LANES;
       t = threadIdx.x % LANES, count = LANES;
-      row = (long long)blockIdx.x * ROWS + threadIdx.x / LANES, step = (long long)gridDim.x * ROWS;
+      row = (long long)blockIdx.x * ROWS + threadIdx.x / LANES, step = (long long)groups * ROWS;
     } else {
       t = threadIdx.x, count = blockDim.x;
-      row = blockIdx.x, step = gridDim.x;
+      row = blockIdx.x, step = groups;
     }
   }
   __device__ inline float sum(float v) {
@@ -103,7 +103,7 @@ struct NormArgs {
 template <bool BF16, bool RMS, bool DROP, bool STREAM, int LANES, int CHUNKS>
 __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k_norm(NormArgs a) {
   __shared__ float part[2][kNormMaxWaves];
-  RowThreads<LANES> me(part);
+  RowThreads<LANES> me(part, gridDim.x);
   const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
 template <bool BF16, bool RMS, bool DROP>
 __global__ __launch_bounds__(kNormMaxThreads) void k_norm_any(NormArgs a) {
   __shared__ float part[2][kNormMaxWaves];
-  RowThreads<0> me(part);
+  RowThreads<0> me(part, gridDim.x);
   const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
@@ -248,20 +248,69 @@ struct NormBwdArgs {
   const void *total, *weight, *dy, *dtotal;
   const float *mean, *rstd;
   void *dx, *dresidual;
-  float *parts;  // [gridDim.x][2][width]: sums of dy xh and of dy; NULL: not wanted
+  float *parts;  // [groups][2][width]: sums of dy xh and of dy; NULL: not wanted, or written by column groups
+  float *dweight, *dbias;  // what column groups write
   long long rows;
-  int width;
-  bool w_bf16;
+  int width, groups;  // groups: workgroups that walk the rows; those behind them take kGroupColumns columns each
+  bool w_bf16, accumulate;
   Drop drop;
 };
+
+template <bool BF16>
+__device__ inline float value_at(const void *p, long long i) {
+  return BF16 ? __builtin_bit_cast(float, (uint32_t)((const uint16_t *)p)[i] << 16) : ((const float *)p)[i];
+}
+
+// dweight and dbias of kGroupColumns columns, of all rows: what a workgroup behind the rows' own does in a short call, beside
+// them, instead of a second launch behind them.  The rows are read once more, out of the caches.  A wave takes 16
+// columns of 4 rows.
+constexpr int kGroupColumns = 16;
+template <bool BF16, bool RMS>
+__device__ inline void column_sums(const NormBwdArgs &a) {
+  __shared__ float part[2][kNormMaxWaves][kGroupColumns];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = blockDim.x >> 6, W = a.width;
+  const int c = ((int)blockIdx.x - a.groups) * kGroupColumns + (lane & 15), at = min(c, W - 1);
+  constexpr int FLIGHT = 8;
+  float dw = 0.0f, db = 0.0f;
+  for (long long r0 = 4 * w + (lane >> 4); r0 < a.rows; r0 += 4LL * waves * FLIGHT) {
+    float h[FLIGHT], d[FLIGHT], m[FLIGHT], s[FLIGHT];
+#pragma unroll
+    for (int k = 0; k < FLIGHT; ++k) {
+      const long long r = min(r0 + 4LL * waves * k, a.rows - 1);
+      h[k] = value_at<BF16>(a.total, r * W + at);
+      d[k] = value_at<BF16>(a.dy, r * W + at);
+      m[k] = RMS ? 0.0f : a.mean[r];
+      s[k] = a.rstd[r];
+    }
+#pragma unroll
+    for (int k = 0; k < FLIGHT; ++k) {
+      if (r0 + 4LL * waves * k >= a.rows) break;
+      dw = fmaf(d[k], (h[k] - m[k]) * s[k], dw);
+      db += d[k];
+    }
+  }
+#pragma unroll
+  for (int off = 16; off < kWave; off <<= 1) dw += __shfl_xor(dw, off, kWave), db += __shfl_xor(db, off, kWave);
+  if (lane < 16) part[0][w][lane] = dw, part[1][w][lane] = db;
+  __syncthreads();
+  if (threadIdx.x >= 16 || c >= W) return;
+  dw = db = 0.0f;
+  for (int i = 0; i < waves; ++i) dw += part[0][i][lane], db += part[1][i][lane];
+  if (a.dweight) a.dweight[c] = a.accumulate ? a.dweight[c] + dw : dw;
+  if (a.dbias) a.dbias[c] = a.accumulate ? a.dbias[c] + db : db;
+}
 
 // The gradient of rows as k_norm has them.  Each workgroup adds up its rows' dy xh and dy column by column, in registers,
 // and k_norm_parts adds the workgroups' sums; the sum's gradient is fetched with the row (fetched when the row is
 // begun, 16384 x 4096 took 116 us against 98 on one workgroup per CU).
 template <bool BF16, bool RMS, bool DROP, bool STREAM, int LANES, int CHUNKS>
 __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k_norm_bwd(NormBwdArgs a) {
+  if ((int)blockIdx.x >= a.groups) {
+    column_sums<BF16, RMS>(a);
+    return;
+  }
   __shared__ float part[2][kNormMaxWaves];
-  RowThreads<LANES> me(part);
+  RowThreads<LANES> me(part, a.groups);
   const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
@@ -402,7 +451,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
 template <bool BF16, bool RMS, bool DROP>
 __global__ __launch_bounds__(kNormMaxThreads) void k_norm_bwd_any(NormBwdArgs a) {
   __shared__ float part[2][kNormMaxWaves];
-  RowThreads<0> me(part);
+  RowThreads<0> me(part, gridDim.x);
   const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
@@ -450,14 +499,7 @@ __global__ __launch_bounds__(kColThreads) void k_norm_cols(NormBwdArgs a) {
   if (c >= W) return;
   float dw = 0.0f, db = 0.0f;
   for (long long row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    float h, d;
-    if constexpr (BF16) {
-      h = __builtin_bit_cast(float, (uint32_t)((const uint16_t *)a.total)[row * W + c] << 16);
-      d = __builtin_bit_cast(float, (uint32_t)((const uint16_t *)a.dy)[row * W + c] << 16);
-    } else {
-      h = ((const float *)a.total)[row * W + c];
-      d = ((const float *)a.dy)[row * W + c];
-    }
+    const float h = value_at<BF16>(a.total, row * W + c), d = value_at<BF16>(a.dy, row * W + c);
     dw += d * ((h - (RMS ? 0.0f : a.mean[row])) * a.rstd[row]);
     db += d;
   }
@@ -536,6 +578,11 @@ static int per_cu(int64_t under_way, int64_t wanted) {
   return (int)(n > 8 ? 8 : n);
 }
 constexpr int64_t kNormUnderWay = 16 << 10, kNormBwdUnderWay = 20 << 10;
+
+// A backward call of so many values, and of so many rows for each wave of a workgroup, has its columns summed by workgroups
+// beside the rows' own.
+constexpr int64_t kBesideValues = 1 << 20;
+constexpr int kBesideRows = 128;
 
 static int norm_parts(int64_t rows, int64_t width, int64_t bytes) {
   int64_t groups = rows, most = kColParts;
@@ -639,9 +686,11 @@ extern "C" moe_status_t moe_layer_norm_backward(moe_dtype dtype, moe_norm_kind k
   if (sums && (!stands_alone(dweight, d_bytes, in, 8) || !stands_alone(dbias, d_bytes, in, 9) ||
                !stands_alone(ws, need, in, 7)))
     return MOE_EINVAL;
-  NormBwdArgs a{total, weight, dy, dtotal, mean, rstd, dx, dresidual, sums ? (float *)ws : nullptr, rows, (int)width,
-                w_dtype == MOE_BF16, make_drop(p, rng, offset)};
   const int parts = norm_parts(rows, width, (int64_t)size * (dtotal ? 3 : 2));
+  NormBwdArgs a{total, weight, dy, dtotal, mean, rstd, dx, dresidual, sums ? (float *)ws : nullptr, dweight, dbias, rows,
+                (int)width, parts, w_dtype == MOE_BF16, accumulate != 0, make_drop(p, rng, offset)};
+  // dy is read beside the rows' work only where that does not write over it
+  bool beside = sums && rows && row_kept(width) && rows * width <= kBesideValues && dx != dy && dresidual != dy;
   auto go = [&](auto bf16, auto rms, auto drop) {
     if (!row_kept(width)) {
       if (sums)  // before dx, which may take dy's place
@@ -652,14 +701,16 @@ extern "C" moe_status_t moe_layer_norm_backward(moe_dtype dtype, moe_norm_kind k
       return;
     }
     with_row((int)width, (int64_t)bytes * (3 + (dtotal ? 1 : 0) + (dresidual ? 1 : 0)), [&](auto st, auto l, auto c, int threads, int) {
-      hipLaunchKernelGGL((k_norm_bwd<bf16.value, rms.value, drop.value, st.value, l.value, c.value>), dim3(parts), dim3(threads), 0,
-                         stream, a);
+      beside = beside && c.value == 1 && rows <= kBesideRows * (threads / kWave);
+      if (beside) a.parts = nullptr;
+      hipLaunchKernelGGL((k_norm_bwd<bf16.value, rms.value, drop.value, st.value, l.value, c.value>),
+                         dim3(parts + (beside ? ceil_div(width, kGroupColumns) : 0)), dim3(threads), 0, stream, a);
     });
   };
   auto pick = [&](auto bf16, auto rms) { a.drop.below ? go(bf16, rms, std::true_type{}) : go(bf16, rms, std::false_type{}); };
   auto kinds = [&](auto bf16) { kind == MOE_NORM_RMS ? pick(bf16, std::true_type{}) : pick(bf16, std::false_type{}); };
   if (rows) dtype == MOE_BF16 ? kinds(std::true_type{}) : kinds(std::false_type{});
-  if (sums)
+  if (sums && !beside)
     hipLaunchKernelGGL(k_norm_parts, dim3(ceil_div(width, kWave), 2), dim3(kPartsThreads), 0, stream,
                        (const float *)ws, parts, (int)width, dweight, dbias, accumulate);
   return launch_status();
