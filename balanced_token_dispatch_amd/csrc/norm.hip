@@ -508,37 +508,37 @@ __global__ __launch_bounds__(kColThreads) void k_norm_cols(NormBwdArgs a) {
   p[W + c] = db;
 }
 
-// dweight and dbias from n parts: 64 columns of one of them a workgroup, its waves over the parts.
-constexpr int kPartsThreads = 1024;
+// dweight and dbias from n parts: kPartsColumns columns of one of them a workgroup, its threads over the parts.
+constexpr int kPartsThreads = 1024, kPartsColumns = 32;
 __global__ __launch_bounds__(kPartsThreads) void k_norm_parts(const float *__restrict__ parts, int n, int W,
                                                              float *dweight, float *dbias, int accumulate) {
-  constexpr int WAVES = kPartsThreads / kWave;
-  __shared__ float s[WAVES][kWave];
+  constexpr int LINES = kPartsThreads / kPartsColumns;
+  __shared__ float s[LINES][kPartsColumns];
   float *out = blockIdx.y ? dbias : dweight;
   if (!out) return;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = blockIdx.x * kWave + lane;
+  const int t = threadIdx.x % kPartsColumns, w = threadIdx.x / kPartsColumns, c = blockIdx.x * kPartsColumns + t;
   float v = 0.0f;
   if (c < W) {
-    // all loads of a lane under way together: the parts come from other caches
+    // the loads of a thread under way together: the parts come from other caches
     const float *p = parts + (long long)blockIdx.y * W + c;
-    constexpr int FLIGHT = 32;
-    for (int i0 = w; i0 < n; i0 += WAVES * FLIGHT) {
+    constexpr int FLIGHT = 16;
+    for (int i0 = w; i0 < n; i0 += LINES * FLIGHT) {
       float t[FLIGHT];
 #pragma unroll
       for (int k = 0; k < FLIGHT; ++k) {
-        const int i = i0 + WAVES * k;
+        const int i = i0 + LINES * k;
         t[k] = i < n ? p[(long long)i * 2 * W] : 0.0f;
       }
 #pragma unroll
       for (int k = 0; k < FLIGHT; ++k) v += t[k];
     }
   }
-  s[w][lane] = v;
+  s[w][t] = v;
   __syncthreads();
   if (w || c >= W) return;
   v = 0.0f;
 #pragma unroll
-  for (int i = 0; i < WAVES; ++i) v += s[i][lane];
+  for (int i = 0; i < LINES; ++i) v += s[i][t];
   out[c] = accumulate ? out[c] + v : v;
 }
 
@@ -580,8 +580,9 @@ static int per_cu(int64_t under_way, int64_t wanted) {
 constexpr int64_t kNormUnderWay = 16 << 10, kNormBwdUnderWay = 20 << 10;
 
 // A backward call of so many values, and of so many rows for each wave of a workgroup, has its columns summed by workgroups
-// beside the rows' own.
-constexpr int64_t kBesideValues = 1 << 20;
+// beside the rows' own (us, so / in two launches: 292 x 7168 bf16 11.0 / 16.4, 585 x 7168 19.1 / 16.2, 512 x 4096 9.6 / 13.6,
+// 1024 x 4096 17.9 / 16.3; 512 x 64 fp32, 128 rows a wave, 7.7 / 8.8).
+constexpr int64_t kBesideValues = 1 << 21;
 constexpr int kBesideRows = 128;
 
 static int norm_parts(int64_t rows, int64_t width, int64_t bytes) {
@@ -711,7 +712,7 @@ extern "C" moe_status_t moe_layer_norm_backward(moe_dtype dtype, moe_norm_kind k
   auto kinds = [&](auto bf16) { kind == MOE_NORM_RMS ? pick(bf16, std::true_type{}) : pick(bf16, std::false_type{}); };
   if (rows) dtype == MOE_BF16 ? kinds(std::true_type{}) : kinds(std::false_type{});
   if (sums && !beside)
-    hipLaunchKernelGGL(k_norm_parts, dim3(ceil_div(width, kWave), 2), dim3(kPartsThreads), 0, stream,
+    hipLaunchKernelGGL(k_norm_parts, dim3(ceil_div(width, kPartsColumns), 2), dim3(kPartsThreads), 0, stream,
                        (const float *)ws, parts, (int)width, dweight, dbias, accumulate);
   return launch_status();
 }
