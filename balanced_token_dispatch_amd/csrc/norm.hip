@@ -30,14 +30,16 @@ struct RowThreads {
   long long row, step;
   float (*part)[kNormMaxWaves];
   int slot = 0;
-  __device__ inline RowThreads(float (*p)[kNormMaxWaves], int groups) : part(p) {
+  // groups: workgroups that walk the rows (0: the grid's)
+  __device__ inline RowThreads(float (*p)[kNormMaxWaves], int groups = 0) : part(p) {
+    const unsigned all = groups ? groups : gridDim.x;
     if constexpr (LANES > 0) {
       constexpr int ROWS = kNormLanesThreads / LANES;
       t = threadIdx.x % LANES, count = LANES;
-      row = (long long)blockIdx.x * ROWS + threadIdx.x / LANES, step = (long long)groups * ROWS;
+      row = (long long)blockIdx.x * ROWS + threadIdx.x / LANES, step = (long long)all * ROWS;
     } else {
       t = threadIdx.x, count = blockDim.x;
-      row = blockIdx.x, step = groups;
+      row = blockIdx.x, step = all;
     }
   }
   __device__ inline float sum(float v) {
@@ -103,7 +105,7 @@ struct NormArgs {
 template <bool BF16, bool RMS, bool DROP, bool STREAM, int LANES, int CHUNKS>
 __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k_norm(NormArgs a) {
   __shared__ float part[2][kNormMaxWaves];
-  RowThreads<LANES> me(part, gridDim.x);
+  RowThreads<LANES> me(part);
   const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
@@ -193,7 +195,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
 template <bool BF16, bool RMS, bool DROP>
 __global__ __launch_bounds__(kNormMaxThreads) void k_norm_any(NormArgs a) {
   __shared__ float part[2][kNormMaxWaves];
-  RowThreads<0> me(part, gridDim.x);
+  RowThreads<0> me(part);
   const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
@@ -451,7 +453,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
 template <bool BF16, bool RMS, bool DROP>
 __global__ __launch_bounds__(kNormMaxThreads) void k_norm_bwd_any(NormBwdArgs a) {
   __shared__ float part[2][kNormMaxWaves];
-  RowThreads<0> me(part, gridDim.x);
+  RowThreads<0> me(part);
   const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
