@@ -284,6 +284,10 @@ class LayerStep:
             if t is not None and tuple(t.shape) != (self.s.S, self.s.H):
                 raise MoeError(f"{name} of shape {tuple(t.shape)}, expected (S, H) = ({self.s.S}, {self.s.H})")
 
+    def _check_backward(self):
+        if not self.backward_enabled:
+            raise ValueError("the layer was made without a backward")
+
     def enter(self, x, weight, bias=None, residual=None, eps=1e-5, p=0.0, rng=None, offset=0):
         """total = residual + dropout(x) (kept for leave()), normalised into this rank's token rows."""
         self._check_rows(x=x, residual=residual)
@@ -299,6 +303,7 @@ class LayerStep:
         """This rank's rows of the layer's output gradient (dout_all) from the gradient behind leave(), with its p, rng and
         offset; dout itself is total's (enter_backward's dtotal)."""
         self._check_rows(dout=dout)
+        self._check_backward()
         r, S = self.rank, self.s.S
         moe_dropout(dout, self.dout_all[r * S:(r + 1) * S], p, rng, offset=offset)
 
@@ -307,6 +312,7 @@ class LayerStep:
         """The gradients of enter(), with its weight, p, rng and offset, from the token rows' gradient dy (the layer's dx and
         the gate's together) and total's by other ways (dtotal).  leave() has not written over total since."""
         self._check_rows(dy=dy, dx=dx, dtotal=dtotal, dresidual=dresidual)
+        self._check_backward()
         moe_layer_norm_backward(self.total, weight, self.norm_rstd, dy, dx, dweight, self.norm_ws, dbias=dbias,
                                 mean=self.norm_mean, kind=self.norm, dtotal=dtotal, dresidual=dresidual,
                                 accumulate=accumulate, p=p, rng=rng, offset=offset)

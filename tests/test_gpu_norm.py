@@ -228,6 +228,17 @@ def test_rows_of_one_value_and_of_large_ones(m, width):
     check_forward(c, forward(m, c), 0.0, 0, 0)
 
 
+@pytest.mark.parametrize("width", [100, 1408, 7168, 20000])
+def test_small_rows_without_eps(m, width):
+    """Scaled by an even power of two, rows give the same y bit for bit, down to squares of 2^-120."""
+    x = torch.randn(3, width, device="cuda")
+    w, y, z = torch.ones(width, device="cuda"), torch.empty_like(x), torch.empty_like(x)
+    m.moe_layer_norm(x, w, y, kind="rms", eps=0.0)
+    for e in (-20, -46, -60):
+        m.moe_layer_norm(x * 2.0 ** e, w, z, kind="rms", eps=0.0)
+        assert torch.equal(y, z), e
+
+
 def test_not_finite(m):
     """A NaN or infinity takes its own row, no other; where the dropout takes it away it is gone."""
     c = Rows(1, 4, 1000, F32, "layer", True)

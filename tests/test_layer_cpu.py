@@ -187,7 +187,7 @@ def test_a_block_takes_rows_of_this_layer(layer, monkeypatch):
     for name in ("moe_layer_norm", "moe_layer_norm_backward", "moe_dropout"):
         monkeypatch.setattr(layer, name, lambda *a, **k: seen.append((a, k)))
     x = torch.zeros(4, 32)
-    L = step_of(layer, norm="rms", x_all=torch.zeros(8, 32), out=x.clone(), total=x.clone(), norm_mean=None,
+    L = step_of(layer, norm="rms", backward_enabled=True, x_all=torch.zeros(8, 32), out=x.clone(), total=x.clone(), norm_mean=None,
                 norm_rstd=torch.zeros(4), norm_ws=torch.zeros(8), dout_all=torch.zeros(8, 32))
     w = torch.ones(32)
     calls = (lambda L, t: L.enter(t, w), lambda L, t: L.enter(x, w, residual=t), lambda L, t: L.leave(t),
@@ -199,6 +199,10 @@ def test_a_block_takes_rows_of_this_layer(layer, monkeypatch):
                 call(L, bad)
         with pytest.raises(ValueError, match="without a norm"):
             call(step_of(layer, norm=None), x)
+    forward_only = step_of(layer, norm="rms", backward_enabled=False)
+    for call in calls[3:]:
+        with pytest.raises(ValueError, match="without a backward"):
+            call(forward_only, x)
     assert not seen
     for call in calls:
         call(L, x)
