@@ -47,6 +47,8 @@ scales the expert gradients (and any others given) to a largest global norm.
 In a transformer block (``norm="layer"`` or ``"rms"``): enter() adds the branch before the layer to the
 residual stream, with dropout, and normalises the sum into this rank's token rows; leave() adds the
 layer's output, with dropout; leave_backward() and enter_backward() are their gradients.
+Masks follow from rng, offset and a value's place alone: enter() and leave() have offsets of their own by default, and
+what else shares an rng (layers, ranks with the same seed, steps) needs another offset, or another rng[1], to draw others.
 count_experts(), balance_loss() and balance_loss_backward() are the gate's balance and z losses, for each
 of ``sequences`` packed sequences.
 """
@@ -68,6 +70,10 @@ from . import (GEMM_DGRAD, GEMM_FWD, GEMM_WGRAD, NORMS, MoeError, balance_loss_w
 # S*K*H*H' from which the backward uses its second stream by default (the R32 S4096 K8 H7168
 # H'2048 step has 4.8e11; its DGRADs take ~0.8 ms each)
 kOverlapMinWork = 1e11
+
+# leave()'s offset unless one is given: enter()'s is 0, and the rows of both have the same places.  So far apart that the
+# steps of a run, for which rng[1] moves on a little each, do not meet it either.
+kLeaveOffset = 1 << 32
 
 
 class QuantWeights:
@@ -294,12 +300,13 @@ class LayerStep:
         moe_layer_norm(x, weight, self.tokens, bias=bias, eps=eps, kind=self.norm, residual=residual, total=self.total,
                        mean=self.norm_mean, rstd=self.norm_rstd, p=p, rng=rng, offset=offset)
 
-    def leave(self, out, p=0.0, rng=None, offset=0):
-        """out = total + dropout(the layer's output): the residual stream behind the layer (out may be total)."""
+    def leave(self, out, p=0.0, rng=None, offset=kLeaveOffset):
+        """out = total + dropout(the layer's output): the residual stream behind the layer (out may be total).  With
+        enter()'s rng it needs another offset than enter() had, as the default is, or both drop the same places."""
         self._check_rows(out=out)
         moe_dropout(self.out, out, p, rng, residual=self.total, offset=offset)
 
-    def leave_backward(self, dout, p=0.0, rng=None, offset=0):
+    def leave_backward(self, dout, p=0.0, rng=None, offset=kLeaveOffset):
         """This rank's rows of the layer's output gradient (dout_all) from the gradient behind leave(), with its p, rng and
         offset; dout itself is total's (enter_backward's dtotal)."""
         self._check_rows(dout=dout)

@@ -523,7 +523,7 @@ moe_status_t moe_grad_clip(int32_t n, const void *const *grads, const int64_t *n
  *   rng    2 int64 (seed, offset), device memory, read when the kernel runs, so
  *          that a captured graph draws anew where rng[1] moves between replays.
  *   offset is added to rng[1]: one for each dropout of a step.  Two tensors
- *          with the same seed and sum share their mask.
+ *          with the same seed and sum share their mask, on any rank.
  *   p      in [0, 1]; with p = 0 rng is not read and may be NULL.
  * The pages name no dropout, norm or balance loss; these are the usual parts
  * of a transformer block around the layer.
