@@ -224,9 +224,10 @@ __device__ inline float lanes_max(float m) {
 }
 
 // A token's logits as numerators of its probabilities: p over sp for the balance loss, z over sz (exp(x - m)) for the
-// z loss.  With softmax scores the two are one.  The logistic is 1 / (1 + t) or t / (1 + t) with t = exp(-|x|); where
-// the largest logit is so low that 1 + t is 1, its ratios are the softmax's.
-constexpr float kLowLogit = -60.0f;
+// z loss.  With softmax scores the two are one.  The logistic is 1 / (1 + t) or t / (1 + t) with t = exp(-|x|).  Where all
+// logits are below 0, t is exp(x - m) exp(m) and p is left over exp(m): only a logit's distance from the largest one goes
+// through an exponential that tells the experts apart.  With exp(-|x|) alone the rounded argument cost P up to 1.3e-6 of itself
+// at -40 and 2.6e-6 at -60, and below -87 t is 0; exp(m) is the same for all of them, and its error reaches P only through 1 + t.
 template <int L, int G, bool SIGMOID, bool Z>
 struct TokenRow {
   f32x4 p[G], z[SIGMOID && Z ? G : 1], rest[SIGMOID ? G : 1];  // rest: 1 - logistic
@@ -243,16 +244,16 @@ struct TokenRow {
       for (int j = 0; j < 4; ++j) m = fmaxf(m, x[i][j]);
     m = lanes_max<L>(m);
     sp = sz = 0.0f;
+    const float low = fminf(m, 0.0f), scale = exp_of(low);
 #pragma unroll
     for (int i = 0; i < G; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float v = x[i][j];
         if constexpr (SIGMOID) {
-          const float t = exp_of(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.0f + t), tr = t * r;
-          p[i][j] = v >= 0.0f ? r : tr;
+          const float t = exp_of(-fabsf(v) - low), r = __builtin_amdgcn_rcpf(fmaf(t, scale, 1.0f)), tr = t * r;
+          p[i][j] = v >= 0.0f ? r : tr;  // a v above 0 has scale 1
           rest[i][j] = v >= 0.0f ? tr : r;
-          if (m < kLowLogit) p[i][j] = exp_of(v - m);
           if constexpr (Z) sz += z[i][j] = exp_of(v - m);
         } else {
           p[i][j] = exp_of(v - m);
