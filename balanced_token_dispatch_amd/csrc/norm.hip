@@ -28,7 +28,7 @@ template <int LANES>
 struct RowThreads {
   int t, count;  // this thread's place, threads a row
   long long row, step;
-  float (*part)[kNormMaxWaves];
+  float (*part)[kNormMaxWaves];  // two places, a third where sum_again() is called
   int slot = 0;
   // groups: workgroups that walk the rows (0: the grid's)
   __device__ inline RowThreads(float (*p)[kNormMaxWaves], int groups = 0) : part(p) {
@@ -50,6 +50,20 @@ struct RowThreads {
       if (blockDim.x == kWave) return v;
       // two places in turn: who writes one again has passed the barrier behind the other's reads
       float *p = part[slot ^= 1];
+      if ((threadIdx.x & 63) == 0) p[threadIdx.x >> 6] = v;
+      __syncthreads();
+      const int w = threadIdx.x & 15;
+      return token_sum<16>(w < (int)(blockDim.x >> 6) ? p[w] : 0.0f);
+    }
+  }
+  // One more sum of a row that needs it, at most one between two of sum(), whose barriers keep its place's uses apart.
+  __device__ inline float sum_again(float v) {
+    if constexpr (LANES > 0) {
+      return token_sum<LANES>(v);
+    } else {
+      v = token_sum<kWave>(v);
+      if (blockDim.x == kWave) return v;
+      float *p = part[2];
       if ((threadIdx.x & 63) == 0) p[threadIdx.x >> 6] = v;
       __syncthreads();
       const int w = threadIdx.x & 15;
@@ -84,10 +98,31 @@ __device__ inline float run_sum(const Run &r, F f) {
   return s;
 }
 
+// The same of the squares of v scale.  Fused by hand: left to the compiler, which of the products are rounded before they are
+// added differed from one use to the next, and a row's last bits with it.
+__device__ inline float run_squares(const Run &r, const float (&v)[8], float scale = 1.0f) {
+  float s = 0.0f;
+  if (r.skip == 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(v[j] * scale, v[j] * scale, s);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = j >= r.skip ? fmaf(v[j] * scale, v[j] * scale, s) : s;
+  }
+  return s;
+}
+
 // 1 / sqrt(v), within one step; the instruction takes numbers below 2^-126 for 0.
 __device__ inline float inverse_root(float v) {
   const bool tiny = v < 0x1p-100f;
   return __builtin_amdgcn_rsqf(tiny ? v * 0x1p60f : v) * (tiny ? 0x1p30f : 1.0f);
+}
+
+// Where the sum of a row's squares is more than fp32 holds (values from 2^53 on at the widest row), the squares are summed
+// again of the values scaled by this: below 2^105, which a row's own sum still holds, they fit at any width.
+constexpr float kLargeScale = 0x1p-80f;
+__device__ inline float inverse_root_large(float v, float eps) {
+  return inverse_root(v + eps * kLargeScale * kLargeScale) * kLargeScale;
 }
 
 __device__ inline void load_w(const void *w, bool bf16, long long i, int n, float (&v)[8]) {
@@ -110,7 +145,7 @@ struct NormArgs {
 // 4096 x 7168 took 48 to 52 us against 46 (fewer waves, more registers).
 template <bool BF16, bool RMS, bool DROP, bool STREAM, int LANES, int CHUNKS>
 __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k_norm(NormArgs a) {
-  __shared__ float part[2][kNormMaxWaves];
+  __shared__ float part[3][kNormMaxWaves];
   RowThreads<LANES> me(part);
   const int W = a.width;
   DropKey key{};
@@ -163,7 +198,7 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] += v[j];
       }
-      sum += run_sum(u, [&](int j) { return RMS ? h[i][j] * h[i][j] : h[i][j]; });
+      sum += RMS ? run_squares(u, h[i]) : run_sum(u, [&](int j) { return h[i][j]; });
     }
     const bool more = row + me.step < a.rows;
     if (more) fetch(x, a.x, row + me.step);
@@ -185,11 +220,18 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
       for (int i = 0; i < CHUNKS; ++i) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] -= mean;
-        sq += run_sum(Run(me.t, me.count, i, W), [&](int j) { return h[i][j] * h[i][j]; });
+        sq += run_squares(Run(me.t, me.count, i, W), h[i]);
       }
       var = me.sum(sq) * rw;
     }
-    const float rstd = inverse_root(var + a.eps);
+    float rstd = inverse_root(var + a.eps);
+    if (__builtin_expect(__any(var == __builtin_inff()), 0)) {  // of the waves of a workgroup that share a row: all or none
+      float sq = 0.0f;
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) sq += run_squares(Run(me.t, me.count, i, W), h[i], kLargeScale);
+      sq = me.sum_again(sq) * rw;
+      if (var == __builtin_inff()) rstd = inverse_root_large(sq, a.eps);
+    }
     if (more && late) fetch(r, a.residual, row + me.step);
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
@@ -227,7 +269,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_norm_any(NormArgs a) {
         for (int j = 0; j < 8; ++j) v[j] += r[j];
       }
     };
-    float mean = 0.0f, sum = 0.0f, sq = 0.0f;
+    float mean = 0.0f, sum = 0.0f;
     if (!RMS) {
       for (int at = 8 * me.t; at < W; at += 8 * me.count) {
         float v[8];
@@ -237,13 +279,22 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_norm_any(NormArgs a) {
       }
       mean = me.sum(sum) / W;
     }
-    for (int at = 8 * me.t; at < W; at += 8 * me.count) {
-      float v[8];
-      read(at, W - at, v);
+    float scale = 1.0f, var;
+    for (;; scale = kLargeScale) {
+      float sq = 0.0f;
+      for (int at = 8 * me.t; at < W; at += 8 * me.count) {
+        float v[8];
+        read(at, W - at, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sq += at + j < W ? (v[j] - mean) * (v[j] - mean) : 0.0f;
+        for (int j = 0; j < 8; ++j) {
+          const float d = at + j < W ? (v[j] - mean) * scale : 0.0f;
+          sq = fmaf(d, d, sq);
+        }
+      }
+      var = me.sum(sq) / W;
+      if (var != __builtin_inff() || scale != 1.0f) break;
     }
-    const float rstd = 1.0f / sqrtf(me.sum(sq) / W + a.eps);
+    const float rstd = scale / sqrtf(var + a.eps * scale * scale);
     for (int at = 8 * me.t; at < W; at += 8 * me.count) {
       const int n = W - at;
       float v[8], w[8], b[8] = {};

@@ -548,8 +548,8 @@ moe_status_t moe_dropout(moe_dtype dtype, int64_t n, const void *x, const void *
  *   weight, bias (nullable)  [width] of w_dtype.
  *   mean, rstd  [rows] fp32, nullable (not kept); mean NULL for MOE_NORM_RMS.
  *   rows >= 0, 1 <= width <= 2^22, eps >= 0; all aligned to their element.
- * A row with a NaN or infinity gives NaN; one whose squares do not fit fp32
- * (values from 2^63 on) has rstd 0.
+ * A row h of finite values below 2^105 is normalised as defined, also where its
+ * squares do not fit fp32.  A row with a NaN or infinity gives NaN.
  *
  * moe_layer_norm_backward -- with xh = (total - mean) rstd and g = dy weight:
  *   dh = rstd (g - mean(g) - xh mean(g xh)) + dtotal    (RMS: without mean(g))
