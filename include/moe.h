@@ -549,7 +549,9 @@ moe_status_t moe_dropout(moe_dtype dtype, int64_t n, const void *x, const void *
  *   mean, rstd  [rows] fp32, nullable (not kept); mean NULL for MOE_NORM_RMS.
  *   rows >= 0, 1 <= width <= 2^22, eps >= 0; all aligned to their element.
  * A row h of finite values below 2^105 is normalised as defined, also where its
- * squares do not fit fp32.  A row with a NaN or infinity gives NaN.
+ * squares do not fit fp32.  A NaN makes its row NaN, and so does an infinity
+ * where there is a mean; for MOE_NORM_RMS an infinity makes rstd 0, its column
+ * NaN and the others the bias.
  *
  * moe_layer_norm_backward -- with xh = (total - mean) rstd and g = dy weight:
  *   dh = rstd (g - mean(g) - xh mean(g xh)) + dtotal    (RMS: without mean(g))

@@ -1,8 +1,9 @@
-"""moe_layer_norm and its gradient on rows of very large values."""
+"""moe_layer_norm and its gradient on rows of very large values and of infinities."""
 import pytest
 import torch
 
 from block_common import BF16, F32, rng_of
+from test_gpu_norm import Rows, forward
 
 pytestmark = pytest.mark.gpu
 # one of each kernel and width of row that are told apart
@@ -61,3 +62,30 @@ def test_gradient_of_large_rows(m, width, kind):
         m.moe_layer_norm_backward(t["total"], w, t["rstd"], dy, out, mean=t.get("mean"), kind=kind)
         dx.append(out * scale)
     assert torch.isfinite(dx[0]).all() and torch.equal(dx[0], dx[1]) and torch.equal(dx[0], dx[2])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_rows_that_are_not_finite(m, width, dtype):
+    """A NaN takes its whole row, an infinity too where a mean is taken; without one, 1 / sqrt(infinity) is 0: the infinite
+    column is NaN (infinity times 0), the others the bias.  Other rows are as they were."""
+    inf, nan = float("inf"), float("nan")
+    for kind in ("layer", "rms"):
+        c = Rows(1, 7, width, dtype, kind, False)
+        c.b = torch.linspace(-1, 1, width, device="cuda")
+        base = forward(m, c)
+        others = torch.tensor([0, 1, 3, 4, 6], device="cuda")
+        for v in (nan, inf, -inf):
+            x = c.x.clone()
+            c.x[2, width // 2], c.x[5, width - 1] = v, v
+            t = forward(m, c)
+            c.x = x
+            for k in base:
+                assert torch.equal(t[k][others], base[k][others])
+            for row, at in ((2, width // 2), (5, width - 1)):
+                if kind == "layer" or v != v:
+                    assert torch.isnan(t["y"][row]).all() and torch.isnan(t["rstd"][row])
+                else:
+                    rest = torch.arange(width, device="cuda") != at
+                    assert t["rstd"][row] == 0 and torch.isnan(t["y"][row, at])
+                    assert torch.equal(t["y"][row, rest], c.b.to(dtype)[rest])
