@@ -1,9 +1,12 @@
-"""moe_layer_norm and its gradient on rows of very large values and of infinities."""
+"""moe_layer_norm and its gradient: rows of very large values, infinities, every kernel in place, a row among others, and
+the borders of the short gradients."""
+import numpy as np
 import pytest
 import torch
 
-from block_common import BF16, F32, rng_of
-from test_gpu_norm import Rows, forward
+import test_gpu_norm as norm
+from block_common import BF16, F32, U, exactly, rng_of
+from test_gpu_norm import Rows, forward, gradients
 
 pytestmark = pytest.mark.gpu
 # one of each kernel and width of row that are told apart
@@ -89,3 +92,58 @@ def test_rows_that_are_not_finite(m, width, dtype):
                     rest = torch.arange(width, device="cuda") != at
                     assert t["rstd"][row] == 0 and torch.isnan(t["y"][row, at])
                     assert torch.equal(t["y"][row, rest], c.b.to(dtype)[rest])
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_in_place_in_every_kernel(m, width, dtype, kind):
+    """y and total in the places of x and residual, dx and dresidual in those of dy and dtotal, either way round: as
+    without, bit for bit, also where the moved-back end of a row is two threads'."""
+    rows = 9
+    c = Rows(3, rows, width, dtype, kind, True)
+    rng = rng_of(5, 6)
+    t = forward(m, c, 0.2, rng)
+    for y_in_x in (True, False):
+        x, res = c.x.clone(), c.residual.clone()
+        y, total = (x, res) if y_in_x else (res, x)
+        m.moe_layer_norm(x, c.w, y, bias=c.b, kind=kind, residual=res, total=total, p=0.2, rng=rng)
+        assert torch.equal(y, t["y"]) and torch.equal(total, t["total"])
+    dy, dt = torch.randn_like(c.x), torch.randn_like(c.x)
+    g = gradients(m, c, t["total"], t.get("mean"), t["rstd"], dy, dt, 0.2, rng)
+    ws = torch.empty(m.layer_norm_backward_workspace_bytes(rows, width), dtype=torch.uint8, device="cuda")
+    mean = exactly(t["mean"])[:, None] if kind == "layer" else 0.0
+    xh, d = (exactly(t["total"]) - mean) * exactly(t["rstd"])[:, None], np.abs(exactly(dy))
+    for dx_in, dres_in in (("dy", "dtotal"), ("dtotal", "dy"), ("dy", None), ("dtotal", None), (None, "dtotal"), (None, "dy")):
+        a, b = dy.clone(), dt.clone()
+        place = {"dy": a, "dtotal": b}
+        dx, dres = (torch.empty_like(dy) if k is None else place[k] for k in (dx_in, dres_in))
+        dw, db = torch.empty(width, device="cuda"), torch.empty(width, device="cuda")
+        m.moe_layer_norm_backward(t["total"], c.w, t["rstd"], a, dx, dw, ws, dbias=db, mean=t.get("mean"), kind=kind, dtotal=b,
+                                  dresidual=dres, p=0.2, rng=rng)
+        assert torch.equal(dx, g["dx"]) and torch.equal(dres, g["dresidual"]), (dx_in, dres_in)
+        # the sums of columns may be added up in another order: each is off by at most rows + 8 roundings of the magnitudes
+        assert (np.abs(exactly(dw) - exactly(g["dweight"])) <= 2 * (rows + 8) * U * (d * np.abs(xh)).sum(0)).all()
+        if kind == "layer":
+            assert (np.abs(exactly(db) - exactly(g["dbias"])) <= 2 * (rows + 8) * U * d.sum(0)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_a_row_alone_is_the_row_among_others(m, width, dtype):
+    """Bit for bit: few rows and one go through the same kernel."""
+    c = Rows(8, 40, width, dtype, "layer", True)
+    whole = forward(m, c)
+    one = Rows(8, 40, width, dtype, "layer", True)
+    one.x, one.residual = c.x[17:18].clone(), c.residual[17:18].clone()
+    alone = forward(m, one)
+    for k in whole:
+        assert torch.equal(alone[k], whole[k][17:18]), k
+
+
+@pytest.mark.parametrize("kind,dtot,p,accumulate", [("layer", True, 0.3, True), ("rms", False, 0.0, False)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,width", [(292, 7168), (293, 7168), (512, 4096), (513, 4096)])
+def test_borders_of_the_short_gradients(m, rows, width, dtype, kind, dtot, p, accumulate):
+    """The last rows and widths whose columns are summed beside the rows, and the first that are not (2^21 values)."""
+    norm.test_backward(m, rows, width, dtype, kind, dtot, p, accumulate)
