@@ -232,7 +232,10 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
       sq = me.sum_again(sq) * rw;
       if (var == __builtin_inff()) rstd = inverse_root_large(sq, a.eps);
     }
-    if (more && late) fetch(r, a.residual, row + me.step);
+    if (more && late) {
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): behind x, not beside it (32768 x 7168 327 us beside it, 322 behind)
+      fetch(r, a.residual, row + me.step);
+    }
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
       const Run u(me.t, me.count, i, W);
