@@ -6,12 +6,16 @@
 // added up in chunks of tokens.  A chunk's tokens of one sequence give one partial sum, at place (chunk +
 // sequence): along the tokens one of the two grows with each new partial sum, so no place is taken twice.
 //
-// Latency-bound at usual sizes, by the exponentials at many tokens and by HBM at many experts; in a graph, us:
+// Latency-bound at usual sizes, by the exponentials at many tokens and by HBM at many experts; calls in a graph over three
+// sets of inputs, us:
 //   tokens x experts, sequences      counts (K = 8)   losses   gradient (added to the router's)
-//   64 x 64, 1 (K = 6)                2.0              3.9      3.5
-//   8192 x 384 fp32, 4                3.8              8.9      8.5
-//   32768 x 256 bf16 logistic, 61     8.5              14       17     (25 MB and 50 MB move in 4 and 9)
-//   65536 x 1024 fp32, 16             7.8              47       161    (5.6 and 5.0 TB/s)
+//   64 x 64 fp32, 1 (K = 6)           4.4              4.8      4.3
+//   8192 x 384 fp32, 4                5.3              10.7     11.6
+//   32768 x 256 bf16 logistic, 61     9.1              16.1     17.9   (17 MB and 50 MB move in 3 and 8.5)
+//   32768 x 256 bf16 softmax, 61      9.4              14.1     14.6
+//   65536 x 1024 fp32, 16             8.5              59.5     162    (4.5 and 5.0 TB/s)
+//   65536 x 64 bf16, 128 (K = 6)      11.5             14.1     13.1   (in one sequence 8.9, 11.4, 10.9)
+//   65536 x 64 bf16, 4096 (K = 6)     68               21.8     16.7   (bins cleared and flushed for each piece of a sequence)
 #include <type_traits>
 
 #include "lanes.hpp"

@@ -1,5 +1,5 @@
 // moe_dropout: out = residual + drop(x).  Streams its tensors once: HBM-bound.  8192 x 7168 bf16 with residual (352 MB) take
-// 54 to 58 us, 6.1 to 6.5 TB/s, where torch's copy moves 5.1; without residual 41 us, where the ten rounds for 8 elements
+// 54 to 59 us, 6.0 to 6.5 TB/s, where torch's copy moves 5.1; without residual 41 to 43, where the ten rounds for 8 elements
 // take about half of the arithmetic's time; 6 x 1408 2.5 us.
 #include <type_traits>
 

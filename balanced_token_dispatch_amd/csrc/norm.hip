@@ -5,11 +5,12 @@
 // then the mean of its squared differences are summed: both in fp32, the second from the differences, so
 // that a mean far from 0 costs no digits.  Rows wider than the registers of a workgroup are read again.
 //
-// HBM-bound, with dropout nearly as much by the ten rounds of its counter: bf16 rows of 7168 with residual, kernel
-// times: 32768 rms rows (1.9 GB) 322 us, 5.8 TB/s; 4096 with dropout and statistics (235 MB) 44, 5.3 TB/s; the gradient
-// of 8192 with dropout and the residual's gradient (587 MB) 109 and 5 for the sums of columns, 5.2 TB/s.  One row 3.2 us.
-// The best copy reaches 5.9.  With one row a workgroup and no loads ahead these took 381, 68 and 157 + 12.  Rows above
-// 16384 columns, read two or three times: 2 to 3.7 TB/s of what they would have to move.
+// HBM-bound, with dropout nearly as much by the ten rounds of its counter: bf16 rows of 7168 with residual, median kernel
+// times over three sets of inputs: 32768 rms rows (1.9 GB) 325 us, 5.8 TB/s; 4096 with dropout and statistics (235 MB) 44 to
+// 45, 5.3 TB/s; the gradient of 8192 with dropout and the residual's gradient (587 MB) 108 and 5 for the sums of columns,
+// 5.2 TB/s; a gradient of 2^24 values (2048 rows, 117 MB) 32 with them, 3.6 TB/s.  One row 3.4 us.  The best copy reaches
+// 5.9.  With one row a workgroup and no loads ahead these took 381, 68 and 157 + 12.  Rows above 16384 columns, read two or
+// three times: 2.1 to 3.4 TB/s of what they would have to move.
 #include <type_traits>
 
 #include "dropout.hpp"
@@ -233,7 +234,9 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
       if (var == __builtin_inff()) rstd = inverse_root_large(sq, a.eps);
     }
     if (more && late) {
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): behind x, not beside it (32768 x 7168 327 us beside it, 322 behind)
+      // vmcnt(0): behind the next x, not beside it (rms, us beside / behind: 32768 x 7168 bf16 325 / 320, 8192 x 7168 fp32
+      // 189 / 177, 32768 x 6144 bf16 282 / 287; layer norm the same within 1%)
+      __builtin_amdgcn_s_waitcnt(0x0F70);
       fetch(r, a.residual, row + me.step);
     }
 #pragma unroll
@@ -386,7 +389,9 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
   const int W = a.width;
   DropKey key{};
   if (DROP) key = drop_key(a.drop);
-  // With two runs a thread the registers of 1024 threads do not hold it all (spilled, 4096 x 16384 bf16 took 212 us).  The
+  // With two runs a thread the registers of 1024 threads do not hold it all (spilled, 4096 x 16384 bf16 took 212 us; as it is,
+  // 12 of the 16 variants still keep 8 to 80 bytes a thread in scratch, the most in fp32 with dropout: 2730 x 12288 fp32 171
+  // us with dropout and the residual's gradient, 122 without).  The
   // sums of the columns go to LDS then (each thread its own), dtotal is fetched when its row is begun, and the weights of
   // fp32 rows are read again for each row (4 x 2^25 values in 12288 columns 125 us, 128 kept; bf16 67, 60 kept).
   constexpr bool LDS = CHUNKS > 1, KEEP = !LDS || BF16;
@@ -458,7 +463,8 @@ __global__ __launch_bounds__(LANES ? kNormLanesThreads : kNormMaxThreads) void k
     if (row + me.step < a.rows) fetch(row + me.step);
     if (!RMS) sg = me.sum(sg) * rw * rs;
     sgx = me.sum(sgx) * rw * rs;
-    // from here on every thread has its columns: an output may take their place
+    // an output may take its columns' place from here on: every thread's loads of them stand before the sums, those of dtotal
+    // too where their values are used only below (a wave's memory accesses keep their order, and the sums' barrier the waves')
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
       const Run u(me.t, me.count, i, W);

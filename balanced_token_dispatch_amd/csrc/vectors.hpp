@@ -136,7 +136,8 @@ __device__ inline char *row_at(void *p, long long bytes) { return (char *)p + by
 // little of it in the memory-side cache (256 MB) then, and evictions cost.  A kernel and one that reads its results
 // after it, us with / without: norm of 7168 columns with its sum written, 235 MB 60.8 / 58.8, 470 MB 118 / 123, 940 MB
 // 231 / 248; dropout 84 MB 22.2 / 21.7, 252 MB 57.5 / 58.9, 504 MB 111 / 117.  Alone, the norm of 470 MB takes 79.0 / 81.8,
-// the dropout of 352 MB 55.4 / 62.3.
+// the dropout of 352 MB 55.4 / 62.3.  Norm rows of up to 512 and above 16384 columns and the balance loss do not ask (not
+// measured for them).
 constexpr int64_t kStreamBytes = 256 << 20;
 
 // Whether two ranges share memory.  Ranges that are the same one are told apart by `same`.
